@@ -206,6 +206,53 @@ kla_status_t check_pgdn(int gain, float band, float eps) {
   return KLA_OK;
 }
 
+// Layout of a packed or dense batch of sequences: num_seqs, cu_seqlens and its host mirror
+// against B and T.  *longest: tokens of the longest sequence.
+kla_status_t check_seqs(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B, int T,
+                        int *longest) {
+  *longest = T;
+  if (cu_seqlens == nullptr) {
+    if (cu_seqlens_host != nullptr) return KLA_ERR_NULL;
+    return num_seqs == B ? KLA_OK : KLA_ERR_SHAPE;
+  }
+  if (cu_seqlens_host == nullptr) return KLA_ERR_NULL;
+  if (B != 1) return KLA_ERR_SHAPE;
+  if (cu_seqlens_host[0] != 0 || cu_seqlens_host[num_seqs] != T) return KLA_ERR_SEQLENS;
+  *longest = 0;
+  for (int n = 0; n < num_seqs; ++n) {
+    if (cu_seqlens_host[n + 1] < cu_seqlens_host[n]) return KLA_ERR_SEQLENS;
+    *longest = std::max(*longest, cu_seqlens_host[n + 1] - cu_seqlens_host[n]);
+  }
+  return (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) ? KLA_ERR_ALIGN : KLA_OK;
+}
+
+// Tokens of a sequence dimension: tile arithmetic in ints may run one tile past the end.
+constexpr int kMaxTokens = 0x7fffffff - 65536;
+
+kla_status_t check_glr(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B, int H, int T,
+                       int d, int dtype, kla::GlrArgs *a) {
+  if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
+  if (B < 0 || H <= 0 || T < 0 || T > kMaxTokens || d <= 0 || d > (1 << 24) || num_seqs < 0) return KLA_ERR_SHAPE;
+  if ((long long)B * H > 0x7fffffffLL || (long long)B * H * T > (1LL << 40)) return KLA_ERR_SHAPE;
+  *a = kla::GlrArgs{};
+  const kla_status_t st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, T, &a->longest);
+  if (st != KLA_OK) return st;
+  a->cu_seqlens = cu_seqlens;
+  a->num_seqs = num_seqs;
+  a->H = H;
+  a->T = T;
+  a->d = d;
+  a->dtype = dtype;
+  return kla::glr_grid_fits(*a) ? KLA_OK : KLA_ERR_SHAPE;
+}
+
+kla_status_t run_glr(kla::GlrArgs &a, bool bwd, void *workspace, size_t workspace_bytes, void *stream) {
+  const size_t need = kla::glr_workspace_bytes(a);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KLA_ERR_WORKSPACE;
+  a.workspace = workspace;
+  return from_hip(kla::launch_glr_chunk(a, bwd, reinterpret_cast<hipStream_t>(stream)));
+}
+
 float band_log(float band) { return band == 1.f ? 0.f : std::log(band); }
 
 }  // namespace
@@ -416,6 +463,69 @@ kla_status_t kla_gdn_decode_step(const void *q, const void *k, const void *v, co
                                  kla_dtype_t dtype_, void *stream) {
   const int dtype = raw(dtype_);
   return decode_impl(q, k, v, g, beta, 0.f, 1, state, o, N, H, dk, dv, dtype, stream);
+}
+
+size_t kla_glr_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B,
+                                     int H, int T, int d, kla_dtype_t dtype_) {
+  kla::GlrArgs a;
+  if (check_glr(cu_seqlens, cu_seqlens_host, num_seqs, B, H, T, d, raw(dtype_), &a) != KLA_OK) return 0;
+  return num_seqs == 0 ? 0 : kla::glr_workspace_bytes(a);
+}
+
+kla_status_t kla_glr_chunk_fwd(const void *x, const void *g, const float *initial_state, void *o, float *final_state,
+                               const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B, int H,
+                               int T, int d, kla_dtype_t dtype_, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+  kla::GlrArgs a;
+  const kla_status_t st = check_glr(cu_seqlens, cu_seqlens_host, num_seqs, B, H, T, d, raw(dtype_), &a);
+  if (st != KLA_OK) return st;
+  if (num_seqs == 0) return KLA_OK;
+  if ((long long)B * T > 0 && (!x || !g || !o)) return KLA_ERR_NULL;
+  if (misaligned(x) || misaligned(g) || misaligned(initial_state) || misaligned(o) || misaligned(final_state) ||
+      misaligned(workspace))
+    return KLA_ERR_ALIGN;
+  a.x = x;
+  a.g = g;
+  a.y0 = initial_state;
+  a.o = o;
+  a.yend = final_state;
+  return run_glr(a, false, workspace, workspace_bytes, stream);
+}
+
+kla_status_t kla_glr_chunk_bwd(const void *g, const void *o, const float *initial_state, const void *dout,
+                               const float *dfinal_state, void *dx, void *dg, float *dinitial_state,
+                               const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B, int H,
+                               int T, int d, kla_dtype_t dtype_, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+  kla::GlrArgs a;
+  const kla_status_t st = check_glr(cu_seqlens, cu_seqlens_host, num_seqs, B, H, T, d, raw(dtype_), &a);
+  if (st != KLA_OK) return st;
+  if (num_seqs == 0) return KLA_OK;
+  if ((long long)B * T > 0 && (!g || !o || !dout || !dx || !dg)) return KLA_ERR_NULL;
+  if (misaligned(g) || misaligned(o) || misaligned(initial_state) || misaligned(dout) || misaligned(dfinal_state) ||
+      misaligned(dx) || misaligned(dg) || misaligned(dinitial_state) || misaligned(workspace))
+    return KLA_ERR_ALIGN;
+  a.x = dout;
+  a.g = g;
+  a.h = o;
+  a.y0 = dfinal_state;
+  a.h0 = initial_state;
+  a.o = dx;
+  a.dg = dg;
+  a.yend = dinitial_state;
+  return run_glr(a, true, workspace, workspace_bytes, stream);
+}
+
+kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, void *o, int N, int H, int d,
+                                 kla_dtype_t dtype_, void *stream) {
+  const int dtype = raw(dtype_);
+  if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
+  if (N < 0 || H <= 0 || d <= 0 || (long long)N * H > 0x7fffffffLL) return KLA_ERR_SHAPE;
+  if ((double)N * H * d > (double)(1LL << 38)) return KLA_ERR_SHAPE;  // 256 channels to a workgroup at least
+  if (N == 0) return KLA_OK;
+  if (!x || !g || !state || !o) return KLA_ERR_NULL;
+  if (misaligned(x) || misaligned(g) || misaligned(state) || misaligned(o)) return KLA_ERR_ALIGN;
+  return from_hip(kla::launch_glr_step(x, g, state, o, (size_t)N * H * d, dtype, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -130,6 +130,25 @@ hipError_t launch_seg_table(const SegFixParams &f, int *seg_first, hipStream_t s
 hipError_t launch_seg_finish(const SegFixParams &f, hipStream_t stream);
 bool seg_correct_mfma(int dtype, int dk, int dv);
 
+// The gated linear recurrence (kla_glr.hip).  Forward: x in, o out, y0 / yend the initial
+// and final states.  Backward: x is dL/do, h the forward's output, y0 dL/dh_final, h0 the
+// initial state; o is dx, dg the gate's gradient, yend dL/dh_0.
+struct GlrArgs {
+  const void *x, *g, *h;
+  const float *y0, *h0;
+  void *o, *dg;
+  float *yend;
+  const int32_t *cu_seqlens;  // device, or nullptr
+  int num_seqs, H, T, d, dtype;
+  int longest;                // tokens of the longest sequence
+  void *workspace;            // device, glr_workspace_bytes(*this) bytes
+};
+size_t glr_workspace_bytes(const GlrArgs &a);
+bool glr_grid_fits(const GlrArgs &a);  // the launch's workgroups fit an int
+hipError_t launch_glr_chunk(const GlrArgs &a, bool bwd, hipStream_t stream);
+hipError_t launch_glr_step(const void *x, const void *g, float *state, void *o, size_t n, int dtype,
+                           hipStream_t stream);
+
 // True when the backward's two state passes run side by side (64-column slices, both
 // within one round of workgroups on `cus` CUs): see kla_chunk.hip.
 bool bwd_scans_concurrent(const ChunkArgs &a, int cus);

@@ -16,7 +16,8 @@ import torch
 __all__ = ["chunk_fwd", "chunk_workspace_bytes", "chunk_fwd_workspace_bytes", "pgdn_chunk_fwd", "pgdn_decode_step",
            "pgdn_chunk_workspace_bytes",
            "GAINS", "decode_step", "gdn_chunk_fwd", "gdn_decode_step", "chunk_bwd",
-           "gdn_chunk_bwd", "chunk_bwd_workspace_bytes", "lib", "lib_path", "KlaError", "KLA_DT_BF16",
+           "gdn_chunk_bwd", "chunk_bwd_workspace_bytes", "glr_chunk_fwd", "glr_chunk_bwd", "glr_decode_step",
+           "glr_chunk_workspace_bytes", "lib", "lib_path", "KlaError", "KLA_DT_BF16",
            "KLA_DT_F32"]
 
 KLA_DT_BF16 = 0
@@ -90,6 +91,15 @@ def lib() -> ctypes.CDLL:
         L.kla_pgdn_decode_step.argtypes = [vp, vp, vp, vp, vp, f32, i32, f32, vp, vp, vp,
                                            i32, i32, i32, i32, i32, vp]
         L.kla_pgdn_decode_step.restype = i32
+        L.kla_glr_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, sz, vp]
+        L.kla_glr_chunk_fwd.restype = i32
+        L.kla_glr_chunk_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, sz,
+                                        vp]
+        L.kla_glr_chunk_bwd.restype = i32
+        L.kla_glr_chunk_workspace_bytes.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32]
+        L.kla_glr_chunk_workspace_bytes.restype = sz
+        L.kla_glr_decode_step.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp]
+        L.kla_glr_decode_step.restype = i32
         L.kla_status_str.argtypes = [i32]
         L.kla_status_str.restype = ctypes.c_char_p
         L.kla_abi_version.argtypes = []
@@ -583,4 +593,171 @@ def pgdn_decode_step(
                                     float(band), _ptr(state), _ptr(acc), _ptr(out), N, H, dk, dv, _DTYPES[dtype],
                                     _stream(dev))
     _check("kla_pgdn_decode_step", st)
+    return out
+
+
+def _device_of(fn: str, t: torch.Tensor) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"kla.{fn}: expected a tensor, got {type(t).__name__}")
+    if t.device.type != "cuda":
+        raise ValueError(f"kla.{fn} needs GPU tensors")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return t.device
+
+
+def _rank(t: torch.Tensor, name: str, rank: int) -> tuple:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() != rank:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rank} dimensions")
+    return tuple(t.shape)
+
+
+def _seqlens(cu_seqlens, cu_seqlens_host, B: int, dev):
+    """Number of sequences and the host mirror of cu_seqlens (None for a dense batch)."""
+    if cu_seqlens is None:
+        if cu_seqlens_host is not None:
+            raise ValueError("cu_seqlens_host without cu_seqlens")
+        return B, None
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
+    if cu_seqlens.numel() == 0:
+        raise ValueError("cu_seqlens must hold at least one offset")
+    if cu_seqlens_host is None:
+        cu_seqlens_host = cu_seqlens
+    if cu_seqlens_host.numel() != cu_seqlens.numel():
+        raise ValueError("cu_seqlens_host does not mirror cu_seqlens")
+    return cu_seqlens.numel() - 1, cu_seqlens_host.to("cpu", torch.int32).contiguous()
+
+
+def _optional(t, name, dtype, shape, dev) -> None:
+    if t is not None:
+        _need(t, name, dtype, shape, dev)
+
+
+def _scratch(workspace, need: int, dev) -> Optional[torch.Tensor]:
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or workspace.dtype != torch.uint8 \
+            or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return workspace
+
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """Call the library on the current stream of the tensors' device, which need not be the
+    current device."""
+    f = getattr(lib(), fn)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = f(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(dev))
+    if st != 0:
+        _check(fn, st)
+
+
+def glr_chunk_workspace_bytes(B: int, H: int, T: int, d: int, dtype: torch.dtype = torch.bfloat16,
+                              cu_seqlens_host: Optional[torch.Tensor] = None) -> int:
+    """Workspace bytes glr_chunk_fwd and glr_chunk_bwd need (kla_glr_chunk_workspace_bytes)."""
+    if cu_seqlens_host is not None:
+        cu = cu_seqlens_host.to("cpu", torch.int32).contiguous()
+        # the device pointer is only tested for NULL here
+        return lib().kla_glr_chunk_workspace_bytes(ctypes.c_void_p(16), cu.data_ptr(), cu.numel() - 1, B, H, T, d,
+                                                   _DTYPES[dtype])
+    return lib().kla_glr_chunk_workspace_bytes(None, None, B, B, H, T, d, _DTYPES[dtype])
+
+
+def glr_chunk_fwd(
+    x: torch.Tensor,
+    g: torch.Tensor,
+    initial_state: Optional[torch.Tensor] = None,
+    cu_seqlens: Optional[torch.Tensor] = None,
+    output_final_state: bool = True,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+    out: Optional[torch.Tensor] = None,
+    final_state: Optional[torch.Tensor] = None,
+    workspace: Optional[torch.Tensor] = None,
+) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gated linear recurrence over whole sequences (kla_glr_chunk_fwd): per channel
+    h_t = exp(g_t) h_{t-1} + x_t, o_t = h_t.
+
+    x, g: [B, H, T, d], bf16 or fp32; initial_state: [N, H, d] fp32 or None; cu_seqlens: int32
+    [N + 1] on the GPU (B must be 1) or None, with its host mirror to avoid a copy back.
+    Returns (o, final_state); ``final_state`` may be passed as the same tensor as
+    ``initial_state``.
+    """
+    dev = _device_of("glr_chunk_fwd", x)
+    dtype = x.dtype
+    B, H, T, d = shape = _rank(x, "x", 4)
+    _need(x, "x", dtype, shape, dev)
+    _need(g, "g", dtype, shape, dev)
+    N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
+    _optional(initial_state, "initial_state", torch.float32, (N, H, d), dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out, "out", dtype, shape, dev)
+    if output_final_state and final_state is None:
+        final_state = torch.empty((N, H, d), dtype=torch.float32, device=dev)
+    _optional(final_state, "final_state", torch.float32, (N, H, d), dev)
+    host_ptr = _ptr(host)
+    ws = _scratch(workspace, lib().kla_glr_chunk_workspace_bytes(_ptr(cu_seqlens), host_ptr, N, B, H, T, d,
+                                                                 _DTYPES[dtype]), dev)
+    _call("kla_glr_chunk_fwd", dev, _ptr(x), _ptr(g), _ptr(initial_state), _ptr(out), _ptr(final_state),
+          _ptr(cu_seqlens), host_ptr, N, B, H, T, d, _DTYPES[dtype], _ptr(ws), 0 if ws is None else ws.numel())
+    return out, final_state
+
+
+def glr_chunk_bwd(
+    g: torch.Tensor,
+    o: torch.Tensor,
+    do: torch.Tensor,
+    initial_state: Optional[torch.Tensor] = None,
+    dfinal_state: Optional[torch.Tensor] = None,
+    cu_seqlens: Optional[torch.Tensor] = None,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+    need_dinitial: bool = True,
+    workspace: Optional[torch.Tensor] = None,
+):
+    """Gradients of glr_chunk_fwd (kla_glr_chunk_bwd) from its output ``o`` and the upstream
+    gradients ``do`` [B, H, T, d] and ``dfinal_state`` [N, H, d] fp32 or None.
+
+    Returns (dx, dg, dinitial_state): dx, dg in the inputs' dtype, dinitial_state [N, H, d]
+    fp32 (None unless ``need_dinitial``).
+    """
+    dev = _device_of("glr_chunk_bwd", g)
+    dtype = g.dtype
+    B, H, T, d = shape = _rank(g, "g", 4)
+    for t, name in ((g, "g"), (o, "o"), (do, "do")):
+        _need(t, name, dtype, shape, dev)
+    N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
+    _optional(initial_state, "initial_state", torch.float32, (N, H, d), dev)
+    _optional(dfinal_state, "dfinal_state", torch.float32, (N, H, d), dev)
+    dx, dg = torch.empty_like(g), torch.empty_like(g)
+    dh0 = torch.empty((N, H, d), dtype=torch.float32, device=dev) if need_dinitial else None
+    host_ptr = _ptr(host)
+    ws = _scratch(workspace, lib().kla_glr_chunk_workspace_bytes(_ptr(cu_seqlens), host_ptr, N, B, H, T, d,
+                                                                 _DTYPES[dtype]), dev)
+    _call("kla_glr_chunk_bwd", dev, _ptr(g), _ptr(o), _ptr(initial_state), _ptr(do), _ptr(dfinal_state), _ptr(dx),
+          _ptr(dg), _ptr(dh0), _ptr(cu_seqlens), host_ptr, N, B, H, T, d, _DTYPES[dtype], _ptr(ws),
+          0 if ws is None else ws.numel())
+    return dx, dg, dh0
+
+
+def glr_decode_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of the gated linear recurrence (kla_glr_decode_step): x, g [N, H, d];
+    ``state`` [N, H, d] fp32 is updated in place.  Returns o [N, H, d]."""
+    dev = _device_of("glr_decode_step", x)
+    dtype = x.dtype
+    N, H, d = shape = _rank(x, "x", 3)
+    _need(x, "x", dtype, shape, dev)
+    _need(g, "g", dtype, shape, dev)
+    _need(state, "state", torch.float32, shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out, "out", dtype, shape, dev)
+    _call("kla_glr_decode_step", dev, _ptr(x), _ptr(g), _ptr(state), _ptr(out), N, H, d, _DTYPES[dtype])
     return out

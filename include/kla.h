@@ -447,6 +447,78 @@ kla_status_t kla_pgdn_decode_step(const void *q, const void *k, const void *v,
                                   void *o, int N, int H, int dk, int dv,
                                   kla_dtype_t dtype, void *stream);
 
+/*
+ * kla_glr_chunk_fwd -- gated linear recurrence: the mixer whose state is one number per
+ * channel with a decay of its own, in place of a dk x dv matrix with a decay per head.
+ * Per sequence, head and channel:
+ *
+ *     h_t = exp(g_t) h_{t-1} + x_t,     o_t = h_t
+ *
+ *   x, g           [B, H, T, d]  dtype; g is the log-decay (g <= 0; -inf forgets the state).
+ *                  A layer without heads passes H = 1 and its width as d.
+ *   initial_state  [N, H, d] fp32, or NULL = zeros
+ *   o              [B, H, T, d]  dtype, written for every token
+ *   final_state    [N, H, d] fp32, or NULL = not written.  May alias initial_state.
+ *   cu_seqlens, cu_seqlens_host, num_seqs (N), B, H, T: as kla_chunk_fwd, without its
+ *                  limit on H
+ *   workspace      kla_glr_chunk_workspace_bytes(...) bytes for the same arguments (16-byte
+ *                  aligned, no initialisation needed; NULL when that is 0)
+ *
+ * Any d in [1, 2^24] and either dtype; d a multiple of 8 (BF16) or 4 (F32) moves 16 bytes at
+ * a time, another d runs the same kernel an element at a time.  Sums and states are fp32.
+ * Decays are composed as products over runs of tokens: where g > 0 makes such a product
+ * overflow fp32, outputs are not finite even if the recurrence would be.  Kernels run on
+ * `stream` only; results repeat bit for bit.  Status codes as kla_chunk_fwd.
+ */
+kla_status_t kla_glr_chunk_fwd(const void *x, const void *g, const float *initial_state,
+                               void *o, float *final_state,
+                               const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                               int num_seqs, int B, int H, int T, int d,
+                               kla_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * kla_glr_chunk_bwd -- gradients of kla_glr_chunk_fwd.  With dh_t the gradient that reaches
+ * h_t (dL/do_t plus what comes back from token t + 1):
+ *
+ *     dh_t = do_t + exp(g_{t+1}) dh_{t+1}   (at the last token: do_t + dL/dh_final)
+ *     dx_t = dh_t,   dg_t = dh_t exp(g_t) h_{t-1},   dL/dh_initial = exp(g_1) dh_1
+ *
+ *   g, initial_state, cu_seqlens, ...: the forward call's
+ *   o               [B, H, T, d] dtype: the forward's output, which holds h_{t-1} for every
+ *                   token but a sequence's first (initial_state).  x is not needed.  With
+ *                   BF16 that h_{t-1} is o's rounding of it, half a step of bf16 in dg, as much
+ *                   as storing dg in bf16 takes.
+ *   dout            [B, H, T, d] dtype
+ *   dfinal_state    [N, H, d] fp32, or NULL (zero)
+ *   dx, dg          [B, H, T, d] dtype (written; must not alias the inputs)
+ *   dinitial_state  [N, H, d] fp32 (written), or NULL (not computed)
+ *
+ * Workspace and everything else as kla_glr_chunk_fwd.
+ */
+kla_status_t kla_glr_chunk_bwd(const void *g, const void *o, const float *initial_state,
+                               const void *dout, const float *dfinal_state, void *dx, void *dg,
+                               float *dinitial_state,
+                               const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                               int num_seqs, int B, int H, int T, int d,
+                               kla_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * kla_glr_chunk_workspace_bytes -- device workspace of kla_glr_chunk_fwd and _bwd (host-only,
+ * no HIP call): two fp32 maps of d channels per (sequence, head, segment) where few channels
+ * make the library cut long sequences into segments, else 0; 0 for arguments they would reject.
+ */
+size_t kla_glr_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                                     int num_seqs, int B, int H, int T, int d, kla_dtype_t dtype);
+
+/*
+ * kla_glr_decode_step -- one token of the gated linear recurrence for N sequences x H heads:
+ * x, g [N, H, d] dtype; state [N, H, d] fp32 updated IN PLACE; o [N, H, d] dtype.  Any d.
+ */
+kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, void *o,
+                                 int N, int H, int d, kla_dtype_t dtype, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *kla_status_str(kla_status_t s);
 
