@@ -253,6 +253,55 @@ kla_status_t run_glr(kla::GlrArgs &a, bool bwd, void *workspace, size_t workspac
   return from_hip(kla::launch_glr_chunk(a, bwd, reinterpret_cast<hipStream_t>(stream)));
 }
 
+// The 4-bit cache's own arguments.
+kla_status_t check_kv4(int Hkv, int D, int num_pages, int page_size, int max_pages, int N, int dtype) {
+  if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
+  if (N < 0 || Hkv <= 0 || Hkv > (1 << 20) || D <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0)
+    return KLA_ERR_SHAPE;
+  if ((D != 64 && D != 128) || page_size % 16 != 0 || page_size > (1 << 20)) return KLA_ERR_UNSUPPORTED;
+  return KLA_OK;
+}
+
+kla_status_t kv4_move(void *k, void *v, const void *codes, const void *scales, const int32_t *table,
+                      const int32_t *start, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs,
+                      int B, int Hkv, int T, int D, int num_pages, int page_size, int max_pages, int dtype, bool read,
+                      void *stream) {
+  kla_status_t st = check_kv4(Hkv, D, num_pages, page_size, max_pages, num_seqs, dtype);
+  if (st != KLA_OK) return st;
+  if (B < 0 || T < 0 || T > kMaxTokens) return KLA_ERR_SHAPE;
+  int longest;
+  st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, T, &longest);
+  if (st != KLA_OK) return st;
+  if ((double)B * Hkv * T > (double)0x7fffffff) return KLA_ERR_SHAPE;
+  if (num_seqs == 0 || (long long)B * T == 0) return KLA_OK;
+  if (!k || !v || !codes || !scales || !table || !start) return KLA_ERR_NULL;
+  if (misaligned(k) || misaligned(v) || misaligned(codes) || misaligned(scales) || misaligned(table) || misaligned(start))
+    return KLA_ERR_ALIGN;
+  const kla::Kv4Cache c{const_cast<void *>(codes), const_cast<void *>(scales), table, num_pages, page_size, max_pages,
+                        Hkv};
+  return from_hip(kla::launch_kv4_move(c, k, v, start, cu_seqlens, num_seqs, B, T, D, dtype, read,
+                                       reinterpret_cast<hipStream_t>(stream)));
+}
+
+// The decode step's sizes; a's sizes are set where they are fine.
+kla_status_t check_kv4_decode(int N, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, int max_len,
+                              int dtype, kla::Kv4DecodeArgs *a) {
+  const kla_status_t st = check_kv4(Hkv, D, num_pages, page_size, max_pages, N, dtype);
+  if (st != KLA_OK) return st;
+  if (Hq <= 0 || Hq > (1 << 20) || Hq % Hkv != 0 || max_len < 0 || max_len > kMaxTokens) return KLA_ERR_SHAPE;
+  *a = kla::Kv4DecodeArgs{};
+  a->c.num_pages = num_pages;
+  a->c.page = page_size;
+  a->c.max_pages = max_pages;
+  a->c.Hkv = Hkv;
+  a->N = N;
+  a->Hq = Hq;
+  a->D = D;
+  a->max_len = max_len;
+  a->dtype = dtype;
+  return kla::kv4_decode_grid_fits(*a) ? KLA_OK : KLA_ERR_SHAPE;
+}
+
 float band_log(float band) { return band == 1.f ? 0.f : std::log(band); }
 
 }  // namespace
@@ -335,7 +384,7 @@ const char *kla_status_str(kla_status_t s) {
     case KLA_ERR_ALIGN: return "data pointers must be 16-byte aligned";
     case KLA_ERR_WORKSPACE: return "workspace missing or smaller than kla_chunk_workspace_bytes()";
     case KLA_ERR_HIP: return "HIP runtime error";
-    case KLA_ERR_PARAM: return "gain must be a kla_gain_t and band finite and >= 1";
+    case KLA_ERR_PARAM: return "gain must be a kla_gain_t and band finite and >= 1; an attention scale finite";
     case KLA_ERR_SCRATCH: return "the call needs more scratch than kla_chunk_fwd_noalloc's fixed buffer holds";
   }
   return "unknown status";
@@ -526,6 +575,54 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
   if (!x || !g || !state || !o) return KLA_ERR_NULL;
   if (misaligned(x) || misaligned(g) || misaligned(state) || misaligned(o)) return KLA_ERR_ALIGN;
   return from_hip(kla::launch_glr_step(x, g, state, o, (size_t)N * H * d, dtype, reinterpret_cast<hipStream_t>(stream)));
+}
+
+kla_status_t kla_kv4_append(const void *k, const void *v, void *codes, void *scales, const int32_t *block_table,
+                            const int32_t *start, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                            int num_seqs, int B, int Hkv, int T, int D, int num_pages, int page_size, int max_pages,
+                            kla_dtype_t dtype_, void *stream) {
+  return kv4_move(const_cast<void *>(k), const_cast<void *>(v), codes, scales, block_table, start, cu_seqlens,
+                  cu_seqlens_host, num_seqs, B, Hkv, T, D, num_pages, page_size, max_pages, raw(dtype_), false, stream);
+}
+
+kla_status_t kla_kv4_read(void *k, void *v, const void *codes, const void *scales, const int32_t *block_table,
+                          const int32_t *start, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                          int num_seqs, int B, int Hkv, int T, int D, int num_pages, int page_size, int max_pages,
+                          kla_dtype_t dtype_, void *stream) {
+  return kv4_move(k, v, codes, scales, block_table, start, cu_seqlens, cu_seqlens_host, num_seqs, B, Hkv, T, D,
+                  num_pages, page_size, max_pages, raw(dtype_), true, stream);
+}
+
+size_t kla_attn_kv4_decode_workspace_bytes(int N, int Hq, int Hkv, int D, int max_len, kla_dtype_t dtype_) {
+  kla::Kv4DecodeArgs a;
+  if (check_kv4_decode(N, Hq, Hkv, D, 1, 16, 1, max_len, raw(dtype_), &a) != KLA_OK || N == 0) return 0;
+  return kla::kv4_decode_workspace_bytes(a);
+}
+
+kla_status_t kla_attn_kv4_decode_step(const void *q, const void *codes, const void *scales,
+                                      const int32_t *block_table, const int32_t *seq_lens, float scale, void *o, int N,
+                                      int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, int max_len,
+                                      kla_dtype_t dtype_, void *workspace, size_t workspace_bytes, void *stream) {
+  kla::Kv4DecodeArgs a;
+  const kla_status_t st =
+      check_kv4_decode(N, Hq, Hkv, D, num_pages, page_size, max_pages, max_len, raw(dtype_), &a);
+  if (st != KLA_OK) return st;
+  if (!std::isfinite(scale)) return KLA_ERR_PARAM;
+  if (N == 0) return KLA_OK;
+  if (!q || !codes || !scales || !block_table || !seq_lens || !o) return KLA_ERR_NULL;
+  if (misaligned(q) || misaligned(codes) || misaligned(scales) || misaligned(block_table) || misaligned(seq_lens) ||
+      misaligned(o) || misaligned(workspace))
+    return KLA_ERR_ALIGN;
+  const size_t need = kla::kv4_decode_workspace_bytes(a);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KLA_ERR_WORKSPACE;
+  a.c.codes = const_cast<void *>(codes);
+  a.c.scales = const_cast<void *>(scales);
+  a.c.table = block_table;
+  a.q = q;
+  a.o = o;
+  a.lens = seq_lens;
+  a.scale = scale;
+  return from_hip(kla::launch_attn_kv4_decode(a, workspace, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -149,6 +149,27 @@ hipError_t launch_glr_chunk(const GlrArgs &a, bool bwd, hipStream_t stream);
 hipError_t launch_glr_step(const void *x, const void *g, float *state, void *o, size_t n, int dtype,
                            hipStream_t stream);
 
+// The 4-bit key/value cache (kla_kv4.hip): codes [num_pages, 2, Hkv, page, D/2], scales
+// [num_pages, 2, Hkv, page, D/32], block table [N, max_pages].
+struct Kv4Cache {
+  void *codes, *scales;
+  const int32_t *table;
+  int num_pages, page, max_pages, Hkv;
+};
+hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,
+                           int T, int D, int dtype, bool read, hipStream_t stream);
+struct Kv4DecodeArgs {
+  Kv4Cache c;
+  const void *q;
+  void *o;
+  const int32_t *lens;
+  float scale;
+  int N, Hq, D, max_len, dtype;
+};
+size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs &a);
+bool kv4_decode_grid_fits(const Kv4DecodeArgs &a);
+hipError_t launch_attn_kv4_decode(const Kv4DecodeArgs &a, void *workspace, hipStream_t stream);
+
 // True when the backward's two state passes run side by side (64-column slices, both
 // within one round of workgroups on `cus` CUs): see kla_chunk.hip.
 bool bwd_scans_concurrent(const ChunkArgs &a, int cus);

@@ -1,0 +1,488 @@
+// kla_kv4.hip -- a paged key/value cache held in 4 bits, and attention of single tokens over
+// it (gfx950).
+//
+// Format (include/kla.h, kla_kv4_append): per token, head and K or V, blocks of 32 channels
+// share a power-of-two scale 2^(s - 127) (one byte, E8M0), and every channel is one E2M1 code
+// (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), the even channel in a byte's low half:
+// D/2 + D/32 bytes for D channels, 68 for D = 128 against 256 in bf16.  With
+// s - 127 = floor(log2 max|x|) - 2 every step is exact but the one rounding to a code (to the
+// nearest, ties to the even code, beyond 6 to 6), which gfx950's v_cvt_scalef32_pk_fp4_f32
+// does; the values read back are exact in bf16.
+//
+// Bound: all three kernels by HBM.  kla_kv4_append and kla_kv4_read give four lanes to a block
+// of 32 channels (16 bytes of bf16 and 4 of codes each).  The decode kernel is described below.
+#include <algorithm>
+
+#include "kla_common.h"
+#include "kla_internal.h"
+
+namespace kla {
+
+namespace {
+
+struct KvParams {
+  uint8_t *codes, *scales;
+  const int32_t *table;
+  int num_pages, page, max_pages, Hkv;
+};
+
+// Row (in units of a token's codes or scales) of position pos of sequence n in K (j = 0) or V
+// (j = 1) of a head; -1 where the table does not lead to a page of the cache.
+__device__ __forceinline__ long long kv_row(const KvParams &p, int n, int pos, int j, int head) {
+  if (pos < 0 || pos / p.page >= p.max_pages) return -1;
+  const int id = p.table[(size_t)n * p.max_pages + pos / p.page];
+  if (id < 0 || id >= p.num_pages) return -1;
+  return (((long long)id * 2 + j) * p.Hkv + head) * p.page + pos % p.page;
+}
+
+template <int CTRL>
+__device__ __forceinline__ unsigned quad_max(unsigned v) {
+  return max(v, (unsigned)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true));
+}
+
+struct KvMoveParams {
+  KvParams kv;
+  void *k, *v;                // [B, Hkv, T, D]
+  const int32_t *start, *cu;  // device
+  int N, T;
+  long long rows;             // B * Hkv * T
+};
+
+// eight channels as fp32
+template <typename E>
+__device__ __forceinline__ void ld8(const E *p, float *f) {
+  constexpr int PER = 16 / sizeof(E);
+#pragma unroll
+  for (int i = 0; i < 8; i += PER) {
+    const uint4 u = ldg16(p + i);
+    E e[PER];
+    __builtin_memcpy(e, &u, 16);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) f[i + j] = Elem<E>::to_f32(e[j]);
+  }
+}
+template <typename E>
+__device__ __forceinline__ void st8(E *p, const float *f) {
+  constexpr int PER = 16 / sizeof(E);
+#pragma unroll
+  for (int i = 0; i < 8; i += PER) {
+    E e[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) e[j] = Elem<E>::from_f32(f[i + j]);
+    uint4 u;
+    __builtin_memcpy(&u, e, 16);
+    stg16(p + i, u);
+  }
+}
+
+// D / 8 lanes to a row; blockIdx.y: K or V.
+template <typename E, int D, bool READ>
+__global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
+  constexpr int LPR = D / 8;
+  const int lane = threadIdx.x % LPR;
+  const long long row = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  if (row >= p.rows) return;
+  const int t = (int)(row % p.T), head = (int)((row / p.T) % p.kv.Hkv);
+  int n = (int)(row / p.T / p.kv.Hkv), at = t;
+  if (p.cu) {
+    // the last sequence that starts at or before t and is not empty (device offsets clamped)
+    int lo = 0, hi = p.N;  // cu[lo] <= t < cu[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cu[mid] <= t) lo = mid; else hi = mid;
+    }
+    n = lo;
+    at = t - max(p.cu[n], 0);
+  }
+  const long long pos = (long long)p.start[n] + at;
+  const int j = blockIdx.y;
+  const long long dst = pos > 0x7fffffffLL ? -1 : kv_row(p.kv, n, (int)max(pos, -1LL), j, head);
+  E *x = (E *)(j ? p.v : p.k) + row * D + 8 * lane;
+  float f[8];
+  if constexpr (READ) {
+    if (dst < 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    } else {
+      const unsigned u = *reinterpret_cast<const unsigned *>(p.kv.codes + dst * (D / 2) + 4 * lane);
+      const float s = __builtin_bit_cast(float, (unsigned)p.kv.scales[dst * (D / 32) + lane / 4] << 23);
+      typedef float f32x2 __attribute__((ext_vector_type(2)));
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, s, 1);
+      const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, s, 3);
+      f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1], f[4] = c[0], f[5] = c[1], f[6] = d[0], f[7] = d[1];
+    }
+    st8(x, f);
+  } else {
+    ld8((const E *)x, f);
+    unsigned top = 0;  // |x| as bits: NaN above infinity above every number
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(unsigned, f[i]) & 0x7fffffffu);
+    top = quad_max<0xB1>(top);
+    top = quad_max<0x4E>(top);
+    const unsigned e = top >> 23, s = e == 255 ? 255u : (e > 3 ? e - 2 : 1u);
+    const float sc = __builtin_bit_cast(float, s << 23);
+    unsigned u = 0;
+    u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[0], f[1], sc, 0);
+    u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[2], f[3], sc, 1);
+    u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[4], f[5], sc, 2);
+    u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[6], f[7], sc, 3);
+    if (dst >= 0) {
+      *reinterpret_cast<unsigned *>(p.kv.codes + dst * (D / 2) + 4 * lane) = u;
+      if (lane % 4 == 0) p.kv.scales[dst * (D / 32) + lane / 4] = (uint8_t)s;
+    }
+  }
+}
+
+// ---- attention of one token per sequence ------------------------------------------------------
+//
+// o = softmax(scale q K^T) V over the sequence's cached tokens.  A workgroup (four waves) owns
+// one (sequence, key head, up to 16 of its query heads, run of `per` tokens); its waves take
+// tiles of 32 tokens in turn, each with its own running maximum, sum and output, joined in LDS
+// at the end, and the runs of one head are joined by a second kernel.
+//
+// Codes become MFMA operands without LDS.  K: lane (r = lane & 15, c = lane >> 4) holds a
+// quarter of key r's row, channels c D/4 and up; its j-th eight channels are its slots of the
+// j-th v_mfma_f32_16x16x32_bf16, q being laid out the same.  The scores S^T come with heads
+// along the lanes and keys 4c .. 4c+3 in each, so that two 16-key tiles are the left-over
+// operand P^T of the second product as they stand: slots 8c + e are the keys 4c + e and
+// 16 + 4c + e - 4.  V: the lane loads channels r D/16 and up of those eight keys, converts
+// pairs of channels (v_cvt_scalef32_pk_bf16_fp4 applies the scale too) and exchanges halves
+// (v_perm) into pairs of keys; MFMA j takes channel r D/16 + j of every lane.
+//
+// Queries in fp32 run the same products with q and P split into three bf16 terms (24 bits),
+// exact against the cache's values.
+struct KvDecodeParams {
+  KvParams kv;
+  const void *q;
+  void *o;
+  const int32_t *lens;
+  float scale_log2;    // scale * log2(e)
+  int N, Hq, G, GB;    // G query heads to a key head, in GB blocks of 16
+  int max_len, splits, per;
+  float *part_o, *part_ml;  // [N Hq, splits, D], [N Hq, splits, 2] where splits > 1
+};
+
+constexpr int KV_MAX_PER = 8192;  // tokens of a run
+
+typedef bf16 bf16x8v __attribute__((ext_vector_type(8)));
+
+// eight channels in a dword as four bf16 pairs
+__device__ __forceinline__ void cvt8(unsigned u, float s, unsigned *r) {
+  r[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, s, 0));
+  r[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, s, 1));
+  r[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, s, 2));
+  r[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, s, 3));
+}
+
+template <typename E, int D>
+__global__ __launch_bounds__(256) void kla_kv4_decode_kernel(KvDecodeParams p) {
+  constexpr int NT = sizeof(E) == 2 ? 1 : 3;  // bf16 terms of q and P
+  constexpr int KJ = D / 32;                  // products over the channels, 8 channels a lane
+  constexpr int DW = D / 16;                  // channels of V a lane holds
+  __shared__ int s_page[KV_MAX_PER / 16];
+  __shared__ float s_o[4][16][D + 4];
+  __shared__ float s_ml[4][16][2];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 15, c = lane >> 4;
+  unsigned b = blockIdx.x;
+  const int split = b % p.splits;
+  b /= p.splits;
+  const int gb = b % p.GB;
+  b /= p.GB;
+  const int head = b % p.kv.Hkv, n = b / p.kv.Hkv;
+  const int g0 = gb * 16, gn = min(p.G - g0, 16);  // query heads of this workgroup
+  const int hq0 = head * p.G + g0;
+  // tokens of the sequence, of this run
+  const long long room = (long long)p.kv.max_pages * p.kv.page;
+  const int len = (int)min((long long)min(max(p.lens[n], 0), p.max_len), room);
+  const int lo = split * p.per, hi = (int)min((long long)len, (long long)lo + p.per);
+
+  if (hi > lo) {
+    for (int i = tid; i < (hi - lo + 31) / 32 * 2; i += 256) {
+      const int t = lo + 16 * i;
+      int id = -1;
+      if (t < hi) {
+        id = p.kv.table[(size_t)n * p.kv.max_pages + t / p.kv.page];
+        if (id >= p.kv.num_pages) id = -1;
+      }
+      s_page[i] = id;
+    }
+  }
+  // q: slots 8c + e of product j are channels c D/4 + 8j + e
+  bf16x8v q[NT][KJ];
+#pragma unroll
+  for (int j = 0; j < KJ; ++j) {
+    float f[8] = {};
+    if (r < gn) ld8((const E *)p.q + ((size_t)n * p.Hq + hq0 + r) * D + c * (D / 4) + 8 * j, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const bf16 h = (bf16)f[i];
+        q[t][j][i] = h;
+        f[i] -= (float)h;
+      }
+  }
+  __syncthreads();
+
+  f32x4 acc[DW];
+#pragma unroll
+  for (int j = 0; j < DW; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+
+  // one tile's codes and scales
+  unsigned kc[2][KJ], vc[8];
+  uint8_t ks[2], vs[8];
+  int id0, id1;
+  auto load = [&](int t) {
+    id0 = __builtin_amdgcn_readfirstlane(s_page[(t - lo) >> 4]);
+    id1 = __builtin_amdgcn_readfirstlane(s_page[((t - lo) >> 4) + 1]);
+    const size_t pg = (size_t)p.kv.Hkv * p.kv.page;
+    // rows of the two 16-token blocks (page 0 where there is none: masked below)
+    const size_t r0 = (size_t)max(id0, 0) * 2 * pg + (size_t)head * p.kv.page + t % p.kv.page;
+    const size_t r1 = (size_t)max(id1, 0) * 2 * pg + (size_t)head * p.kv.page + (t + 16) % p.kv.page;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const size_t row = (h ? r1 : r0) + r;
+      const uint8_t *a = p.kv.codes + row * (D / 2) + c * (D / 8);
+      if constexpr (D == 128) {
+        const uint4 u = ldg16(a);
+        kc[h][0] = u.x, kc[h][1] = u.y, kc[h][2] = u.z, kc[h][3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(a);
+        kc[h][0] = u.x, kc[h][1] = u.y;
+      }
+      ks[h] = p.kv.scales[row * (D / 32) + (D == 128 ? c : c / 2)];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const size_t row = (e < 4 ? r0 : r1) + pg + 4 * c + (e & 3);
+      if constexpr (D == 128) vc[e] = *reinterpret_cast<const unsigned *>(p.kv.codes + row * 64 + 4 * r);
+      else vc[e] = *reinterpret_cast<const unsigned short *>(p.kv.codes + row * 32 + 2 * r);
+      vs[e] = p.kv.scales[row * (D / 32) + (r * DW) / 32];
+    }
+  };
+
+  int t = lo + 32 * wave;
+  if (t < hi) load(t);
+  for (; t < hi; t += 128) {
+    // scores of keys t + 16h + 4c + i against head r
+    float x[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      const float sc = __builtin_bit_cast(float, (unsigned)ks[h] << 23);
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) {
+        unsigned w[4];
+        cvt8(kc[h][j], sc, w);
+        bf16x8v a;
+        __builtin_memcpy(&a, w, 16);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[u][j], s, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[4 * h + i] = s[i] * p.scale_log2;
+    }
+    unsigned va[8];
+    float vf[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      va[e] = vc[e];
+      vf[e] = __builtin_bit_cast(float, (unsigned)vs[e] << 23);
+    }
+    if (id0 < 0 || id1 < 0 || t + 32 > hi) {
+      // tokens past the end and tokens of missing pages: no score, and a value of zero
+      // whatever the memory behind them holds
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool none = (e < 4 ? id0 : id1) < 0 || t + 16 * (e >> 2) + 4 * c + (e & 3) >= hi;
+        x[e] = none ? -INFINITY : x[e];
+        va[e] = none ? 0u : va[e];
+        vf[e] = none ? 1.f : vf[e];
+      }
+    }
+    if (t + 128 < hi) load(t + 128);
+
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float mn = fmaxf(m, top);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    if (__any(mn > m)) {
+      const float al = __builtin_amdgcn_exp2f(m - base);
+      l *= al;
+#pragma unroll
+      for (int j = 0; j < DW; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] *= al;
+      m = mn;
+    }
+    bf16x8v pt[NT];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float v = __builtin_amdgcn_exp2f(x[e] - base);
+      l += v;
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        const bf16 h = (bf16)v;  // P in bf16 terms: one has half a step of 2^-8, as the output's rounding
+        pt[u][e] = h;
+        v -= (float)h;
+      }
+    }
+    // V: pairs of channels of each key, then pairs of keys of each channel
+    unsigned w[8][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cvt8(va[e], vf[e], w[e]);
+#pragma unroll
+    for (int j = 0; j < DW; ++j) {
+      unsigned a[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        a[e] = __builtin_amdgcn_perm(w[2 * e + 1][j / 2], w[2 * e][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+      bf16x8v av;
+      __builtin_memcpy(&av, a, 16);
+#pragma unroll
+      for (int u = 0; u < NT; ++u) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, pt[u], acc[j], 0, 0, 0);
+    }
+  }
+
+  // join the waves
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (c == 0) {
+    s_ml[wave][r][0] = m;
+    s_ml[wave][r][1] = l;
+  }
+#pragma unroll
+  for (int j = 0; j < DW; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_o[wave][r][(4 * c + i) * DW + j] = acc[j][i];
+  __syncthreads();
+  for (int i = tid; i < gn * D; i += 256) {
+    const int g = i / D, d = i % D;
+    float mm = s_ml[0][g][0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) mm = fmaxf(mm, s_ml[w][g][0]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, oo = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = __builtin_amdgcn_exp2f(s_ml[w][g][0] - base);
+      ll = fmaf(s_ml[w][g][1], f, ll);
+      oo = fmaf(s_o[w][g][d], f, oo);
+    }
+    const size_t row = (size_t)n * p.Hq + hq0 + g;
+    if (p.splits == 1) {
+      ((E *)p.o)[row * D + d] = Elem<E>::from_f32(ll == 0.f ? 0.f : oo / ll);
+    } else {
+      p.part_o[(row * p.splits + split) * D + d] = oo;
+      if (d == 0) {
+        p.part_ml[(row * p.splits + split) * 2] = mm;
+        p.part_ml[(row * p.splits + split) * 2 + 1] = ll;
+      }
+    }
+  }
+}
+
+// The runs of one (sequence, query head), in order.
+template <typename E, int D>
+__global__ __launch_bounds__(D) void kla_kv4_join_kernel(KvDecodeParams p) {
+  const size_t row = blockIdx.x;
+  const float *ml = p.part_ml + row * p.splits * 2;
+  float m = -INFINITY;
+  for (int s = threadIdx.x % 64; s < p.splits; s += 64) m = fmaxf(m, ml[2 * s]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o = 0.f;
+  const float *po = p.part_o + row * p.splits * D + threadIdx.x;
+#pragma unroll 8
+  for (int s = 0; s < p.splits; ++s) {
+    const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
+    l = fmaf(ml[2 * s + 1], f, l);
+    o = fmaf(po[(size_t)s * D], f, o);
+  }
+  ((E *)p.o)[row * D + threadIdx.x] = Elem<E>::from_f32(l == 0.f ? 0.f : o / l);
+}
+
+template <typename E, bool READ>
+hipError_t launch_move(const KvMoveParams &p, int D, hipStream_t st) {
+  const int rpb = 256 / (D / 8);
+  const dim3 grid((unsigned)((p.rows + rpb - 1) / rpb), 2);
+  if (D == 128) hipLaunchKernelGGL((kla_kv4_move_kernel<E, 128, READ>), grid, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((kla_kv4_move_kernel<E, 64, READ>), grid, dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+template <typename E, int D>
+hipError_t launch_kv4_decode(const KvDecodeParams &p, hipStream_t st) {
+  const long long grid = (long long)p.N * p.kv.Hkv * p.GB * p.splits;
+  hipLaunchKernelGGL((kla_kv4_decode_kernel<E, D>), dim3((unsigned)grid), dim3(256), 0, st, p);
+  if (p.splits > 1)
+    hipLaunchKernelGGL((kla_kv4_join_kernel<E, D>), dim3((unsigned)((long long)p.N * p.Hq)), dim3(D), 0, st, p);
+  return hipGetLastError();
+}
+
+KvParams kv_params(const Kv4Cache &c) {
+  return KvParams{(uint8_t *)c.codes, (uint8_t *)c.scales, c.table, c.num_pages, c.page, c.max_pages, c.Hkv};
+}
+
+// Runs of the sequences: as many as bring about 1,024 workgroups (four to a CU), of 256 tokens
+// at least (eight a wave) and KV_MAX_PER at most.
+void kv4_runs(const Kv4DecodeArgs &a, int *splits, int *per) {
+  const long long GB = (a.Hq / a.c.Hkv + 15) / 16, base = (long long)a.N * a.c.Hkv * GB;
+  long long want = std::max<long long>(1, 1024 / std::max<long long>(1, base));
+  want = std::min(want, std::max<long long>(1, a.max_len / 256));
+  long long len = (a.max_len + want - 1) / want;
+  len = std::min<long long>(KV_MAX_PER, std::max<long long>(128, (len + 127) / 128 * 128));
+  *per = (int)len;
+  *splits = (int)std::max<long long>(1, (a.max_len + len - 1) / len);
+}
+
+}  // namespace
+
+size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs &a) {
+  int splits, per;
+  kv4_runs(a, &splits, &per);
+  return splits == 1 ? 0 : (size_t)a.N * a.Hq * splits * (a.D + 2) * sizeof(float);
+}
+
+bool kv4_decode_grid_fits(const Kv4DecodeArgs &a) {
+  int splits, per;
+  kv4_runs(a, &splits, &per);
+  return (long long)a.N * a.c.Hkv * ((a.Hq / a.c.Hkv + 15) / 16) * splits <= 0x7fffffffLL &&
+         (long long)a.N * a.Hq <= 0x7fffffffLL;
+}
+
+hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,
+                           int T, int D, int dtype, bool read, hipStream_t st) {
+  const KvMoveParams p{kv_params(c), k, v, start, cu, N, T, (long long)B * c.Hkv * T};
+  if (p.rows == 0) return hipSuccess;
+  if (dtype == 0) return read ? launch_move<bf16, true>(p, D, st) : launch_move<bf16, false>(p, D, st);
+  return read ? launch_move<float, true>(p, D, st) : launch_move<float, false>(p, D, st);
+}
+
+hipError_t launch_attn_kv4_decode(const Kv4DecodeArgs &a, void *workspace, hipStream_t st) {
+  KvDecodeParams p{};
+  p.kv = kv_params(a.c);
+  p.q = a.q;
+  p.o = a.o;
+  p.lens = a.lens;
+  p.scale_log2 = a.scale * 1.44269504f;
+  p.N = a.N;
+  p.Hq = a.Hq;
+  p.G = a.Hq / a.c.Hkv;
+  p.GB = (p.G + 15) / 16;
+  p.max_len = a.max_len;
+  kv4_runs(a, &p.splits, &p.per);
+  p.part_o = (float *)workspace;
+  p.part_ml = p.part_o + (size_t)a.N * a.Hq * p.splits * a.D;
+  if (a.dtype == 0) return a.D == 128 ? launch_kv4_decode<bf16, 128>(p, st) : launch_kv4_decode<bf16, 64>(p, st);
+  return a.D == 128 ? launch_kv4_decode<float, 128>(p, st) : launch_kv4_decode<float, 64>(p, st);
+}
+
+}  // namespace kla

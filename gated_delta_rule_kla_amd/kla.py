@@ -17,7 +17,8 @@ __all__ = ["chunk_fwd", "chunk_workspace_bytes", "chunk_fwd_workspace_bytes", "p
            "pgdn_chunk_workspace_bytes",
            "GAINS", "decode_step", "gdn_chunk_fwd", "gdn_decode_step", "chunk_bwd",
            "gdn_chunk_bwd", "chunk_bwd_workspace_bytes", "glr_chunk_fwd", "glr_chunk_bwd", "glr_decode_step",
-           "glr_chunk_workspace_bytes", "lib", "lib_path", "KlaError", "KLA_DT_BF16",
+           "glr_chunk_workspace_bytes", "kv4_append", "kv4_read", "kv4_cache", "attn_kv4_decode_step",
+           "attn_kv4_decode_workspace_bytes", "lib", "lib_path", "KlaError", "KLA_DT_BF16",
            "KLA_DT_F32"]
 
 KLA_DT_BF16 = 0
@@ -100,6 +101,14 @@ def lib() -> ctypes.CDLL:
         L.kla_glr_chunk_workspace_bytes.restype = sz
         L.kla_glr_decode_step.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp]
         L.kla_glr_decode_step.restype = i32
+        for f in (L.kla_kv4_append, L.kla_kv4_read):
+            f.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp]
+            f.restype = i32
+        L.kla_attn_kv4_decode_step.argtypes = [vp, vp, vp, vp, vp, f32, vp, i32, i32, i32, i32, i32, i32, i32, i32,
+                                               i32, vp, sz, vp]
+        L.kla_attn_kv4_decode_step.restype = i32
+        L.kla_attn_kv4_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+        L.kla_attn_kv4_decode_workspace_bytes.restype = sz
         L.kla_status_str.argtypes = [i32]
         L.kla_status_str.restype = ctypes.c_char_p
         L.kla_abi_version.argtypes = []
@@ -760,4 +769,129 @@ def glr_decode_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
     else:
         _need(out, "out", dtype, shape, dev)
     _call("kla_glr_decode_step", dev, _ptr(x), _ptr(g), _ptr(state), _ptr(out), N, H, d, _DTYPES[dtype])
+    return out
+
+
+def kv4_cache(num_pages: int, Hkv: int, page_size: int, D: int, device) -> Tuple[torch.Tensor, torch.Tensor]:
+    """An empty 4-bit key/value cache: (codes [num_pages, 2, Hkv, page_size, D/2], scales
+    [num_pages, 2, Hkv, page_size, D/32]), uint8 (the format: kla_kv4_append in include/kla.h)."""
+    return (torch.zeros(num_pages, 2, Hkv, page_size, D // 2, dtype=torch.uint8, device=device),
+            torch.zeros(num_pages, 2, Hkv, page_size, D // 32, dtype=torch.uint8, device=device))
+
+
+def _cache_args(codes, scales, block_table, N: int, dev):
+    P, two, Hkv, page, half = _rank(codes, "codes", 5)
+    if two != 2:
+        raise ValueError(f"codes has shape {tuple(codes.shape)}, expected [num_pages, 2, Hkv, page_size, D/2]")
+    D = 2 * half
+    _need(codes, "codes", torch.uint8, (P, 2, Hkv, page, half), dev)
+    _need(scales, "scales", torch.uint8, (P, 2, Hkv, page, D // 32), dev)
+    _, M = _rank(block_table, "block_table", 2)
+    _need(block_table, "block_table", torch.int32, (N, M), dev)
+    return P, Hkv, page, D, M
+
+
+def kv4_append(
+    k: torch.Tensor,
+    v: torch.Tensor,
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    block_table: torch.Tensor,
+    start: torch.Tensor,
+    cu_seqlens: Optional[torch.Tensor] = None,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+) -> None:
+    """Store keys and values in a 4-bit cache (kla_kv4_append), in place.
+
+    k, v: [B, Hkv, T, D], bf16 or fp32; codes, scales: as kv4_cache makes them; block_table:
+    int32 [N, max_pages]; start: int32 [N], the tokens that each sequence holds already;
+    cu_seqlens as in chunk_fwd (None: N = B).
+    """
+    dev = _device_of("kv4_append", k)
+    B, Hkv, T, D = shape = _rank(k, "k", 4)
+    _need(k, "k", k.dtype, shape, dev)
+    _need(v, "v", k.dtype, shape, dev)
+    N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
+    P, H, page, Dc, M = _cache_args(codes, scales, block_table, N, dev)
+    if (H, Dc) != (Hkv, D):
+        raise ValueError(f"k has {Hkv} heads of {D} channels, the cache {H} of {Dc}")
+    _need(start, "start", torch.int32, (N,), dev)
+    _call("kla_kv4_append", dev, _ptr(k), _ptr(v), _ptr(codes), _ptr(scales), _ptr(block_table), _ptr(start),
+          _ptr(cu_seqlens), _ptr(host), N, B, Hkv, T, D, P, page, M, _DTYPES[k.dtype])
+
+
+def kv4_read(
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    block_table: torch.Tensor,
+    start: torch.Tensor,
+    cu_seqlens: torch.Tensor,
+    dtype: torch.dtype = torch.bfloat16,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+    out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The values that a 4-bit cache holds (kla_kv4_read): k, v [1, Hkv, T, D] of positions
+    start[n] ... start[n] + length of sequence n, packed by cu_seqlens (int32 [N + 1], T its
+    last).  With ``out`` (k, v) nothing is copied from the GPU."""
+    if not isinstance(codes, torch.Tensor) or codes.device.type != "cuda":
+        raise ValueError("kla.kv4_read needs GPU tensors")
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    dev = codes.device
+    N, host = _seqlens(cu_seqlens, cu_seqlens_host, 1, dev)
+    if host is None:
+        raise ValueError("kla.kv4_read needs cu_seqlens")
+    P, Hkv, page, D, M = _cache_args(codes, scales, block_table, N, dev)
+    _need(start, "start", torch.int32, (N,), dev)
+    T = int(host[-1])
+    shape = (1, Hkv, max(T, 0), D)
+    if out is None:
+        out = (torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev))
+    _need(out[0], "out[0]", dtype, shape, dev)
+    _need(out[1], "out[1]", dtype, shape, dev)
+    _call("kla_kv4_read", dev, _ptr(out[0]), _ptr(out[1]), _ptr(codes), _ptr(scales), _ptr(block_table), _ptr(start),
+          _ptr(cu_seqlens), _ptr(host), N, 1, Hkv, T, D, P, page, M, _DTYPES[dtype])
+    return out
+
+
+def attn_kv4_decode_workspace_bytes(N: int, Hq: int, Hkv: int, D: int, max_len: int,
+                                    dtype: torch.dtype = torch.bfloat16) -> int:
+    """Workspace bytes attn_kv4_decode_step needs (kla_attn_kv4_decode_workspace_bytes)."""
+    return lib().kla_attn_kv4_decode_workspace_bytes(N, Hq, Hkv, D, int(max_len), _DTYPES[dtype])
+
+
+def attn_kv4_decode_step(
+    q: torch.Tensor,
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    block_table: torch.Tensor,
+    seq_lens: torch.Tensor,
+    scale: Optional[float] = None,
+    max_len: Optional[int] = None,
+    out: Optional[torch.Tensor] = None,
+    workspace: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """Attention of one token per sequence over a 4-bit cache (kla_attn_kv4_decode_step).
+
+    q: [N, Hq, D], bf16 or fp32; seq_lens: int32 [N] cached tokens, the new one's among them;
+    scale: D ** -0.5 when None; max_len: a bound on seq_lens known to the host (the block
+    table's room when None; a tight one makes fewer, fuller workgroups).  Returns o [N, Hq, D].
+    """
+    dev = _device_of("attn_kv4_decode_step", q)
+    N, Hq, D = shape = _rank(q, "q", 3)
+    _need(q, "q", q.dtype, shape, dev)
+    P, Hkv, page, Dc, M = _cache_args(codes, scales, block_table, N, dev)
+    if Dc != D:
+        raise ValueError(f"q has {D} channels, the cache {Dc}")
+    _need(seq_lens, "seq_lens", torch.int32, (N,), dev)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", q.dtype, shape, dev)
+    max_len = M * page if max_len is None else int(max_len)
+    dt = _DTYPES[q.dtype]
+    ws = _scratch(workspace, lib().kla_attn_kv4_decode_workspace_bytes(N, Hq, Hkv, D, max_len, dt), dev)
+    _call("kla_attn_kv4_decode_step", dev, _ptr(q), _ptr(codes), _ptr(scales), _ptr(block_table), _ptr(seq_lens),
+          D ** -0.5 if scale is None else float(scale), _ptr(out), N, Hq, Hkv, D, P, page, M, max_len, dt, _ptr(ws),
+          0 if ws is None else ws.numel())
     return out

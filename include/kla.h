@@ -65,7 +65,8 @@ typedef enum {
     KLA_ERR_ALIGN = -8,       /* a data pointer is not 16-byte aligned           */
     KLA_ERR_HIP = -9,         /* the HIP runtime rejected a launch               */
     KLA_ERR_SCRATCH = -10,    /* kla_chunk_fwd_noalloc: more scratch than its fixed buffer */
-    KLA_ERR_PARAM = -11       /* PGDN: gain not a kla_gain_t, or band not finite and >= 1 */
+    KLA_ERR_PARAM = -11       /* PGDN: gain not a kla_gain_t, or band not finite and >= 1;
+                                 attention: scale not finite                     */
 } kla_status_t;
 
 /* The update coefficient ("gain") of the preconditioned variant (kla_pgdn_*). */
@@ -518,6 +519,81 @@ size_t kla_glr_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *c
  */
 kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, void *o,
                                  int N, int H, int d, kla_dtype_t dtype, void *stream);
+
+/*
+ * kla_kv4_append, kla_kv4_read -- a paged key/value cache held in 4 bits, for the softmax
+ * attention layers that stand between recurrent ones.
+ *
+ * Format.  32 consecutive channels of a token's key or value share a scale 2^(s - 127), s one
+ * byte (E8M0: 255 stands for NaN); a channel is a 4-bit code E2M1 (sign, then 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6), the even channel in the low half of its byte.  The Open Compute Project's
+ * microscaling rule makes them: with E = floor(log2 max|x|) over the 32 channels,
+ * s - 127 = max(E - 2, -126), and a code is x / 2^(s-127) rounded to the nearest, ties to the
+ * even code, beyond 6 to 6.  A block of zeros has s = 1; one that holds an infinity or a NaN
+ * reads back as NaN.  Everything but the rounding to a code is exact, and so are the values
+ * in bf16.
+ *
+ *   k, v          [B, Hkv, T, D] dtype
+ *   codes         [num_pages, 2, Hkv, page_size, D/2] bytes, keys before values
+ *   scales        [num_pages, 2, Hkv, page_size, D/32] bytes
+ *   block_table   device int32 [N, max_pages]: the pages of each sequence, in order
+ *   start         device int32 [N]: the position in its sequence of a sequence's first token
+ *                 of this call (append: the tokens it holds already)
+ *   cu_seqlens, cu_seqlens_host, num_seqs (N), B, T: as kla_chunk_fwd; token i of sequence n
+ *                 has position start[n] + i
+ *
+ * kla_kv4_append stores k and v at their positions, kla_kv4_read writes the stored values of
+ * those positions to k and v (a prompt that is continued after cached tokens attends to them
+ * with kla_attn_fwd).  A position outside the block table, or whose page is outside
+ * [0, num_pages), is not stored and reads as zero (a negative page or start marks padding);
+ * nothing else of the cache is touched.  Two tokens of one call that share a place leave
+ * either's codes and scales, mixed: a place belongs to one token.
+ *
+ * Supported: D 64 or 128, page_size a multiple of 16 up to 2^20, either dtype; B * Hkv * T
+ * below 2^31.  Other status codes as kla_chunk_fwd.  Pointers are 16-byte aligned.
+ */
+kla_status_t kla_kv4_append(const void *k, const void *v, void *codes, void *scales,
+                            const int32_t *block_table, const int32_t *start,
+                            const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                            int num_seqs, int B, int Hkv, int T, int D,
+                            int num_pages, int page_size, int max_pages,
+                            kla_dtype_t dtype, void *stream);
+kla_status_t kla_kv4_read(void *k, void *v, const void *codes, const void *scales,
+                          const int32_t *block_table, const int32_t *start,
+                          const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                          int num_seqs, int B, int Hkv, int T, int D,
+                          int num_pages, int page_size, int max_pages,
+                          kla_dtype_t dtype, void *stream);
+
+/*
+ * kla_attn_kv4_decode_step -- softmax attention of one token per sequence over the 4-bit
+ * cache: o = softmax(scale q K^T) V, query head h reading key head h / (Hq / Hkv).
+ *
+ *   q, o        [N, Hq, D] dtype; Hq a multiple of Hkv
+ *   seq_lens    device int32 [N]: cached tokens of each sequence, the new one's among them
+ *               (append it first).  0: o is zero.
+ *   scale       finite (1 / sqrt(D) in most models)
+ *   max_len     host bound on seq_lens, which sizes the launch and the workspace; a longer
+ *               sequence is read up to max_len, and none beyond its block table
+ *   workspace   kla_attn_kv4_decode_workspace_bytes(...) bytes, as kla_chunk_fwd's
+ *
+ * Tokens on a page outside [0, num_pages) are left out.  Scores, softmax and sums are fp32;
+ * with BF16 the weights are rounded to bf16 before they meet the values (half a step of
+ * 2^-8 each, as much as o's own rounding), with F32 everything keeps 24 bits.  Results
+ * repeat bit for bit.  Supported as kla_kv4_append.
+ */
+kla_status_t kla_attn_kv4_decode_step(const void *q, const void *codes, const void *scales,
+                                      const int32_t *block_table, const int32_t *seq_lens,
+                                      float scale, void *o, int N, int Hq, int Hkv, int D,
+                                      int num_pages, int page_size, int max_pages, int max_len,
+                                      kla_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/* Device workspace of kla_attn_kv4_decode_step (host-only, no HIP call): D + 2 floats per
+ * (sequence, query head, run of tokens) where a sequence is read in several runs, else 0; 0
+ * for arguments it would reject. */
+size_t kla_attn_kv4_decode_workspace_bytes(int N, int Hq, int Hkv, int D, int max_len,
+                                           kla_dtype_t dtype);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *kla_status_str(kla_status_t s);
