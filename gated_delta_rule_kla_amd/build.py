@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkla.so")
 SOURCES = ["kla_api.cpp", "kla_decode.hip", "kla_chunk.hip", "kla_bwd.hip", "kla_general.hip", "kla_seg.hip",
-           "kla_glr.hip", "kla_kv4.hip"]
+           "kla_glr.hip", "kla_attn.hip", "kla_kv4.hip"]
 ARCH = os.environ.get("KLA_OFFLOAD_ARCH", "gfx950")
 
 

@@ -625,4 +625,36 @@ kla_status_t kla_attn_kv4_decode_step(const void *q, const void *codes, const vo
   return from_hip(kla::launch_attn_kv4_decode(a, workspace, reinterpret_cast<hipStream_t>(stream)));
 }
 
+kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float scale, void *o, float *lse,
+                          const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, const int32_t *cu_seqlens_k,
+                          const int32_t *cu_seqlens_k_host, int num_seqs, int B, int Hq, int Hkv, int Tq, int Tk, int D,
+                          kla_dtype_t dtype_, void *stream) {
+  const int dtype = raw(dtype_);
+  if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Tq < 0 || Tk < 0 || Tq > kMaxTokens || Tk > kMaxTokens ||
+      D <= 0 || num_seqs < 0)
+    return KLA_ERR_SHAPE;
+  if (!kla::attn_supported(dtype, D)) return KLA_ERR_UNSUPPORTED;
+  if ((long long)B * Hq > 0x7fffffffLL) return KLA_ERR_SHAPE;
+  if (!std::isfinite(scale)) return KLA_ERR_PARAM;
+  int longest;
+  kla_status_t st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, Tq, &longest);
+  if (st != KLA_OK) return st;
+  if ((cu_seqlens_k == nullptr) != (cu_seqlens_k_host == nullptr)) return KLA_ERR_NULL;
+  if (cu_seqlens_k != nullptr) {
+    if (cu_seqlens == nullptr) return KLA_ERR_NULL;
+    st = check_seqs(cu_seqlens_k, cu_seqlens_k_host, num_seqs, B, Tk, &longest);
+    if (st != KLA_OK) return st;
+  } else if (cu_seqlens != nullptr && Tk != Tq) {
+    return KLA_ERR_SHAPE;
+  }
+  const kla::AttnArgs a{q, k, v, o, lse, cu_seqlens, cu_seqlens_k ? cu_seqlens_k : cu_seqlens, scale, num_seqs, B, Hq,
+                        Hkv, Tq, Tk, D, dtype};
+  if (!kla::attn_grid_fits(a)) return KLA_ERR_SHAPE;
+  if (num_seqs == 0 || (long long)B * Tq == 0) return KLA_OK;
+  if (!q || !o || (Tk > 0 && (!k || !v))) return KLA_ERR_NULL;
+  if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(o) || misaligned(lse)) return KLA_ERR_ALIGN;
+  return from_hip(kla::launch_attn(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

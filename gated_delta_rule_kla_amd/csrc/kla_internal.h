@@ -170,6 +170,19 @@ size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs &a);
 bool kv4_decode_grid_fits(const Kv4DecodeArgs &a);
 hipError_t launch_attn_kv4_decode(const Kv4DecodeArgs &a, void *workspace, hipStream_t stream);
 
+// Causal attention over whole prompts (kla_attn.hip).
+struct AttnArgs {
+  const void *q, *k, *v;
+  void *o;
+  float *lse;                  // or nullptr
+  const int32_t *cu_q, *cu_k;  // device, both or neither
+  float scale;
+  int num_seqs, B, Hq, Hkv, Tq, Tk, D, dtype;
+};
+bool attn_supported(int dtype, int D);
+bool attn_grid_fits(const AttnArgs &a);
+hipError_t launch_attn(const AttnArgs &a, hipStream_t stream);
+
 // True when the backward's two state passes run side by side (64-column slices, both
 // within one round of workgroups on `cus` CUs): see kla_chunk.hip.
 bool bwd_scans_concurrent(const ChunkArgs &a, int cus);

@@ -17,7 +17,7 @@ __all__ = ["chunk_fwd", "chunk_workspace_bytes", "chunk_fwd_workspace_bytes", "p
            "pgdn_chunk_workspace_bytes",
            "GAINS", "decode_step", "gdn_chunk_fwd", "gdn_decode_step", "chunk_bwd",
            "gdn_chunk_bwd", "chunk_bwd_workspace_bytes", "glr_chunk_fwd", "glr_chunk_bwd", "glr_decode_step",
-           "glr_chunk_workspace_bytes", "kv4_append", "kv4_read", "kv4_cache", "attn_kv4_decode_step",
+           "glr_chunk_workspace_bytes", "attn_fwd", "kv4_append", "kv4_read", "kv4_cache", "attn_kv4_decode_step",
            "attn_kv4_decode_workspace_bytes", "lib", "lib_path", "KlaError", "KLA_DT_BF16",
            "KLA_DT_F32"]
 
@@ -101,6 +101,8 @@ def lib() -> ctypes.CDLL:
         L.kla_glr_chunk_workspace_bytes.restype = sz
         L.kla_glr_decode_step.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp]
         L.kla_glr_decode_step.restype = i32
+        L.kla_attn_fwd.argtypes = [vp, vp, vp, f32, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp]
+        L.kla_attn_fwd.restype = i32
         for f in (L.kla_kv4_append, L.kla_kv4_read):
             f.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp]
             f.restype = i32
@@ -770,6 +772,55 @@ def glr_decode_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
         _need(out, "out", dtype, shape, dev)
     _call("kla_glr_decode_step", dev, _ptr(x), _ptr(g), _ptr(state), _ptr(out), N, H, d, _DTYPES[dtype])
     return out
+
+
+def attn_fwd(
+    q: torch.Tensor,
+    k: torch.Tensor,
+    v: torch.Tensor,
+    scale: Optional[float] = None,
+    cu_seqlens: Optional[torch.Tensor] = None,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+    cu_seqlens_k: Optional[torch.Tensor] = None,
+    cu_seqlens_k_host: Optional[torch.Tensor] = None,
+    out: Optional[torch.Tensor] = None,
+    lse: Optional[torch.Tensor] = None,
+) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal softmax attention over whole prompts (kla_attn_fwd).
+
+    q: [B, Hq, Tq, D]; k, v: [B, Hkv, Tk, D], bf16 or fp32, Hq a multiple of Hkv; scale:
+    D ** -0.5 when None.  cu_seqlens: int32 [N + 1] packs the queries of N sequences (B must be
+    1), cu_seqlens_k their keys (None: the same offsets); the last query of a sequence sees its
+    last key.  Returns (o, lse): lse [B, Hq, Tq] fp32, the logarithm of each query's sum.
+    """
+    dev = _device_of("attn_fwd", q)
+    dtype = q.dtype
+    B, Hq, Tq, D = shape = _rank(q, "q", 4)
+    _, Hkv, Tk, _ = _rank(k, "k", 4)
+    _need(q, "q", dtype, shape, dev)
+    _need(k, "k", dtype, (B, Hkv, Tk, D), dev)
+    _need(v, "v", dtype, (B, Hkv, Tk, D), dev)
+    N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
+    if cu_seqlens_k is None:
+        if cu_seqlens_k_host is not None:
+            raise ValueError("cu_seqlens_k_host without cu_seqlens_k")
+        host_k = None
+    else:
+        Nk, host_k = _seqlens(cu_seqlens_k, cu_seqlens_k_host, B, dev)
+        if cu_seqlens is None or Nk != N:
+            raise ValueError("cu_seqlens_k needs cu_seqlens of as many sequences")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out, "out", dtype, shape, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", torch.float32, (B, Hq, Tq), dev)
+    _call("kla_attn_fwd", dev, _ptr(q), _ptr(k), _ptr(v), D ** -0.5 if scale is None else float(scale), _ptr(out),
+          _ptr(lse), _ptr(cu_seqlens), _ptr(host), _ptr(cu_seqlens_k), _ptr(host_k), N, B, Hq, Hkv, Tq, Tk, D,
+          _DTYPES[dtype])
+    return out, lse
 
 
 def kv4_cache(num_pages: int, Hkv: int, page_size: int, D: int, device) -> Tuple[torch.Tensor, torch.Tensor]:

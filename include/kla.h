@@ -521,6 +521,39 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
                                  int N, int H, int d, kla_dtype_t dtype, void *stream);
 
 /*
+ * kla_attn_fwd -- causal softmax attention over whole prompts: the quadratic mixer of stacks
+ * that mix it with the recurrent ones above.  Per sequence and query head h, with key head
+ * h / (Hq / Hkv) and off = (its keys) - (its queries):
+ *
+ *     o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j),   j <= i + off
+ *     lse_i = ln sum_j p_ij
+ *
+ * so a sequence's last query sees its last key: with as many keys as queries this is a whole
+ * prompt, with more a prompt continued after earlier keys.  A query that sees no key (off < 0)
+ * has o = 0 and lse = -inf.
+ *
+ *   q, o       [B, Hq, Tq, D]   dtype; Hq a multiple of Hkv
+ *   k, v       [B, Hkv, Tk, D]  dtype
+ *   scale      finite (1 / sqrt(D) in most models)
+ *   lse        [B, Hq, Tq] fp32, or NULL (not written)
+ *   cu_seqlens, cu_seqlens_host, num_seqs (N), B, Tq: the queries' sequences, as kla_chunk_fwd's
+ *   cu_seqlens_k, cu_seqlens_k_host  the keys' (N + 1 offsets to Tk), for packed sequences
+ *              only; NULL: the queries' offsets (Tk = Tq).  Dense batches: Tq queries and Tk
+ *              keys in every row.
+ *
+ * Supported: D 64 or 128, either dtype.  Scores, softmax and sums are fp32; with BF16 the
+ * weights are rounded to bf16 before they meet the values (half a step of 2^-8 each, as much
+ * as o's own rounding).  Keys and values that a query does not see do not reach it, also
+ * where they are infinite or NaN.  No workspace; results repeat bit for bit.  Status codes as
+ * kla_chunk_fwd, KLA_ERR_PARAM for a scale that is not finite.
+ */
+kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float scale, void *o, float *lse,
+                          const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                          const int32_t *cu_seqlens_k, const int32_t *cu_seqlens_k_host,
+                          int num_seqs, int B, int Hq, int Hkv, int Tq, int Tk, int D,
+                          kla_dtype_t dtype, void *stream);
+
+/*
  * kla_kv4_append, kla_kv4_read -- a paged key/value cache held in 4 bits, for the softmax
  * attention layers that stand between recurrent ones.
  *

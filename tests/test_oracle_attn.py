@@ -135,3 +135,29 @@ def test_decode_workspace():
     one = kla.attn_kv4_decode_workspace_bytes(1, 16, 2, 128, 131072)
     assert one > 0 and one % (16 * 130 * 4) == 0
     assert kla.attn_kv4_decode_workspace_bytes(1, 15, 2, 128, 131072) == 0
+
+
+def attn(**kw):
+    a = dict(q=FAKE, k=FAKE, lse=FAKE, scale=0.1, cu=None, cuh=None, ck=None, ckh=None, N=2, B=2, Hq=8, Hkv=4, Tq=10,
+             Tk=10, D=128, dtype=0)
+    a.update(kw)
+    host = [None if x is None else (ctypes.c_int32 * len(x))(*x) for x in (a["cuh"], a["ckh"])]
+    at = [None if x is None else ctypes.addressof(x) for x in host]
+    return kla.lib().kla_attn_fwd(a["q"], a["k"], FAKE, a["scale"], FAKE, a["lse"], a["cu"], at[0], a["ck"], at[1],
+                                  a["N"], a["B"], a["Hq"], a["Hkv"], a["Tq"], a["Tk"], a["D"], a["dtype"], None)
+
+
+@built
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=2), -3), (dict(B=-1, N=-1), -2), (dict(Hq=6), -2), (dict(Hkv=0), -2), (dict(Tq=-1), -2),
+    (dict(Tk=-1), -2), (dict(Tk=0x7fffffff), -2), (dict(N=3), -2), (dict(D=0), -2), (dict(D=80), -4),
+    (dict(B=1 << 20, N=1 << 20, Hq=1 << 12), -2), (dict(B=1 << 15, N=1 << 15, Hq=1 << 15, Tq=1 << 20), -2),
+    (dict(scale=float("nan")), -11), (dict(q=None), -1), (dict(k=None), -1), (dict(q=FAKE + 8), -8),
+    (dict(lse=FAKE + 4), -8), (dict(cu=FAKE, cuh=[0, 4, 10]), -2), (dict(cu=FAKE, cuh=[0, 4, 9], B=1), -5),
+    (dict(cu=FAKE, cuh=[0, 4, 10], B=1, Tk=11), -2), (dict(cu=FAKE, cuh=[0, 4, 10], ck=FAKE, B=1), -1),
+    (dict(cu=FAKE, cuh=[0, 4, 10], ck=FAKE, ckh=[0, 4, 11], B=1), -5), (dict(ck=FAKE, ckh=[0, 4, 10]), -1),
+    (dict(cu=FAKE, cuh=[0, 4, 10], ck=FAKE + 2, ckh=[0, 4, 10], B=1), -8), (dict(Tq=0, q=None), 0),
+    (dict(B=0, N=0), 0),
+])
+def test_attn_refusals(kw, status):
+    assert attn(**kw) == status
