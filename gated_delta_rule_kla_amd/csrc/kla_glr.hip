@@ -10,18 +10,26 @@
 // that depends on the sizes alone, so results repeat bit for bit.
 //
 // The forward reads x and g and writes o once (6 bytes per element in bf16), the backward
-// reads g, o and do and writes dx and dg: both are bound by HBM.  One workgroup owns a
-// slice of CG * V channels of one (sequence, head) and walks its tokens in tiles of
-// RG * R rows: thread (row group rg, channel group cg) holds R consecutive rows of V
-// channels (16-byte loads, the next tile's in flight while this one is computed), composes
-// them, a shuffle scan composes the row groups of a wave, and the waves' maps meet in LDS,
-// one barrier per tile.  Every byte is read once and no workgroup waits for another.
+// reads g, o and do and writes dx and dg (10 bytes): both are bound by HBM.  One workgroup of
+// eight waves owns a slice of 64 (or 32) bytes of the rows of one (sequence, head) and walks
+// its tokens in tiles of 512 (1,024) rows, the next tile's 16-byte loads in flight in
+// registers.  A tile goes through LDS from the loads' order (consecutive lanes along a row) to
+// the scan's (lane = 16 channel groups' row groups): each lane composes R consecutive rows of V
+// channels, DPP row shifts compose the 16 row groups of a wave (two instructions a step and
+// channel), the waves' maps meet in LDS behind the one barrier of a tile, and the outputs go
+// back through LDS into whole row pieces.  Every byte is read once and no workgroup waits for
+// another.  Measured on B=4 H=16 T=4096 d=128: forward 46 us (4.4 TB/s; a copy of 1 GiB
+// reaches 5.2), 32 packed sequences of 268 M elements backward 613 us (4.4 TB/s); a first form
+// with the scan's steps as lane shuffles in the loads' order took 56 and 790 us.
 //
-// Where few channels leave most CUs idle, sequences are cut into segments (SEG): a first
-// pass forms each segment's map, and the second starts every segment from the maps of those
-// before it; it reads x and g twice.
+// Where few channels leave most CUs idle, sequences are cut into segments: a first pass forms
+// each segment's map, and the second starts every segment from the maps of those before it; it
+// reads x and g twice (glr_plan has the rule).
+#include <algorithm>
+
 #include "kla_common.h"
 #include "kla_internal.h"
+#include "kla_ops.h"
 
 namespace kla {
 
@@ -36,8 +44,8 @@ struct GlrParams {
   float *yend;               // [N,H,d] end of the scan (final state / dinitial), or nullptr
   const int32_t *cu;         // device, or nullptr (dense)
   int N, H, T, d;
-  int slices;                // channel slices of a head
-  int segs, seg_rows;        // segments of a sequence at most, tokens in one
+  int lines, inner;          // 128-byte lines of a head's channels, slices of one
+  int segs, nseg, seg_rows;  // segments of a sequence at most, of this launch, tokens in one
   float *maps;               // [N,H,segs,2,d]: the segments' maps (A then C)
 };
 
@@ -50,16 +58,11 @@ template <typename E, int V>
 struct Vec {
   E v[V];
 };
+// V elements at a multiple of their size (V divides d)
 template <typename E, int V>
 __device__ __forceinline__ Vec<E, V> ld(const E *p) {
   Vec<E, V> r;
-  if constexpr (V * sizeof(E) == 16) {
-    const uint4 u = ldg16(p);
-    __builtin_memcpy(&r, &u, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = p[i];
-  }
+  __builtin_memcpy(&r, __builtin_assume_aligned(p, V * sizeof(E)), V * sizeof(E));
   return r;
 }
 template <typename E, int V>
@@ -67,34 +70,71 @@ __device__ __forceinline__ void st(E *p, const float *f) {
   Vec<E, V> r;
 #pragma unroll
   for (int i = 0; i < V; ++i) r.v[i] = Elem<E>::from_f32(f[i]);
-  if constexpr (V * sizeof(E) == 16) {
-    uint4 u;
-    __builtin_memcpy(&u, &r, 16);
-    stg16(p, u);
+  __builtin_memcpy(__builtin_assume_aligned(p, V * sizeof(E)), &r, V * sizeof(E));
+}
+
+// V floats; V > 1 divides d, so rows of floats are 16-byte aligned
+template <int V>
+__device__ __forceinline__ void ldf(float *r, const float *p) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *reinterpret_cast<f32x4 *>(r + i) = *reinterpret_cast<const f32x4 *>(p + i);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = r.v[i];
+    for (int i = 0; i < V; ++i) r[i] = p[i];
   }
 }
 
 enum { GLR_WHOLE = 0, GLR_MAPS = 1, GLR_CARRIED = 2 };
 
-template <typename E, int V, int CG, int NW, int R, bool BWD, int MODE>
-__global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
-  constexpr int GW = 64 / CG;       // row groups of a wave
-  constexpr int ROWS = NW * GW * R; // rows of a tile
-  constexpr int CW = CG * V;
-  __shared__ float s_map[2][NW][2][CW];
+// v of the lane S before this one in its row of 16; the row's first S lanes keep `old`.
+template <int S>
+__device__ __forceinline__ float row_shr(float old, float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v),
+                                                               0x110 + S, 0xF, 0xF, false));
+}
+template <int S, int V>
+__device__ __forceinline__ void scan_step(float *A, float *C) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    // the map S lanes before, then this one; in front of the row's first lanes the identity
+    C[i] = fmaf(row_shr<S>(0.f, C[i]), A[i], C[i]);
+    A[i] = row_shr<S>(1.f, A[i]) * A[i];
+  }
+}
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int cg = lane % CG, gw = lane / CG;
-  // workgroups: slice fastest, then head and sequence; segments slowest
-  unsigned b = blockIdx.x;
-  const int slice = b % p.slices;
-  b /= p.slices;
+// LDS of a workgroup: per wave its rows of the tensors it reads, and a row set on its way out.
+template <typename E, int V, int NW, int R, bool BWD, int MODE, bool PIECES>
+struct GlrLds {
+  static constexpr int CG = 4, CW = CG * V;
+  static constexpr int NT = BWD && MODE != GLR_MAPS ? 3 : 2;
+  static constexpr int ROWB = CW * (int)sizeof(E), P = 64 / (ROWB < 64 ? ROWB : 64);  // row sets to 1 KB
+  static constexpr int STAGE = PIECES ? R * 16 * ROWB : 16;
+  float map[2][NW][2][CW], carry[2][2][CW];
+  __attribute__((aligned(1024))) char in[NW][NT][STAGE];
+  __attribute__((aligned(1024))) char out[NW][BWD ? 2 : 1][PIECES ? 1024 : 16];
+};
+
+template <typename E, int V, int NW, int R, bool BWD, int MODE, bool PIECES>
+__global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
+  using Lds = GlrLds<E, V, NW, R, BWD, MODE, PIECES>;
+  constexpr int CG = 4, GW = 16;      // channel groups; row groups of a wave
+  constexpr int ROWS = NW * GW * R;   // rows of a tile
+  constexpr int CW = CG * V, P = Lds::P, NT = Lds::NT;
+  constexpr bool HV = NT == 3;
+  __shared__ Lds s;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int cg = lane >> 4, gw = lane & 15;
+  // workgroups go round the eight XCDs: the slices of one 128-byte line stay on one, side by
+  // side in time, so that its L2 reads the line once
+  const unsigned u = blockIdx.x / (8 * p.inner) * 8 + blockIdx.x % 8, in = blockIdx.x / 8 % p.inner;
+  unsigned b = u / p.lines;
+  const int slice = (u % p.lines) * p.inner + in;
   const int head = b % p.H;
   b /= p.H;
   const int seq = b % p.N, seg = b / p.N;
+  if (seg >= p.nseg || slice * CW >= p.d) return;
 
   // the tokens of this sequence (device cu_seqlens clamped to [0, T]), then of the segment
   int t0 = 0, t1 = p.T;
@@ -131,136 +171,223 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
     for (int i = 0; i < V; ++i) start[i] = p.y0 ? p.y0[sh + i] : 0.f;
   }
   if (MODE == GLR_CARRIED) {
+    ldf<V>(carry, start);
+#pragma unroll 4
+    for (int q = 0; q < seg; ++q) {
+      float ma[V], mc[V];
+      ldf<V>(ma, p.maps + mrow + (size_t)q * 2 * p.d);
+      ldf<V>(mc, p.maps + mrow + (size_t)q * 2 * p.d + p.d);
 #pragma unroll
-    for (int i = 0; i < V; ++i) carry[i] = start[i];
-    for (int s = 0; s < seg; ++s) {
-      const float *m = p.maps + mrow + (size_t)s * 2 * p.d;
-#pragma unroll
-      for (int i = 0; i < V; ++i) carry[i] = fmaf(m[i], carry[i], m[p.d + i]);
+      for (int i = 0; i < V; ++i) carry[i] = fmaf(ma[i], carry[i], mc[i]);
     }
   }
 
-  // scan step j of the segment is token t0 + skip + j, backwards t1 - 1 - skip - j
-  const E *px = (const E *)p.x + (row0 + (BWD ? t1 - 1 - skip : t0 + skip)) * p.d + cc;
-  const E *pg = (const E *)p.g + (row0 + (BWD ? t1 - 1 - skip : t0 + skip)) * p.d + cc;
-  const E *ph = BWD ? (const E *)p.h + (row0 + (t1 - 1 - skip)) * p.d + cc : nullptr;
-  const long long step = BWD ? -(long long)p.d : p.d;
+  // Scan step j of the segment is token t0 + skip + j, backwards t1 - 1 - skip - j.  A tile's n
+  // steps from base are the n rows from token `low` on, row k of them being step k, backwards
+  // n - 1 - k.
+  const int pitch = p.d * (int)sizeof(E);
+  auto low = [&](int base, int n) { return BWD ? t1 - skip - base - n : t0 + skip + base; };
+  // PIECES: this lane's 16 bytes of a row, row set and row group (P row sets to a load)
+  constexpr int LPR = PIECES ? Lds::ROWB / 16 : 1;
+  const int piece = lane % LPR, slot = lane / LPR, dgw = slot % 16, dr = slot / 16;
+  const int dc = slice * CW + piece * (16 / (int)sizeof(E));
+  const bool dlive = dc < p.d;
+  const unsigned dcol = (dlive ? dc : 0) * (unsigned)sizeof(E);
+  const int dj = (wave * GW + dgw) * R + dr, j0 = (wave * GW + gw) * R;
 
-  Vec<E, V> nx[R], ng[R], nh[BWD && MODE != GLR_MAPS ? R : 1];
-  const int j0 = (wave * GW + gw) * R;  // this thread's first step in a tile
-  auto load = [&](int base) {
+  // the next tile
+  uint4 pre[NT][PIECES ? R / P : 1];
+  Vec<E, V> nx[R], ng[R], nh[HV ? R : 1];  // not PIECES
+  auto fetch = [&](int base) {
+    const int n = min(ROWS, len - base), lo = low(base, n);
+    const size_t first = (row0 + lo) * p.d;
+    const int back = BWD && lo > t0 ? 0 : 1;  // h_{t-1} is a row up, where the sequence has one
+    if constexpr (PIECES) {
+      const E *x = (const E *)p.x + first, *g = (const E *)p.g + first;
+      const E *h = HV ? (const E *)p.h + first - (back ? 0 : p.d) : nullptr;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int j = min(base + j0 + r, len - 1);  // rows past the end repeat the last one
-      nx[r] = ld<E, V>(px + j * step);
-      ng[r] = ld<E, V>(pg + j * step);
-      if constexpr (BWD && MODE != GLR_MAPS) {
-        // h_{t-1}: the output of the token before, which the sequence's first does not have
-        const int jh = min(skip + j + 1, len_seq - 1) - skip;
-        nh[r] = ld<E, V>(ph + jh * step);
+      for (int i = 0; i < R / P; ++i) {
+        const int j = min(dj + i * P, n - 1), k = BWD ? n - 1 - j : j;  // past the end: the last
+        const unsigned off = (unsigned)k * pitch + dcol;
+        pre[0][i] = ldg16((const char *)x + off);
+        pre[1][i] = ldg16((const char *)g + off);
+        if constexpr (HV) pre[2][i] = ldg16((const char *)h + ((unsigned)max(k - back, 0) * pitch + dcol));
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int j = min(j0 + r, n - 1), k = BWD ? n - 1 - j : j;
+        const size_t at = first + (size_t)k * p.d + cc;
+        nx[r] = ld<E, V>((const E *)p.x + at);
+        ng[r] = ld<E, V>((const E *)p.g + at);
+        if constexpr (HV) nh[r] = ld<E, V>((const E *)p.h + at - (k > 0 || !back ? p.d : 0));
       }
     }
   };
-  if (len > 0) load(0);
+  // this lane's row r of a tensor in the stage
+  auto staged = [&](int t, int r) {
+    return s.in[wave][t] + (r / P) * 1024 + ((r % P) * 16 + gw) * Lds::ROWB + cg * V * (int)sizeof(E);
+  };
+  if (len > 0) fetch(0);
 
   int buf = 0;
   for (int base = 0; base < len; base += ROWS, buf ^= 1) {
-    float a[R][V], x[R][V];
-    Vec<E, V> hv[BWD && MODE != GLR_MAPS ? R : 1];
+    float a[R][V];
+    Vec<E, V> xv[R], hv[HV ? R : 1];
+    const int left = len - base - j0;
+    if constexpr (PIECES) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool in = base + j0 + r < len;
+      for (int i = 0; i < R / P; ++i)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        a[r][i] = in ? decay(Elem<E>::to_f32(ng[r].v[i]), (const E *)nullptr) : 1.f;
-        x[r][i] = in ? Elem<E>::to_f32(nx[r].v[i]) : 0.f;
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<uint4 *>(s.in[wave][t] + 1024 * i + 16 * lane) = pre[t][i];
+      Vec<E, V> gv[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        __builtin_memcpy(&xv[r], __builtin_assume_aligned(staged(0, r), V * sizeof(E)), V * sizeof(E));
+        __builtin_memcpy(&gv[r], __builtin_assume_aligned(staged(1, r), V * sizeof(E)), V * sizeof(E));
+        if constexpr (HV) __builtin_memcpy(&hv[r], __builtin_assume_aligned(staged(2, r), V * sizeof(E)), V * sizeof(E));
       }
-      if constexpr (BWD && MODE != GLR_MAPS) hv[r] = nh[r];
+      if (base + ROWS < len) fetch(base + ROWS);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[r][i] = decay(Elem<E>::to_f32(gv[r].v[i]), (const E *)nullptr);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        xv[r] = nx[r];
+        if constexpr (HV) hv[r] = nh[r];
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[r][i] = decay(Elem<E>::to_f32(ng[r].v[i]), (const E *)nullptr);
+      }
+      if (base + ROWS < len) fetch(base + ROWS);
     }
-    if (base + ROWS < len) load(base + ROWS);
+    const bool full = base + ROWS <= len;
+    if (!full) {
+      // rows past the end: the identity
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (r >= left) {
+            a[r][i] = 1.f;
+            xv[r].v[i] = Elem<E>::from_f32(0.f);
+          }
+        }
+    }
 
-    // this thread's rows as one map
+    // this thread's rows as one map, then all maps of the wave up to it
     float A[V], C[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      A[i] = 1.f;
-      C[i] = 0.f;
+      A[i] = a[0][i];
+      C[i] = BWD ? a[0][i] * Elem<E>::to_f32(xv[0].v[i]) : Elem<E>::to_f32(xv[0].v[i]);
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 1; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        C[i] = BWD ? a[r][i] * (C[i] + x[r][i]) : fmaf(a[r][i], C[i], x[r][i]);
+        const float x = Elem<E>::to_f32(xv[r].v[i]);
+        C[i] = BWD ? a[r][i] * (C[i] + x) : fmaf(a[r][i], C[i], x);
         A[i] *= a[r][i];
       }
-    // inclusive scan over the wave's row groups
-#pragma unroll
-    for (int s = 1; s < GW; s <<= 1)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float pa = __shfl_up(A[i], s * CG), pc = __shfl_up(C[i], s * CG);
-        if (gw >= s) {
-          C[i] = fmaf(A[i], pc, C[i]);
-          A[i] *= pa;
-        }
-      }
+    scan_step<1, V>(A, C);
+    scan_step<2, V>(A, C);
+    scan_step<4, V>(A, C);
+    scan_step<8, V>(A, C);
     if (gw == GW - 1) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s_map[buf][wave][0][cg * V + i] = A[i];
-        s_map[buf][wave][1][cg * V + i] = C[i];
+        s.map[buf][wave][0][cg * V + i] = A[i];
+        s.map[buf][wave][1][cg * V + i] = C[i];
       }
     }
-    __syncthreads();
-    // the value before this wave, and before the next tile (two buffers: a wave can be at
-    // most one barrier ahead of another)
+    lds_barrier();
+    // the value before this wave; the last wave's goes on to the next tile (two buffers: a wave
+    // is at most one barrier ahead of another)
     float y[V];
+    if (MODE != GLR_MAPS || wave == NW - 1) {
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
+      for (int i = 0; i < V; ++i) y[i] = base == 0 ? carry[i] : s.carry[buf][0][cg * V + i];
+      if (MODE == GLR_MAPS && base > 0) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (w == wave) y[i] = carry[i];
-        const float ma = s_map[buf][w][0][cg * V + i], mc = s_map[buf][w][1][cg * V + i];
-        carry[i] = fmaf(ma, carry[i], mc);
-        if (MODE == GLR_MAPS) total[i] *= ma;
+        for (int i = 0; i < V; ++i) total[i] = s.carry[buf][1][cg * V + i];
+      }
+#pragma unroll
+      for (int w = 0; w < NW - 1; ++w) {
+        if (w < wave) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float ma = s.map[buf][w][0][cg * V + i];
+            y[i] = fmaf(ma, y[i], s.map[buf][w][1][cg * V + i]);
+            if (MODE == GLR_MAPS) total[i] *= ma;
+          }
+        }
+      }
+      if (wave == NW - 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          carry[i] = fmaf(A[i], y[i], C[i]);
+          if (MODE == GLR_MAPS) total[i] *= A[i];
+          if (gw == GW - 1) {
+            s.carry[buf ^ 1][0][cg * V + i] = carry[i];
+            if (MODE == GLR_MAPS) s.carry[buf ^ 1][1][cg * V + i] = total[i];
+          }
+        }
       }
     }
     if constexpr (MODE != GLR_MAPS) {
       // the value before this thread's rows
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float pa = __shfl_up(A[i], CG), pc = __shfl_up(C[i], CG);
-        if (gw > 0) y[i] = fmaf(pa, y[i], pc);
-      }
+      for (int i = 0; i < V; ++i) y[i] = fmaf(row_shr<1>(1.f, A[i]), y[i], row_shr<1>(0.f, C[i]));
+      const int n = min(ROWS, len - base);
+      const size_t first = (row0 + low(base, n)) * p.d;
+      // rows r of all lanes: through LDS into whole rows (PIECES), or each lane its own piece
+      auto put = [&](E *dst, int t, int r, const float *f) {
+        if constexpr (PIECES) {
+          Vec<E, V> w;
+#pragma unroll
+          for (int i = 0; i < V; ++i) w.v[i] = Elem<E>::from_f32(f[i]);
+          char *at = s.out[wave][t] + ((r % P) * 16 + gw) * Lds::ROWB + cg * V * (int)sizeof(E);
+          __builtin_memcpy(__builtin_assume_aligned(at, V * sizeof(E)), &w, V * sizeof(E));
+          if (r % P == P - 1) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(s.out[wave][t] + 16 * lane);
+            const int j = dj + r / P * P, k = BWD ? n - 1 - j : j;
+            if (full ? dlive : dlive && j < n) stg16((char *)(dst + first) + (unsigned)k * (size_t)pitch + dcol, q);
+          }
+        } else {
+          const int j = j0 + r, k = BWD ? n - 1 - j : j;
+          if (live && r < left) st<E, V>(dst + first + (size_t)k * p.d + cc, f);
+        }
+      };
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int j = base + j0 + r;
         float out[V], dg[V];
         if constexpr (BWD) {
-          const bool first = skip + j + 1 >= len_seq;  // the sequence's first token: h_{t-1} = h0
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            out[i] = y[i] + x[r][i];
+            out[i] = y[i] + Elem<E>::to_f32(xv[r].v[i]);
             y[i] = a[r][i] * out[i];
-            const float hp = first ? (p.h0 ? p.h0[sh + i] : 0.f) : Elem<E>::to_f32(hv[r].v[i]);
-            dg[i] = y[i] * hp;
+            dg[i] = y[i] * Elem<E>::to_f32(hv[r].v[i]);
+          }
+          if (skip + base + j0 + r + 1 == len_seq) {  // the sequence's first token: h_{t-1} = h0
+#pragma unroll
+            for (int i = 0; i < V; ++i) dg[i] = y[i] * (p.h0 ? p.h0[sh + i] : 0.f);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            y[i] = fmaf(a[r][i], y[i], x[r][i]);
+            y[i] = fmaf(a[r][i], y[i], Elem<E>::to_f32(xv[r].v[i]));
             out[i] = y[i];
           }
         }
-        if (live && j < len) {
-          const size_t at = (row0 + (BWD ? t1 - 1 - skip - j : t0 + skip + j)) * p.d + c;
-          st<E, V>((E *)p.o + at, out);
-          if constexpr (BWD) st<E, V>((E *)p.dg + at, dg);
-        }
+        put((E *)p.o, 0, r, out);
+        if constexpr (BWD) put((E *)p.dg, 1, r, dg);
       }
     }
   }
-  if (!live || wave || gw) return;
+  if (!live || wave != NW - 1 || gw != GW - 1) return;
+  // where there was no token, carry is what the segment started from
   if (MODE == GLR_MAPS) {
     float *m = p.maps + mrow + (size_t)seg * 2 * p.d;
 #pragma unroll
@@ -299,57 +426,89 @@ __global__ __launch_bounds__(256) void kla_glr_step_kernel(const E *__restrict__
   st<E, V>(o + i, h);
 }
 
-template <typename E, int V, int CG, int NW, int R, bool BWD>
+template <typename E, int V, int NW, int R, bool BWD, bool PIECES>
 struct GlrShape {
-  static constexpr int ROWS = NW * (64 / CG) * R, CW = CG * V;
-  static long long slices(int d) { return (d + CW - 1) / CW; }
-  static hipError_t launch(GlrParams p, long long segs, hipStream_t st) {
-    p.slices = (int)slices(p.d);
-    const long long grid = (long long)p.N * p.H * p.slices;
+  static constexpr int ROWS = NW * 16 * R, CW = 4 * V;
+  static constexpr int INNER = 128 / (CW * (int)sizeof(E)) > 1 ? 128 / (CW * (int)sizeof(E)) : 1;
+  template <int MODE>
+  static void go(GlrParams p, long long segs, hipStream_t st) {
+    p.nseg = (int)segs;
+    p.inner = INNER;
+    p.lines = (p.d + CW * p.inner - 1) / (CW * p.inner);
+    const long long units = (long long)p.N * p.H * p.lines * segs;
+    const long long grid = (units + 7) / 8 * 8 * p.inner;
+    hipLaunchKernelGGL((kla_glr_kernel<E, V, NW, R, BWD, MODE, PIECES>), dim3((unsigned)grid), dim3(64 * NW), 0, st, p);
+  }
+  static hipError_t launch(const GlrParams &p, long long segs, hipStream_t st) {
     if (segs <= 1) {
-      hipLaunchKernelGGL((kla_glr_kernel<E, V, CG, NW, R, BWD, GLR_WHOLE>), dim3((unsigned)grid), dim3(64 * NW), 0, st, p);
+      go<GLR_WHOLE>(p, 1, st);
     } else {
-      // the last segment's map is not needed
-      hipLaunchKernelGGL((kla_glr_kernel<E, V, CG, NW, R, BWD, GLR_MAPS>), dim3((unsigned)(grid * (segs - 1))),
-                         dim3(64 * NW), 0, st, p);
-      hipLaunchKernelGGL((kla_glr_kernel<E, V, CG, NW, R, BWD, GLR_CARRIED>), dim3((unsigned)(grid * segs)), dim3(64 * NW),
-                         0, st, p);
+      go<GLR_MAPS>(p, segs - 1, st);  // the last segment's map is not needed
+      go<GLR_CARRIED>(p, segs, st);
     }
     return hipGetLastError();
   }
 };
 
-constexpr int GLR_SEG_ROWS = 1024;  // a multiple of every shape's tile rows
+// How a call runs: slices of 64 or 32 bytes of a row, sequences whole or in segments.
+//
+// A CU keeps a limited number of lines in flight (about 21 GB/s where it takes 64 bytes of
+// each, half that at 32), so it takes all 256 CUs to fill HBM's rate.  Slices of 64 bytes where
+// they make 256 workgroups (8,192 channels, T = 4096: 46 us against 59 with 32 bytes); slices
+// of 32 where that makes them 256 (4,096 channels, T = 65536: 442 us against 595, and 575 with
+// segments, which read x and g twice); segments below (2,048 channels, T = 32768: 148 us
+// against 181 with 32 bytes and 273 whole; 256 channels, T = 65536: 44 against 222 and 444).
+// Short sequences do not pay for a second pass (512 channels, 3,000 tokens: 15 us with 32
+// bytes, 19 with segments), nor for tiles of 1,024 rows (5,000 channels, 1,500 tokens: 19 us
+// whole, 25 with 32 bytes).
+struct GlrPlan {
+  bool pieces, narrow;
+  int segs, seg_rows;
+};
+
+GlrPlan glr_plan(const GlrArgs &a) {
+  const int e = a.dtype == 0 ? 2 : 4;
+  // rows of 16-byte pieces whose tile offsets fit 32 bits; others element by element
+  const bool pieces = a.d * (long long)e % 16 == 0 && (long long)a.d * e <= (1 << 20);
+  const int V = pieces ? 16 / e : (a.d % (8 / e) == 0 ? 8 / e : 1);
+  const long long wide = (long long)a.num_seqs * a.H * ((a.d + 4 * V - 1) / (4 * V));
+  GlrPlan r{pieces, false, 1, 0};
+  if (wide >= 256 || a.longest <= 2048) return r;
+  if (pieces && (wide >= 128 || a.longest <= 3584)) {
+    r.narrow = true;
+    return r;
+  }
+  const long long want = std::min<long long>((256 + wide - 1) / wide, (a.longest + 511) / 512);
+  const long long rows = ((a.longest + want - 1) / want + 511) / 512 * 512;
+  r.seg_rows = (int)rows;
+  r.segs = (int)((a.longest + rows - 1) / rows);
+  return r;
+}
 
 template <typename E, bool BWD>
-hipError_t launch_glr(const GlrParams &p, long long segs, hipStream_t st) {
+hipError_t launch_glr(const GlrParams &p, const GlrPlan &plan, hipStream_t st) {
   constexpr int V = 16 / sizeof(E);
-  if (p.d % V == 0) return GlrShape<E, V, 4, 4, 4, BWD>::launch(p, segs, st);
-  return GlrShape<E, 1, 16, 4, 4, BWD>::launch(p, segs, st);
+  if (plan.pieces)
+    return plan.narrow ? GlrShape<E, V / 2, 8, 8, BWD, true>::launch(p, plan.segs, st)
+                       : GlrShape<E, V, 8, 4, BWD, true>::launch(p, plan.segs, st);
+  if (p.d % (V / 2) == 0) return GlrShape<E, V / 2, 8, 4, BWD, false>::launch(p, plan.segs, st);
+  return GlrShape<E, 1, 8, 4, BWD, false>::launch(p, plan.segs, st);
 }
 
 }  // namespace
 
-// Workgroups of one segment, and segments of the longest sequence: 1 unless few channels
-// leave CUs idle.
-static long long glr_groups(const GlrArgs &a) {
-  const int V = a.dtype == 0 ? 8 : 4;
-  const long long cw = a.d % V == 0 ? 4 * V : 16;
-  return (long long)a.num_seqs * a.H * ((a.d + cw - 1) / cw);
+bool glr_grid_fits(const GlrArgs &a) {
+  // slices of 4 channels at least, in groups of up to 32, over a multiple of 8 groups
+  return ((double)a.num_seqs * a.H * (a.d / 4 + 33.0) + 8) * glr_plan(a).segs <= 0x7fffffff;
 }
-static long long glr_segments(const GlrArgs &a) {
-  const long long segs = ((long long)a.longest + GLR_SEG_ROWS - 1) / GLR_SEG_ROWS;
-  return glr_groups(a) >= 256 || segs < 2 ? 1 : segs;
-}
-
-bool glr_grid_fits(const GlrArgs &a) { return glr_groups(a) * glr_segments(a) <= 0x7fffffffLL; }
 
 size_t glr_workspace_bytes(const GlrArgs &a) {
-  const long long segs = glr_segments(a);
+  const long long segs = glr_plan(a).segs;
   return segs <= 1 ? 0 : (size_t)a.num_seqs * a.H * segs * 2 * a.d * sizeof(float);
 }
 
 hipError_t launch_glr_chunk(const GlrArgs &a, bool bwd, hipStream_t st) {
+  const GlrPlan plan = glr_plan(a);
   GlrParams p{};
   p.x = a.x;
   p.g = a.g;
@@ -364,12 +523,11 @@ hipError_t launch_glr_chunk(const GlrArgs &a, bool bwd, hipStream_t st) {
   p.H = a.H;
   p.T = a.T;
   p.d = a.d;
-  const long long segs = glr_segments(a);
-  p.segs = (int)segs;
-  p.seg_rows = GLR_SEG_ROWS;
+  p.segs = plan.segs;
+  p.seg_rows = plan.seg_rows;
   p.maps = (float *)a.workspace;
-  if (a.dtype == 0) return bwd ? launch_glr<bf16, true>(p, segs, st) : launch_glr<bf16, false>(p, segs, st);
-  return bwd ? launch_glr<float, true>(p, segs, st) : launch_glr<float, false>(p, segs, st);
+  if (a.dtype == 0) return bwd ? launch_glr<bf16, true>(p, plan, st) : launch_glr<bf16, false>(p, plan, st);
+  return bwd ? launch_glr<float, true>(p, plan, st) : launch_glr<float, false>(p, plan, st);
 }
 
 template <typename E>
