@@ -228,73 +228,81 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
   auto staged = [&](int t, int r) {
     return s.in[wave][t] + (r / P) * 1024 + ((r % P) * 16 + gw) * Lds::ROWB + cg * V * (int)sizeof(E);
   };
-  if (len > 0) fetch(0);
+  // a wave has rows in the tile from base on (all of them but in a sequence's last tile)
+  const int w0 = wave * GW * R;
+  if (w0 < len) fetch(0);
 
   int buf = 0;
   for (int base = 0; base < len; base += ROWS, buf ^= 1) {
-    float a[R][V];
+    float a[R][V], A[V], C[V];
     Vec<E, V> xv[R], hv[HV ? R : 1];
     const int left = len - base - j0;
-    if constexpr (PIECES) {
-#pragma unroll
-      for (int i = 0; i < R / P; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<uint4 *>(s.in[wave][t] + 1024 * i + 16 * lane) = pre[t][i];
-      Vec<E, V> gv[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        __builtin_memcpy(&xv[r], __builtin_assume_aligned(staged(0, r), V * sizeof(E)), V * sizeof(E));
-        __builtin_memcpy(&gv[r], __builtin_assume_aligned(staged(1, r), V * sizeof(E)), V * sizeof(E));
-        if constexpr (HV) __builtin_memcpy(&hv[r], __builtin_assume_aligned(staged(2, r), V * sizeof(E)), V * sizeof(E));
-      }
-      if (base + ROWS < len) fetch(base + ROWS);
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[r][i] = decay(Elem<E>::to_f32(gv[r].v[i]), (const E *)nullptr);
-    } else {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        xv[r] = nx[r];
-        if constexpr (HV) hv[r] = nh[r];
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[r][i] = decay(Elem<E>::to_f32(ng[r].v[i]), (const E *)nullptr);
-      }
-      if (base + ROWS < len) fetch(base + ROWS);
-    }
     const bool full = base + ROWS <= len;
-    if (!full) {
-      // rows past the end: the identity
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (r >= left) {
-            a[r][i] = 1.f;
-            xv[r].v[i] = Elem<E>::from_f32(0.f);
-          }
-        }
-    }
-
-    // this thread's rows as one map, then all maps of the wave up to it
-    float A[V], C[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      A[i] = a[0][i];
-      C[i] = BWD ? a[0][i] * Elem<E>::to_f32(xv[0].v[i]) : Elem<E>::to_f32(xv[0].v[i]);
+      A[i] = 1.f;
+      C[i] = 0.f;
     }
+    if (base + w0 < len) {
+      if constexpr (PIECES) {
 #pragma unroll
-    for (int r = 1; r < R; ++r)
+        for (int i = 0; i < R / P; ++i)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) *reinterpret_cast<uint4 *>(s.in[wave][t] + 1024 * i + 16 * lane) = pre[t][i];
+        Vec<E, V> gv[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          __builtin_memcpy(&xv[r], __builtin_assume_aligned(staged(0, r), V * sizeof(E)), V * sizeof(E));
+          __builtin_memcpy(&gv[r], __builtin_assume_aligned(staged(1, r), V * sizeof(E)), V * sizeof(E));
+          if constexpr (HV) __builtin_memcpy(&hv[r], __builtin_assume_aligned(staged(2, r), V * sizeof(E)), V * sizeof(E));
+        }
+        if (base + ROWS + w0 < len) fetch(base + ROWS);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < V; ++i) a[r][i] = decay(Elem<E>::to_f32(gv[r].v[i]), (const E *)nullptr);
+      } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          xv[r] = nx[r];
+          if constexpr (HV) hv[r] = nh[r];
+#pragma unroll
+          for (int i = 0; i < V; ++i) a[r][i] = decay(Elem<E>::to_f32(ng[r].v[i]), (const E *)nullptr);
+        }
+        if (base + ROWS + w0 < len) fetch(base + ROWS);
+      }
+      if (!full) {
+        // rows past the end: the identity
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (r >= left) {
+              a[r][i] = 1.f;
+              xv[r].v[i] = Elem<E>::from_f32(0.f);
+            }
+          }
+      }
+
+      // this thread's rows as one map, then all maps of the wave up to it
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float x = Elem<E>::to_f32(xv[r].v[i]);
-        C[i] = BWD ? a[r][i] * (C[i] + x) : fmaf(a[r][i], C[i], x);
-        A[i] *= a[r][i];
+        A[i] = a[0][i];
+        C[i] = BWD ? a[0][i] * Elem<E>::to_f32(xv[0].v[i]) : Elem<E>::to_f32(xv[0].v[i]);
       }
-    scan_step<1, V>(A, C);
-    scan_step<2, V>(A, C);
-    scan_step<4, V>(A, C);
-    scan_step<8, V>(A, C);
+#pragma unroll
+      for (int r = 1; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float x = Elem<E>::to_f32(xv[r].v[i]);
+          C[i] = BWD ? a[r][i] * (C[i] + x) : fmaf(a[r][i], C[i], x);
+          A[i] *= a[r][i];
+        }
+      scan_step<1, V>(A, C);
+      scan_step<2, V>(A, C);
+      scan_step<4, V>(A, C);
+      scan_step<8, V>(A, C);
+    }
     if (gw == GW - 1) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -336,7 +344,7 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
         }
       }
     }
-    if constexpr (MODE != GLR_MAPS) {
+    if (MODE != GLR_MAPS && base + w0 < len) {
       // the value before this thread's rows
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] = fmaf(row_shr<1>(1.f, A[i]), y[i], row_shr<1>(0.f, C[i]));
@@ -439,6 +447,10 @@ struct GlrShape {
     const long long grid = (units + 7) / 8 * 8 * p.inner;
     hipLaunchKernelGGL((kla_glr_kernel<E, V, NW, R, BWD, MODE, PIECES>), dim3((unsigned)grid), dim3(64 * NW), 0, st, p);
   }
+  static hipError_t whole(const GlrParams &p, hipStream_t st) {
+    go<GLR_WHOLE>(p, 1, st);
+    return hipGetLastError();
+  }
   static hipError_t launch(const GlrParams &p, long long segs, hipStream_t st) {
     if (segs <= 1) {
       go<GLR_WHOLE>(p, 1, st);
@@ -461,8 +473,13 @@ struct GlrShape {
 // Short sequences do not pay for a second pass (512 channels, 3,000 tokens: 15 us with 32
 // bytes, 19 with segments), nor for tiles of 1,024 rows (5,000 channels, 1,500 tokens: 19 us
 // whole, 25 with 32 bytes).
+//
+// Tiles fit the longest sequence: one wave's 64 rows, four waves' 256 or eight waves' 512
+// (19 sequences of 2 to 7 tokens,
+// 16 heads of 2,560 channels: 37 us against 393 with 512 rows).
 struct GlrPlan {
   bool pieces, narrow;
+  int waves;
   int segs, seg_rows;
 };
 
@@ -472,7 +489,7 @@ GlrPlan glr_plan(const GlrArgs &a) {
   const bool pieces = a.d * (long long)e % 16 == 0 && (long long)a.d * e <= (1 << 20);
   const int V = pieces ? 16 / e : (a.d % (8 / e) == 0 ? 8 / e : 1);
   const long long wide = (long long)a.num_seqs * a.H * ((a.d + 4 * V - 1) / (4 * V));
-  GlrPlan r{pieces, false, 1, 0};
+  GlrPlan r{pieces, false, a.longest <= 64 ? 1 : (a.longest <= 256 ? 4 : 8), 1, 0};
   if (wide >= 256 || a.longest <= 2048) return r;
   if (pieces && (wide >= 128 || a.longest <= 3584)) {
     r.narrow = true;
@@ -485,14 +502,20 @@ GlrPlan glr_plan(const GlrArgs &a) {
   return r;
 }
 
+template <typename E, int V, bool BWD, bool PIECES>
+hipError_t launch_glr_v(const GlrParams &p, const GlrPlan &plan, hipStream_t st) {
+  if (plan.waves == 1) return GlrShape<E, V, 1, 4, BWD, PIECES>::whole(p, st);
+  if (plan.waves == 4) return GlrShape<E, V, 4, 4, BWD, PIECES>::whole(p, st);
+  return GlrShape<E, V, 8, 4, BWD, PIECES>::launch(p, plan.segs, st);
+}
+
 template <typename E, bool BWD>
 hipError_t launch_glr(const GlrParams &p, const GlrPlan &plan, hipStream_t st) {
   constexpr int V = 16 / sizeof(E);
-  if (plan.pieces)
-    return plan.narrow ? GlrShape<E, V / 2, 8, 8, BWD, true>::launch(p, plan.segs, st)
-                       : GlrShape<E, V, 8, 4, BWD, true>::launch(p, plan.segs, st);
-  if (p.d % (V / 2) == 0) return GlrShape<E, V / 2, 8, 4, BWD, false>::launch(p, plan.segs, st);
-  return GlrShape<E, 1, 8, 4, BWD, false>::launch(p, plan.segs, st);
+  if (plan.narrow) return GlrShape<E, V / 2, 8, 8, BWD, true>::whole(p, st);
+  if (plan.pieces) return launch_glr_v<E, V, BWD, true>(p, plan, st);
+  if (p.d % (V / 2) == 0) return launch_glr_v<E, V / 2, BWD, false>(p, plan, st);
+  return launch_glr_v<E, 1, BWD, false>(p, plan, st);
 }
 
 }  // namespace

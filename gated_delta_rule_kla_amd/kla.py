@@ -607,6 +607,13 @@ def pgdn_decode_step(
     return out
 
 
+def _fit(t, name: str, dtype, shape, dev) -> None:
+    """_need's check, in the order that costs least where everything is fine."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
+
+
 def _device_of(fn: str, t: torch.Tensor) -> torch.device:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"kla.{fn}: expected a tensor, got {type(t).__name__}")
@@ -631,19 +638,20 @@ def _seqlens(cu_seqlens, cu_seqlens_host, B: int, dev):
         if cu_seqlens_host is not None:
             raise ValueError("cu_seqlens_host without cu_seqlens")
         return B, None
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
+    _fit(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
     if cu_seqlens.numel() == 0:
         raise ValueError("cu_seqlens must hold at least one offset")
-    if cu_seqlens_host is None:
-        cu_seqlens_host = cu_seqlens
-    if cu_seqlens_host.numel() != cu_seqlens.numel():
+    host = cu_seqlens if cu_seqlens_host is None else cu_seqlens_host
+    if host.numel() != cu_seqlens.numel():
         raise ValueError("cu_seqlens_host does not mirror cu_seqlens")
-    return cu_seqlens.numel() - 1, cu_seqlens_host.to("cpu", torch.int32).contiguous()
+    if host.dtype != torch.int32 or host.device.type != "cpu" or not host.is_contiguous():
+        host = host.to("cpu", torch.int32).contiguous()
+    return cu_seqlens.numel() - 1, host
 
 
 def _optional(t, name, dtype, shape, dev) -> None:
     if t is not None:
-        _need(t, name, dtype, shape, dev)
+        _fit(t, name, dtype, shape, dev)
 
 
 def _scratch(workspace, need: int, dev) -> Optional[torch.Tensor]:
@@ -658,12 +666,12 @@ def _scratch(workspace, need: int, dev) -> Optional[torch.Tensor]:
 def _call(fn: str, dev: torch.device, *args) -> None:
     """Call the library on the current stream of the tensors' device, which need not be the
     current device."""
-    f = getattr(lib(), fn)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = f(*args, _stream(dev))
+    f, index = getattr(lib(), fn), dev.index
+    if index == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _stream(dev))
+            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         _check(fn, st)
 
@@ -701,14 +709,14 @@ def glr_chunk_fwd(
     dev = _device_of("glr_chunk_fwd", x)
     dtype = x.dtype
     B, H, T, d = shape = _rank(x, "x", 4)
-    _need(x, "x", dtype, shape, dev)
-    _need(g, "g", dtype, shape, dev)
+    _fit(x, "x", dtype, shape, dev)
+    _fit(g, "g", dtype, shape, dev)
     N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
     _optional(initial_state, "initial_state", torch.float32, (N, H, d), dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty_like(x)
     else:
-        _need(out, "out", dtype, shape, dev)
+        _fit(out, "out", dtype, shape, dev)
     if output_final_state and final_state is None:
         final_state = torch.empty((N, H, d), dtype=torch.float32, device=dev)
     _optional(final_state, "final_state", torch.float32, (N, H, d), dev)
@@ -741,7 +749,7 @@ def glr_chunk_bwd(
     dtype = g.dtype
     B, H, T, d = shape = _rank(g, "g", 4)
     for t, name in ((g, "g"), (o, "o"), (do, "do")):
-        _need(t, name, dtype, shape, dev)
+        _fit(t, name, dtype, shape, dev)
     N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
     _optional(initial_state, "initial_state", torch.float32, (N, H, d), dev)
     _optional(dfinal_state, "dfinal_state", torch.float32, (N, H, d), dev)
@@ -763,13 +771,13 @@ def glr_decode_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
     dev = _device_of("glr_decode_step", x)
     dtype = x.dtype
     N, H, d = shape = _rank(x, "x", 3)
-    _need(x, "x", dtype, shape, dev)
-    _need(g, "g", dtype, shape, dev)
-    _need(state, "state", torch.float32, shape, dev)
+    _fit(x, "x", dtype, shape, dev)
+    _fit(g, "g", dtype, shape, dev)
+    _fit(state, "state", torch.float32, shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty_like(x)
     else:
-        _need(out, "out", dtype, shape, dev)
+        _fit(out, "out", dtype, shape, dev)
     _call("kla_glr_decode_step", dev, _ptr(x), _ptr(g), _ptr(state), _ptr(out), N, H, d, _DTYPES[dtype])
     return out
 
@@ -797,9 +805,9 @@ def attn_fwd(
     dtype = q.dtype
     B, Hq, Tq, D = shape = _rank(q, "q", 4)
     _, Hkv, Tk, _ = _rank(k, "k", 4)
-    _need(q, "q", dtype, shape, dev)
-    _need(k, "k", dtype, (B, Hkv, Tk, D), dev)
-    _need(v, "v", dtype, (B, Hkv, Tk, D), dev)
+    _fit(q, "q", dtype, shape, dev)
+    _fit(k, "k", dtype, (B, Hkv, Tk, D), dev)
+    _fit(v, "v", dtype, (B, Hkv, Tk, D), dev)
     N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
     if cu_seqlens_k is None:
         if cu_seqlens_k_host is not None:
@@ -810,13 +818,13 @@ def attn_fwd(
         if cu_seqlens is None or Nk != N:
             raise ValueError("cu_seqlens_k needs cu_seqlens of as many sequences")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty_like(q)
     else:
-        _need(out, "out", dtype, shape, dev)
+        _fit(out, "out", dtype, shape, dev)
     if lse is None:
         lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
     else:
-        _need(lse, "lse", torch.float32, (B, Hq, Tq), dev)
+        _fit(lse, "lse", torch.float32, (B, Hq, Tq), dev)
     _call("kla_attn_fwd", dev, _ptr(q), _ptr(k), _ptr(v), D ** -0.5 if scale is None else float(scale), _ptr(out),
           _ptr(lse), _ptr(cu_seqlens), _ptr(host), _ptr(cu_seqlens_k), _ptr(host_k), N, B, Hq, Hkv, Tq, Tk, D,
           _DTYPES[dtype])
@@ -835,10 +843,10 @@ def _cache_args(codes, scales, block_table, N: int, dev):
     if two != 2:
         raise ValueError(f"codes has shape {tuple(codes.shape)}, expected [num_pages, 2, Hkv, page_size, D/2]")
     D = 2 * half
-    _need(codes, "codes", torch.uint8, (P, 2, Hkv, page, half), dev)
-    _need(scales, "scales", torch.uint8, (P, 2, Hkv, page, D // 32), dev)
+    _fit(codes, "codes", torch.uint8, (P, 2, Hkv, page, half), dev)
+    _fit(scales, "scales", torch.uint8, (P, 2, Hkv, page, D // 32), dev)
     _, M = _rank(block_table, "block_table", 2)
-    _need(block_table, "block_table", torch.int32, (N, M), dev)
+    _fit(block_table, "block_table", torch.int32, (N, M), dev)
     return P, Hkv, page, D, M
 
 
@@ -860,13 +868,13 @@ def kv4_append(
     """
     dev = _device_of("kv4_append", k)
     B, Hkv, T, D = shape = _rank(k, "k", 4)
-    _need(k, "k", k.dtype, shape, dev)
-    _need(v, "v", k.dtype, shape, dev)
+    _fit(k, "k", k.dtype, shape, dev)
+    _fit(v, "v", k.dtype, shape, dev)
     N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
     P, H, page, Dc, M = _cache_args(codes, scales, block_table, N, dev)
     if (H, Dc) != (Hkv, D):
         raise ValueError(f"k has {Hkv} heads of {D} channels, the cache {H} of {Dc}")
-    _need(start, "start", torch.int32, (N,), dev)
+    _fit(start, "start", torch.int32, (N,), dev)
     _call("kla_kv4_append", dev, _ptr(k), _ptr(v), _ptr(codes), _ptr(scales), _ptr(block_table), _ptr(start),
           _ptr(cu_seqlens), _ptr(host), N, B, Hkv, T, D, P, page, M, _DTYPES[k.dtype])
 
@@ -893,13 +901,15 @@ def kv4_read(
     if host is None:
         raise ValueError("kla.kv4_read needs cu_seqlens")
     P, Hkv, page, D, M = _cache_args(codes, scales, block_table, N, dev)
-    _need(start, "start", torch.int32, (N,), dev)
-    T = int(host[-1])
+    _fit(start, "start", torch.int32, (N,), dev)
+    T = ctypes.c_int32.from_address(host.data_ptr() + 4 * N).value  # host[-1]
     shape = (1, Hkv, max(T, 0), D)
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev))
-    _need(out[0], "out[0]", dtype, shape, dev)
-    _need(out[1], "out[1]", dtype, shape, dev)
+        k = torch.empty(shape, dtype=dtype, device=dev)
+        out = (k, torch.empty_like(k))
+    else:
+        _fit(out[0], "out[0]", dtype, shape, dev)
+        _fit(out[1], "out[1]", dtype, shape, dev)
     _call("kla_kv4_read", dev, _ptr(out[0]), _ptr(out[1]), _ptr(codes), _ptr(scales), _ptr(block_table), _ptr(start),
           _ptr(cu_seqlens), _ptr(host), N, 1, Hkv, T, D, P, page, M, _DTYPES[dtype])
     return out
@@ -930,15 +940,15 @@ def attn_kv4_decode_step(
     """
     dev = _device_of("attn_kv4_decode_step", q)
     N, Hq, D = shape = _rank(q, "q", 3)
-    _need(q, "q", q.dtype, shape, dev)
+    _fit(q, "q", q.dtype, shape, dev)
     P, Hkv, page, Dc, M = _cache_args(codes, scales, block_table, N, dev)
     if Dc != D:
         raise ValueError(f"q has {D} channels, the cache {Dc}")
-    _need(seq_lens, "seq_lens", torch.int32, (N,), dev)
+    _fit(seq_lens, "seq_lens", torch.int32, (N,), dev)
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(q)
     else:
-        _need(out, "out", q.dtype, shape, dev)
+        _fit(out, "out", q.dtype, shape, dev)
     max_len = M * page if max_len is None else int(max_len)
     dt = _DTYPES[q.dtype]
     ws = _scratch(workspace, lib().kla_attn_kv4_decode_workspace_bytes(N, Hq, Hkv, D, max_len, dt), dev)
