@@ -75,60 +75,100 @@ __device__ __forceinline__ void st8(E *p, const float *f) {
   }
 }
 
-// D / 8 lanes to a row; blockIdx.y: K or V.
+// A workgroup moves 64 consecutive tokens of one head's keys or values: the first wave finds
+// their places (sequence, position, page) while the other loads are in flight, then D / 8 lanes
+// move a row.  With one row per 16 lanes and the search in each of them, 146,000 tokens of 4
+// heads took 170 us one way; with four rows a thread in flight 90.
+constexpr int KV_TOKENS = 64, KV_CU = 1024;  // tokens of a workgroup; offsets searched in LDS
+
 template <typename E, int D, bool READ>
 __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
-  constexpr int LPR = D / 8;
-  const int lane = threadIdx.x % LPR;
-  const long long row = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-  if (row >= p.rows) return;
-  const int t = (int)(row % p.T), head = (int)((row / p.T) % p.kv.Hkv);
-  int n = (int)(row / p.T / p.kv.Hkv), at = t;
-  if (p.cu) {
-    // the last sequence that starts at or before t and is not empty (device offsets clamped)
-    int lo = 0, hi = p.N;  // cu[lo] <= t < cu[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.cu[mid] <= t) lo = mid; else hi = mid;
-    }
-    n = lo;
-    at = t - max(p.cu[n], 0);
+  constexpr int LPR = D / 8, RPT = KV_TOKENS * LPR / 256;  // lanes of a row, rows of a thread
+  __shared__ long long s_row[KV_TOKENS];
+  __shared__ int s_cu[KV_CU];
+  const int tid = threadIdx.x, lane = tid % LPR;
+  const unsigned jh = blockIdx.x % (2 * p.kv.Hkv);
+  const int j = jh / p.kv.Hkv, head = jh % p.kv.Hkv;
+  const long long tok0 = (long long)(blockIdx.x / (2 * p.kv.Hkv)) * KV_TOKENS, toks = p.rows / p.kv.Hkv;  // B * T
+  E *const base = (E *)(j ? p.v : p.k);
+
+  auto x_of = [&](int i) {  // row i of the workgroup (the last one's again past the end)
+    const long long tok = min(tok0 + i, toks - 1);
+    return base + (((tok / p.T) * p.kv.Hkv + head) * p.T + tok % p.T) * D + 8 * lane;
+  };
+  float f[RPT][8];
+  if constexpr (!READ) {
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) ld8((const E *)x_of(tid / LPR + 256 / LPR * r), f[r]);
   }
-  const long long pos = (long long)p.start[n] + at;
-  const int j = blockIdx.y;
-  const long long dst = pos > 0x7fffffffLL ? -1 : kv_row(p.kv, n, (int)max(pos, -1LL), j, head);
-  E *x = (E *)(j ? p.v : p.k) + row * D + 8 * lane;
-  float f[8];
-  if constexpr (READ) {
-    if (dst < 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-    } else {
-      const unsigned u = *reinterpret_cast<const unsigned *>(p.kv.codes + dst * (D / 2) + 4 * lane);
-      const float s = __builtin_bit_cast(float, (unsigned)p.kv.scales[dst * (D / 32) + lane / 4] << 23);
-      typedef float f32x2 __attribute__((ext_vector_type(2)));
-      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, s, 1);
-      const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, s, 3);
-      f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1], f[4] = c[0], f[5] = c[1], f[6] = d[0], f[7] = d[1];
+  const bool near = p.cu && p.N < KV_CU;
+  if (near) {
+    for (int i = tid; i <= p.N; i += 256) s_cu[i] = p.cu[i];
+    __syncthreads();
+  }
+  if (tid < KV_TOKENS) {
+    const long long tok = tok0 + tid;
+    long long row = -1;
+    if (tok < toks) {
+      int n = (int)(tok / p.T), at = (int)(tok % p.T);
+      if (p.cu) {
+        // the last sequence that starts at or before the token (its offsets not decreasing)
+        int lo = 0, hi = p.N;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if ((near ? s_cu[mid] : p.cu[mid]) <= at) lo = mid; else hi = mid;
+        }
+        n = lo;
+        at -= max(near ? s_cu[n] : p.cu[n], 0);
+      }
+      const long long pos = (long long)p.start[n] + at;
+      if (pos >= 0 && pos <= 0x7fffffffLL) row = kv_row(p.kv, n, (int)pos, j, head);
     }
-    st8(x, f);
-  } else {
-    ld8((const E *)x, f);
-    unsigned top = 0;  // |x| as bits: NaN above infinity above every number
+    s_row[tid] = row;
+  }
+  __syncthreads();
+  if constexpr (READ) {
+    unsigned u[RPT];
+    uint8_t sc[RPT];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(unsigned, f[i]) & 0x7fffffffu);
-    top = quad_max<0xB1>(top);
-    top = quad_max<0x4E>(top);
-    const unsigned e = top >> 23, s = e == 255 ? 255u : (e > 3 ? e - 2 : 1u);
-    const float sc = __builtin_bit_cast(float, s << 23);
-    unsigned u = 0;
-    u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[0], f[1], sc, 0);
-    u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[2], f[3], sc, 1);
-    u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[4], f[5], sc, 2);
-    u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[6], f[7], sc, 3);
-    if (dst >= 0) {
-      *reinterpret_cast<unsigned *>(p.kv.codes + dst * (D / 2) + 4 * lane) = u;
-      if (lane % 4 == 0) p.kv.scales[dst * (D / 32) + lane / 4] = (uint8_t)s;
+    for (int r = 0; r < RPT; ++r) {
+      const long long row = s_row[tid / LPR + 256 / LPR * r];
+      // a token without a place: zero codes
+      u[r] = row >= 0 ? *reinterpret_cast<const unsigned *>(p.kv.codes + row * (D / 2) + 4 * lane) : 0u;
+      sc[r] = row >= 0 ? p.kv.scales[row * (D / 32) + lane / 4] : 127;
+    }
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      const float s = __builtin_bit_cast(float, (unsigned)sc[r] << 23);
+      typedef float f32x2 __attribute__((ext_vector_type(2)));
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u[r], s, 0);
+      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u[r], s, 1);
+      const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u[r], s, 2);
+      const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u[r], s, 3);
+      const float y[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+      const int i = tid / LPR + 256 / LPR * r;
+      if (tok0 + i < toks) st8(x_of(i), y);
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      unsigned top = 0;  // |x| as bits: NaN above infinity above every number
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(unsigned, f[r][i]) & 0x7fffffffu);
+      top = quad_max<0xB1>(top);
+      top = quad_max<0x4E>(top);
+      const unsigned e = top >> 23, s = e == 255 ? 255u : (e > 3 ? e - 2 : 1u);
+      const float sc = __builtin_bit_cast(float, s << 23);
+      unsigned u = 0;
+      u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[r][0], f[r][1], sc, 0);
+      u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[r][2], f[r][3], sc, 1);
+      u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[r][4], f[r][5], sc, 2);
+      u = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(u, f[r][6], f[r][7], sc, 3);
+      const long long row = s_row[tid / LPR + 256 / LPR * r];
+      if (row >= 0) {
+        *reinterpret_cast<unsigned *>(p.kv.codes + row * (D / 2) + 4 * lane) = u;
+        if (lane % 4 == 0) p.kv.scales[row * (D / 32) + lane / 4] = (uint8_t)s;
+      }
     }
   }
 }
@@ -140,14 +180,22 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
 // tiles of 32 tokens in turn, each with its own running maximum, sum and output, joined in LDS
 // at the end, and the runs of one head are joined by a second kernel.
 //
-// Codes become MFMA operands without LDS.  K: lane (r = lane & 15, c = lane >> 4) holds a
+// K's codes become MFMA operands as they are loaded.  Lane (r = lane & 15, c = lane >> 4) holds a
 // quarter of key r's row, channels c D/4 and up; its j-th eight channels are its slots of the
 // j-th v_mfma_f32_16x16x32_bf16, q being laid out the same.  The scores S^T come with heads
 // along the lanes and keys 4c .. 4c+3 in each, so that two 16-key tiles are the left-over
 // operand P^T of the second product as they stand: slots 8c + e are the keys 4c + e and
-// 16 + 4c + e - 4.  V: the lane loads channels r D/16 and up of those eight keys, converts
-// pairs of channels (v_cvt_scalef32_pk_bf16_fp4 applies the scale too) and exchanges halves
-// (v_perm) into pairs of keys; MFMA j takes channel r D/16 + j of every lane.
+// 16 + 4c + e - 4.  V goes through LDS, still in 4 bits, into lanes that hold channels r D/16
+// and up of those eight keys; they convert pairs of channels (v_cvt_scalef32_pk_bf16_fp4
+// applies the scale too) and exchange halves (v_perm) into pairs of keys, and MFMA j takes
+// channel r D/16 + j of every lane.
+//
+// Measured (64 sequences of 4,096 to 16,384 tokens, 16 heads over 4, D = 128, 326 MB): 75 us a
+// step, 4.3 TB/s, where 4 KB reads in any order reach 5.8; of it the joining kernel is 5.  With
+// V's dwords and scale bytes loaded straight into that layout, and the runs of a sequence side
+// by side in the grid, it took 107; a second tile in flight, or two or four workgroups on a CU
+// for three, change nothing: what is left is spread over the conversions (37% of the issue
+// slots), the latency of one tile's chain and the lengths' unevenness.
 //
 // Queries in fp32 run the same products with q and P split into three bf16 terms (24 bits),
 // exact against the cache's values.
@@ -175,22 +223,26 @@ __device__ __forceinline__ void cvt8(unsigned u, float s, unsigned *r) {
 }
 
 template <typename E, int D>
-__global__ __launch_bounds__(256) void kla_kv4_decode_kernel(KvDecodeParams p) {
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void kla_kv4_decode_kernel(KvDecodeParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;  // bf16 terms of q and P
   constexpr int KJ = D / 32;                  // products over the channels, 8 channels a lane
   constexpr int DW = D / 16;                  // channels of V a lane holds
   __shared__ int s_page[KV_MAX_PER / 16];
   __shared__ float s_o[4][16][D + 4];
   __shared__ float s_ml[4][16][2];
+  __shared__ __attribute__((aligned(16))) uint8_t s_v[4][32 * D / 2];
+  __shared__ unsigned s_sc[4][64];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, c = lane >> 4;
+  // runs slowest: workgroups go round the eight XCDs, and with the runs of a sequence side by
+  // side the first ones, which every sequence has, met on a few of them
   unsigned b = blockIdx.x;
-  const int split = b % p.splits;
-  b /= p.splits;
   const int gb = b % p.GB;
   b /= p.GB;
-  const int head = b % p.kv.Hkv, n = b / p.kv.Hkv;
+  const int head = b % p.kv.Hkv;
+  b /= p.kv.Hkv;
+  const int n = b % p.N, split = b / p.N;
   const int g0 = gb * 16, gn = min(p.G - g0, 16);  // query heads of this workgroup
   const int hq0 = head * p.G + g0;
   // tokens of the sequence, of this run
@@ -231,52 +283,69 @@ __global__ __launch_bounds__(256) void kla_kv4_decode_kernel(KvDecodeParams p) {
   for (int j = 0; j < DW; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
 
-  // one tile's codes and scales
-  unsigned kc[2][KJ], vc[8];
-  uint8_t ks[2], vs[8];
-  int id0, id1;
-  auto load = [&](int t) {
-    id0 = __builtin_amdgcn_readfirstlane(s_page[(t - lo) >> 4]);
-    id1 = __builtin_amdgcn_readfirstlane(s_page[((t - lo) >> 4) + 1]);
+  // A tile's codes and scales as they are loaded: K in operand layout, V in 16-byte pieces of
+  // rows, and the 32 keys' scales, then the values', a row to a lane.
+  constexpr int VP = D / 64;           // pieces of V a lane loads
+  constexpr int LPR = D / 32;          // lanes of a row of V
+  struct Tile {
+    unsigned k[2][KJ];
+    uint4 v[VP];
+    unsigned sc;
+    int id0, id1;
+  } next;
+  auto load = [&](Tile &x, int t) {
+    x.id0 = __builtin_amdgcn_readfirstlane(s_page[(t - lo) >> 4]);
+    x.id1 = __builtin_amdgcn_readfirstlane(s_page[((t - lo) >> 4) + 1]);
     const size_t pg = (size_t)p.kv.Hkv * p.kv.page;
     // rows of the two 16-token blocks (page 0 where there is none: masked below)
-    const size_t r0 = (size_t)max(id0, 0) * 2 * pg + (size_t)head * p.kv.page + t % p.kv.page;
-    const size_t r1 = (size_t)max(id1, 0) * 2 * pg + (size_t)head * p.kv.page + (t + 16) % p.kv.page;
+    const size_t r0 = (size_t)max(x.id0, 0) * 2 * pg + (size_t)head * p.kv.page + t % p.kv.page;
+    const size_t r1 = (size_t)max(x.id1, 0) * 2 * pg + (size_t)head * p.kv.page + (t + 16) % p.kv.page;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const size_t row = (h ? r1 : r0) + r;
-      const uint8_t *a = p.kv.codes + row * (D / 2) + c * (D / 8);
+      const uint8_t *a = p.kv.codes + ((h ? r1 : r0) + r) * (D / 2) + c * (D / 8);
       if constexpr (D == 128) {
         const uint4 u = ldg16(a);
-        kc[h][0] = u.x, kc[h][1] = u.y, kc[h][2] = u.z, kc[h][3] = u.w;
+        x.k[h][0] = u.x, x.k[h][1] = u.y, x.k[h][2] = u.z, x.k[h][3] = u.w;
       } else {
         const uint2 u = *reinterpret_cast<const uint2 *>(a);
-        kc[h][0] = u.x, kc[h][1] = u.y;
+        x.k[h][0] = u.x, x.k[h][1] = u.y;
       }
-      ks[h] = p.kv.scales[row * (D / 32) + (D == 128 ? c : c / 2)];
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const size_t row = (e < 4 ? r0 : r1) + pg + 4 * c + (e & 3);
-      if constexpr (D == 128) vc[e] = *reinterpret_cast<const unsigned *>(p.kv.codes + row * 64 + 4 * r);
-      else vc[e] = *reinterpret_cast<const unsigned short *>(p.kv.codes + row * 32 + 2 * r);
-      vs[e] = p.kv.scales[row * (D / 32) + (r * DW) / 32];
+    for (int i = 0; i < VP; ++i) {
+      const int key = lane / LPR + 64 / LPR * i;
+      x.v[i] = ldg16(p.kv.codes + ((key < 16 ? r0 : r1) + pg + key % 16) * (D / 2) + 16 * (lane % LPR));
     }
+    const uint8_t *a = p.kv.scales + ((lane & 16 ? r1 : r0) + (lane & 15) + (lane & 32 ? pg : 0)) * (D / 32);
+    if constexpr (D == 128) x.sc = *reinterpret_cast<const unsigned *>(a);
+    else x.sc = *reinterpret_cast<const unsigned short *>(a);
   };
 
   int t = lo + 32 * wave;
-  if (t < hi) load(t);
+  if (t < hi) load(next, t);
   for (; t < hi; t += 128) {
+    const Tile x0 = next;
+    if (t + 128 < hi) load(next, t + 128);
+    // V and the scales through the wave's own LDS; key 16 h + 4 c + e at slot 16 h + 4 e + c,
+    // so that the four keys of a read fill the banks
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      const int key = lane / LPR + 64 / LPR * i, slot = (key & 16) + 4 * (key & 3) + ((key >> 2) & 3);
+      *reinterpret_cast<uint4 *>(s_v[wave] + slot * (D / 2) + 16 * (lane % LPR)) = x0.v[i];
+    }
+    s_sc[wave][lane] = x0.sc;
+    const uint8_t *sc8 = reinterpret_cast<const uint8_t *>(s_sc[wave]);
+    const int id0 = x0.id0, id1 = x0.id1;
     // scores of keys t + 16h + 4c + i against head r
     float x[8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       f32x4 s = {0.f, 0.f, 0.f, 0.f};
-      const float sc = __builtin_bit_cast(float, (unsigned)ks[h] << 23);
+      const float sc = __builtin_bit_cast(float, (unsigned)sc8[4 * (16 * h + r) + (D == 128 ? c : c / 2)] << 23);
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
         unsigned w[4];
-        cvt8(kc[h][j], sc, w);
+        cvt8(x0.k[h][j], sc, w);
         bf16x8v a;
         __builtin_memcpy(&a, w, 16);
 #pragma unroll
@@ -289,8 +358,10 @@ __global__ __launch_bounds__(256) void kla_kv4_decode_kernel(KvDecodeParams p) {
     float vf[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      va[e] = vc[e];
-      vf[e] = __builtin_bit_cast(float, (unsigned)vs[e] << 23);
+      const uint8_t *a = s_v[wave] + ((e & 4) * 4 + 4 * (e & 3) + c) * (D / 2);
+      if constexpr (D == 128) va[e] = *reinterpret_cast<const unsigned *>(a + 4 * r);
+      else va[e] = *reinterpret_cast<const unsigned short *>(a + 2 * r);
+      vf[e] = __builtin_bit_cast(float, (unsigned)sc8[4 * (32 + 16 * (e >> 2) + 4 * c + (e & 3)) + r * DW / 32] << 23);
     }
     if (id0 < 0 || id1 < 0 || t + 32 > hi) {
       // tokens past the end and tokens of missing pages: no score, and a value of zero
@@ -303,7 +374,6 @@ __global__ __launch_bounds__(256) void kla_kv4_decode_kernel(KvDecodeParams p) {
         vf[e] = none ? 1.f : vf[e];
       }
     }
-    if (t + 128 < hi) load(t + 128);
 
     float top = x[0];
 #pragma unroll
@@ -388,31 +458,52 @@ __global__ __launch_bounds__(256) void kla_kv4_decode_kernel(KvDecodeParams p) {
   }
 }
 
-// The runs of one (sequence, query head), in order.
+// The runs of one (sequence, query head).  Eight groups of threads take every eighth run, four
+// channels to a thread, and meet in LDS: in one group's order the 512 runs of a sequence of
+// 131,072 tokens took 19 us, so 4.
 template <typename E, int D>
-__global__ __launch_bounds__(D) void kla_kv4_join_kernel(KvDecodeParams p) {
+__global__ __launch_bounds__(2 * D) void kla_kv4_join_kernel(KvDecodeParams p) {
+  constexpr int GROUPS = 8, LPG = D / 4;  // lanes of a group
+  __shared__ f32x4 s_o[GROUPS][LPG];
+  __shared__ float s_l[GROUPS];
   const size_t row = blockIdx.x;
+  const int g = threadIdx.x / LPG, lane = threadIdx.x % LPG;
   const float *ml = p.part_ml + row * p.splits * 2;
   float m = -INFINITY;
   for (int s = threadIdx.x % 64; s < p.splits; s += 64) m = fmaxf(m, ml[2 * s]);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
   const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o = 0.f;
-  const float *po = p.part_o + row * p.splits * D + threadIdx.x;
-#pragma unroll 8
-  for (int s = 0; s < p.splits; ++s) {
+  float l = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  const float *po = p.part_o + row * p.splits * D + 4 * lane;
+#pragma unroll 4
+  for (int s = g; s < p.splits; s += GROUPS) {
     const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
+    const f32x4 v = *reinterpret_cast<const f32x4 *>(po + (size_t)s * D);
     l = fmaf(ml[2 * s + 1], f, l);
-    o = fmaf(po[(size_t)s * D], f, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], f, o[i]);
   }
-  ((E *)p.o)[row * D + threadIdx.x] = Elem<E>::from_f32(l == 0.f ? 0.f : o / l);
+  s_o[g][lane] = o;
+  if (lane == 0) s_l[g] = l;
+  __syncthreads();
+  if (g) return;
+#pragma unroll
+  for (int k = 1; k < GROUPS; ++k) {
+    l += s_l[k];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] += s_o[k][lane][i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    ((E *)p.o)[row * D + 4 * lane + i] = Elem<E>::from_f32(l == 0.f ? 0.f : o[i] / l);
 }
 
 template <typename E, bool READ>
 hipError_t launch_move(const KvMoveParams &p, int D, hipStream_t st) {
-  const int rpb = 256 / (D / 8);
-  const dim3 grid((unsigned)((p.rows + rpb - 1) / rpb), 2);
+  const long long toks = p.rows / p.kv.Hkv;
+  const dim3 grid((unsigned)((toks + KV_TOKENS - 1) / KV_TOKENS * 2 * p.kv.Hkv));
   if (D == 128) hipLaunchKernelGGL((kla_kv4_move_kernel<E, 128, READ>), grid, dim3(256), 0, st, p);
   else hipLaunchKernelGGL((kla_kv4_move_kernel<E, 64, READ>), grid, dim3(256), 0, st, p);
   return hipGetLastError();
@@ -423,7 +514,7 @@ hipError_t launch_kv4_decode(const KvDecodeParams &p, hipStream_t st) {
   const long long grid = (long long)p.N * p.kv.Hkv * p.GB * p.splits;
   hipLaunchKernelGGL((kla_kv4_decode_kernel<E, D>), dim3((unsigned)grid), dim3(256), 0, st, p);
   if (p.splits > 1)
-    hipLaunchKernelGGL((kla_kv4_join_kernel<E, D>), dim3((unsigned)((long long)p.N * p.Hq)), dim3(D), 0, st, p);
+    hipLaunchKernelGGL((kla_kv4_join_kernel<E, D>), dim3((unsigned)((long long)p.N * p.Hq)), dim3(2 * D), 0, st, p);
   return hipGetLastError();
 }
 
@@ -431,12 +522,13 @@ KvParams kv_params(const Kv4Cache &c) {
   return KvParams{(uint8_t *)c.codes, (uint8_t *)c.scales, c.table, c.num_pages, c.page, c.max_pages, c.Hkv};
 }
 
-// Runs of the sequences: as many as bring about 1,024 workgroups (four to a CU), of 256 tokens
-// at least (eight a wave) and KV_MAX_PER at most.
+// Runs of the sequences: as many as bring about 1,024 workgroups (64 ragged sequences of 4
+// heads: 75 us, with 512 workgroups 88, with 2,048 78), of 512 tokens at least (four tiles a
+// wave; one sequence of 131,072 tokens: 19.3 us, with 256 tokens 21.6) and KV_MAX_PER at most.
 void kv4_runs(const Kv4DecodeArgs &a, int *splits, int *per) {
   const long long GB = (a.Hq / a.c.Hkv + 15) / 16, base = (long long)a.N * a.c.Hkv * GB;
   long long want = std::max<long long>(1, 1024 / std::max<long long>(1, base));
-  want = std::min(want, std::max<long long>(1, a.max_len / 256));
+  want = std::min(want, std::max<long long>(1, a.max_len / 512));
   long long len = (a.max_len + want - 1) / want;
   len = std::min<long long>(KV_MAX_PER, std::max<long long>(128, (len + 127) / 128 * 128));
   *per = (int)len;
