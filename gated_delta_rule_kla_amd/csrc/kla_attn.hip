@@ -3,15 +3,20 @@
 // o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j) over the keys j that query i
 // sees: j <= i + (lk - lq) of its own sequence (include/kla.h, kla_attn_fwd).
 //
-// One pass over the keys with a running maximum and sum.  A workgroup owns 32 NW queries of
-// one head; each of its NW waves holds 32 of them, their 32 x D output and statistics in
-// registers, and all share tiles of 64 keys and values in LDS, two of them: while one is
-// used, the next arrives by direct global-to-LDS loads.  Both products run transposed on
-// v_mfma_f32_32x32x16_bf16: S^T = K Q^T puts one query in each lane (pair), so maxima and
-// sums need one exchange between the two halves of a wave, and S^T's registers, rounded to
-// bf16, are the right operand P^T of O^T = V^T P^T as they stand: its contraction slots are
-// taken in the order in which the accumulator holds the keys (slot 8h + e of 16 keys is key
-// 4h + e, or 8 + 4h + e - 4).  V^T comes out of the row-major tile by transposing LDS reads.
+// One pass over the keys with a running maximum and sum.  Each wave of a workgroup holds 32
+// queries of one head, their 32 x D output and statistics in registers, and all waves share
+// tiles of 64 keys and values in LDS, two of them: while one is used, the next arrives by
+// direct global-to-LDS loads.  Both products run transposed on v_mfma_f32_32x32x16_bf16: S^T =
+// K Q^T puts one query in each lane (pair), so maxima and sums need one exchange between the
+// two halves of a wave, and S^T's registers, rounded to bf16, are the right operand P^T of
+// O^T = V^T P^T as they stand: its contraction slots are taken in the order in which the
+// accumulator holds the keys (slot 8h + e of 16 keys is key 4h + e, or 8 + 4h + e - 4).  V^T
+// comes out of the row-major tile by transposing LDS reads.
+//
+// Measured: 16,384 tokens, 16 heads of 128 over 2: 1.00 ms, 1.1 PFLOP/s, where a bf16 product
+// of 8192^3 reaches 1.38 and the clock falls to 2.0 GHz under either.  The matrix cores are
+// busy 53% of the cycles and the vector ALU 49%; two groups of waves half a tile apart, a
+// barrier between their phases, took 1.06 ms, operands read ahead of their products 1.00.
 //
 // LDS rows are D values long without padding (the direct loads write 1 KB runs); 16-byte
 // pieces are exchanged within a row instead, K's by the row's low bits, V's by its low two
@@ -138,6 +143,76 @@ __device__ __forceinline__ bf16x8 v_operand(const bf16 *tile, int kk, int j, int
   return bf16x8{w[0][0], w[0][1], w[0][2], w[0][3], w[1][0], w[1][1], w[1][2], w[1][3]};
 }
 
+// The left operand K, keys 32 kb + r against channels 16 j + 8 h and up, from a tile of rows.
+template <int D>
+__device__ __forceinline__ bf16x8 k_operand(const bf16 *tile, int kb, int j, int lane) {
+  const int row = 32 * kb + (lane & 31);
+  return *reinterpret_cast<const bf16x8 *>(tile + row * D + 8 * ((2 * j + (lane >> 5)) ^ (row & (D / 8 - 1))));
+}
+
+// q's row as the right operand.  The running maximum is taken of the unscaled scores, so the
+// scale's sign goes to q.  The values are here when this returns: a wait for them in the loop
+// would also wait for the tile in flight.
+template <int D>
+__device__ __forceinline__ void load_q(const AttnParams &p, const bf16 *row, int h, bf16x8 *q) {
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) q[j] = __builtin_bit_cast(bf16x8, ldg16(row + 16 * j + 8 * h));
+  if (p.flip) {
+    const unsigned a = p.flip == 1 ? 0xffffffffu : 0u, x = p.flip == 1 ? 0x80008000u : 0u;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      u32x4 u = __builtin_bit_cast(u32x4, q[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = (u[i] & a) ^ x;
+      q[j] = __builtin_bit_cast(bf16x8, u);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) asm volatile("" : "+v"(q[j]));
+}
+
+// One tile's softmax: scores x[kb][i] (key 32 kb + 8 (i / 4) + 4 h + i % 4 against query r) to
+// weights, with the running maximum m, this half's sum l and the output so far.  The maximum
+// only moves when a score exceeds it by 2^LAG: weights up to 2^LAG cost no precision (they are
+// floating point, and the sum too), and most tiles leave the output as it is.
+constexpr float LAG = 8.f;
+template <int DB>
+__device__ __forceinline__ void softmax_tile(const f32x16 *x, float c, float &m, float &l, f32x16 *acc, bf16x8 *pt) {
+  float t4[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t4[i] = fmaxf(x[0][i], x[1][i]);
+#pragma unroll
+  for (int k = 4; k < 16; k += 4)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(fmaxf(t4[i], x[0][k + i]), x[1][k + i]);
+  float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+  {  // the other half's
+    const auto w = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, top), __builtin_bit_cast(unsigned, top), false, false);
+    top = fmaxf(__builtin_bit_cast(float, w[0]), __builtin_bit_cast(float, w[1])) * c;
+  }
+  if (__any(top > m + LAG)) {
+    const float mn = top > m + LAG ? top : m;
+    const float al = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
+    l *= al;
+#pragma unroll
+    for (int j = 0; j < DB; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[j][i] *= al;
+    m = mn;
+  }
+  const float base = m == -INFINITY ? 0.f : m;
+  float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float e = __builtin_amdgcn_exp2f(fmaf(x[kb][i], c, -base));
+      s4[i % 4] += e;
+      pt[2 * kb + i / 8][i % 8] = (bf16)e;
+    }
+  l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+}
+
 // A wave's results: lane (r, h) holds query qw + r, channels 32 j + 8 (i / 4) + 4 h + i % 4.
 template <typename E, int D>
 __device__ __forceinline__ void finish(const AttnParams &p, const Span &s, int bh, int qw, const f32x16 *acc, float m,
@@ -177,13 +252,15 @@ __device__ __forceinline__ void finish(const AttnParams &p, const Span &s, int b
   }
 }
 
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void kla_attn_kernel(AttnParams p) {
-  constexpr int BM = 32 * NW, BN = 64;
+// KS = 2: two groups of NW / 2 waves share the queries and take every second tile of keys, and
+// join at the end, so that a workgroup's chain of tiles is half as long.
+template <int D, int NW, int KS>
+__global__ __launch_bounds__(64 * NW, NW / KS == 2 ? 1 : 2) void kla_attn_kernel(AttnParams p) {
+  constexpr int BM = 32 * NW / KS, BN = 64;
   constexpr int PPR = D / 8;         // 16-byte pieces of a row
   constexpr int RPI = 64 / PPR;      // rows of one direct load
   constexpr int KJ = D / 16, DB = D / 32;
-  __shared__ __attribute__((aligned(1024))) bf16 s_k[2][BN * D], s_v[2][BN * D];
+  __shared__ __attribute__((aligned(1024))) bf16 s_k[2][KS * BN * D], s_v[2][KS * BN * D];
 
   int bh, slot;
   place(p, blockIdx.x, &bh, &slot);
@@ -191,30 +268,16 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void kla_attn_kernel(Attn
   Span s;
   if (!find_span<BM>(p, slot, b, &s)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 31, h = lane >> 5;
+  const int r = lane & 31, h = lane >> 5, group = KS == 1 ? 0 : wave / (NW / KS);
   const int off = s.lk - s.lq;
   const bf16 *Q = (const bf16 *)p.q + ((size_t)bh * p.Tq + s.q0) * D;
   const bf16 *K = (const bf16 *)p.k + (((size_t)b * p.Hkv + hk) * p.Tk + s.k0) * D;
   const bf16 *V = (const bf16 *)p.v + (((size_t)b * p.Hkv + hk) * p.Tk + s.k0) * D;
 
-  const int qw = s.first + 32 * wave;                 // this wave's first query
-  const int qi = min(qw + r, s.lq - 1);               // this lane's (queries past the end repeat the last)
+  const int qw = s.first + 32 * (wave % (NW / KS));  // this wave's first query
+  const int qi = min(qw + r, s.lq - 1);              // this lane's (queries past the end repeat the last)
   bf16x8 q[KJ];
-#pragma unroll
-  for (int j = 0; j < KJ; ++j) q[j] = __builtin_bit_cast(bf16x8, ldg16(Q + (size_t)qi * D + 16 * j + 8 * h));
-  if (p.flip) {  // the running maximum is taken of the unscaled scores: the scale's sign goes to q
-    const unsigned a = p.flip == 1 ? 0xffffffffu : 0u, x = p.flip == 1 ? 0x80008000u : 0u;
-#pragma unroll
-    for (int j = 0; j < KJ; ++j) {
-      u32x4 u = __builtin_bit_cast(u32x4, q[j]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = (u[i] & a) ^ x;
-      q[j] = __builtin_bit_cast(bf16x8, u);
-    }
-  }
-  // q is here before the loop: a wait for it inside would also wait for the tile in flight
-#pragma unroll
-  for (int j = 0; j < KJ; ++j) asm volatile("" : "+v"(q[j]));
+  load_q<D>(p, Q + (size_t)qi * D, h, q);
 
   f32x16 acc[DB];
 #pragma unroll
@@ -225,27 +288,28 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void kla_attn_kernel(Attn
 
   // keys up to the last that the workgroup's, and this wave's, last query sees
   const int seen = min(s.first + BM, s.lq) + off;
-  const int tiles = seen > 0 ? (seen + BN - 1) / BN : 0;
+  const int steps = seen > 0 ? (seen + KS * BN - 1) / (KS * BN) : 0;
   const int first_key = qw + off, last_key = min(qw + 31, s.lq - 1) + off;  // of the wave's first and last query
 
   auto fetch = [&](int t, int buf) {
 #pragma unroll
-    for (int i = 0; i < BN / RPI / NW; ++i) {
-      const int r0 = (wave * (BN / RPI / NW) + i) * RPI, row = r0 + lane / PPR, pc = lane % PPR;
-      const size_t key = min(t * BN + row, s.lk - 1);  // past the end: the last key, masked below
+    for (int i = 0; i < KS * BN / RPI / NW; ++i) {
+      const int r0 = (wave * (KS * BN / RPI / NW) + i) * RPI, row = r0 + lane / PPR, pc = lane % PPR;
+      const size_t key = min(t * KS * BN + row, s.lk - 1);  // past the end: the last key, masked below
       load_lds(K + key * D + 8 * (pc ^ (row & (PPR - 1))), s_k[buf] + r0 * D);
       load_lds(V + key * D + 8 * (pc ^ ((row & 3) << 2 & (PPR - 1))), s_v[buf] + r0 * D);
     }
   };
 
-  if (tiles > 0) fetch(0, 0);
-  for (int t = 0; t < tiles; ++t) {
+  if (steps > 0) fetch(0, 0);
+  for (int t = 0; t < steps; ++t) {
     const int buf = t & 1;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (t + 1 < tiles) fetch(t + 1, buf ^ 1);
-    const int key0 = t * BN;
+    if (t + 1 < steps) fetch(t + 1, buf ^ 1);
+    const int key0 = (t * KS + group) * BN;
     if (key0 > last_key || qw >= s.lq) continue;
+    const bf16 *kt = s_k[buf] + group * BN * D, *vt = s_v[buf] + group * BN * D;
 
     f32x16 x[2];
 #pragma unroll
@@ -253,13 +317,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void kla_attn_kernel(Attn
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[kb][i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < KJ; ++j) {
-        const int row = 32 * kb + r;
-        const bf16x8 a = *reinterpret_cast<const bf16x8 *>(s_k[buf] + row * D + 8 * ((2 * j + h) ^ (row & (PPR - 1))));
-        x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[j], x[kb], 0, 0, 0);
-      }
+      for (int j = 0; j < KJ; ++j)
+        x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_operand<D>(kt, kb, j, lane), q[j], x[kb], 0, 0, 0);
     }
-    // x[kb][i]: key key0 + 32 kb + 8 (i / 4) + 4 h + i % 4 against query r
     if (key0 + BN - 1 > first_key) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -267,41 +327,38 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void kla_attn_kernel(Attn
         for (int i = 0; i < 16; ++i)
           if (key0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 > qi + off) x[kb][i] = -INFINITY;
     }
-    float top = x[0][0];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, x[kb][i]);
-    top = fmaxf(top, __shfl_xor(top, 32)) * p.c;
-    if (__any(top > m)) {
-      const float mn = fmaxf(m, top);
-      const float al = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
-      l *= al;
-#pragma unroll
-      for (int j = 0; j < DB; ++j)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[j][i] *= al;
-      m = mn;
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-    bf16x8 pt[4];  // 16 keys each
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float e = __builtin_amdgcn_exp2f(fmaf(x[kb][i], p.c, -base));
-        l += e;
-        pt[2 * kb + i / 8][i % 8] = (bf16)e;
-      }
+    bf16x8 pt[4];
+    softmax_tile<DB>(x, p.c, m, l, acc, pt);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-      for (int j = 0; j < DB; ++j) {
-        const bf16x8 va = v_operand<D>(s_v[buf], kk, j, lane);
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va, pt[kk], acc[j], 0, 0, 0);
-      }
+      for (int j = 0; j < DB; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_operand<D>(vt, kk, j, lane), pt[kk], acc[j], 0, 0, 0);
   }
-
+  if constexpr (KS == 2) {
+    // the second group's results through LDS, lane to lane: the layouts are the same
+    f32x4 *ex = reinterpret_cast<f32x4 *>(wave % (NW / 2) < NW / 4 ? &s_k[0][0] : &s_v[0][0]) +
+                (wave % (NW / 4)) * (4 * DB + 1) * 64 + lane;
+    __syncthreads();
+    if (group == 1) {
+#pragma unroll
+      for (int j = 0; j < DB; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ex[(4 * j + i) * 64] = f32x4{acc[j][4 * i], acc[j][4 * i + 1], acc[j][4 * i + 2], acc[j][4 * i + 3]};
+      ex[4 * DB * 64] = f32x4{m, l, 0.f, 0.f};
+    }
+    __syncthreads();
+    if (group == 1) return;
+    const f32x4 ml = ex[4 * DB * 64];
+    const float mn = fmaxf(m, ml[0]), base = mn == -INFINITY ? 0.f : mn;
+    const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(ml[0] - base);
+    m = mn;
+    l = l * f0 + ml[1] * f1;
+#pragma unroll
+    for (int j = 0; j < DB; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[j][i] = acc[j][i] * f0 + ex[(4 * j + i / 4) * 64][i % 4] * f1;
+  }
   finish<bf16, D>(p, s, bh, qw, acc, m, l, K, V);
 }
 
@@ -462,10 +519,10 @@ unsigned attn_grid(AttnParams *p, int BM) {
   return (unsigned)((long long)p->slots * p->B * p->Hq);
 }
 
-template <int D, int NW>
+template <int D, int NW, int KS>
 hipError_t launch_attn_t(AttnParams p, hipStream_t st) {
-  const unsigned grid = attn_grid(&p, 32 * NW);
-  hipLaunchKernelGGL((kla_attn_kernel<D, NW>), dim3(grid), dim3(64 * NW), 0, st, p);
+  const unsigned grid = attn_grid(&p, 32 * NW / KS);
+  hipLaunchKernelGGL((kla_attn_kernel<D, NW, KS>), dim3(grid), dim3(64 * NW), 0, st, p);
   return hipGetLastError();
 }
 
@@ -476,11 +533,24 @@ hipError_t launch_attn_f32(AttnParams p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Which tiling, by the workgroups that tiles of 128 queries make:
+// - 64 queries, keys in two groups, where those are at most half the CUs (100 queries, 3,000
+//   keys, 16 heads: 41 us against 56 with 128 queries; 500 queries and keys, 4 heads: 12, 14);
+// - 128 queries, keys in two groups, for dense batches of at most two of them a CU (4,096
+//   tokens, 16 heads: 81 us against 93; 2,048: 37, 41); packed sequences are uneven, and lose
+//   (8 of 1,000 to 8,000 tokens: 172 us against 154);
+// - 256 queries where that still makes two workgroups a CU and sequences are long (16,384
+//   tokens, 16 heads: 1,002 us against 1,048; 4,096 tokens, 32 heads: 140, 154);
+// - 128 queries else (12 packed sequences of 200 to 4,096 tokens, 16 heads: 95 us, with 256
+//   queries 102, with two groups 110).
 template <int D>
 hipError_t launch_attn_d(const AttnParams &p, hipStream_t st) {
-  // 256 queries to a workgroup where that still fills the GPU
-  if ((long long)p.B * p.Hq * p.Tq >= 256 * 256) return launch_attn_t<D, 8>(p, st);
-  return launch_attn_t<D, 4>(p, st);
+  const long long seqs = p.cu_q ? p.N : 1, heads = (long long)p.B * p.Hq;
+  const long long wgs = heads * (p.cu_q ? p.Tq / 128 + p.N : (p.Tq + 127) / 128);
+  if (wgs <= 128) return launch_attn_t<D, 4, 2>(p, st);
+  if (!p.cu_q && wgs <= 512) return launch_attn_t<D, 8, 2>(p, st);
+  if (heads * p.Tq >= 512 * 256 && p.Tq >= 2048 * seqs) return launch_attn_t<D, 8, 1>(p, st);
+  return launch_attn_t<D, 4, 1>(p, st);
 }
 
 }  // namespace
@@ -489,7 +559,7 @@ bool attn_supported(int dtype, int D) { return (dtype == 0 || dtype == 1) && (D 
 
 // The finest tiling's workgroups fit an int.
 bool attn_grid_fits(const AttnArgs &a) {
-  const long long slots = (a.cu_q ? a.num_seqs : 1) + (long long)a.Tq / 128;
+  const long long slots = (a.cu_q ? a.num_seqs : 1) + (long long)a.Tq / 64;
   return slots * a.B * a.Hq <= 0x7fffffffLL;
 }
 

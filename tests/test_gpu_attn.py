@@ -103,6 +103,16 @@ def test_large(dtype, Hq, T):
     check(o, lse, q, k, v, 128 ** -0.5, dtype, heads=[0, Hq // 2, Hq - 1], rows=[0, 1, 63, 64, 1000, T - 130, T - 1])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Hq,T,cu", [(1, 16, 3000, None), (2, 32, 2100, None), (1, 16, 3000, [0, 700, 701, 3000])])
+def test_tilings(D, B, Hq, T, cu):
+    """128 queries with the keys in two groups, 256 queries, 128 queries."""
+    q, k, v = inputs(BF, B, Hq, 2, T, T, D, 10)
+    o, lse = kla.attn_fwd(q, k, v, cu_seqlens=None if cu is None else i32(cu))
+    rows = [0, 1, 127, 128, 255, 256, T - 1] if cu is None else None
+    check(o, lse, q, k, v, D ** -0.5, BF, cu, heads=[1, Hq - 1], rows=rows)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("scale", [4.0, -0.3, 0.0, 1e-3])
 def test_scales(dtype, scale):
