@@ -638,15 +638,16 @@ def _seqlens(cu_seqlens, cu_seqlens_host, B: int, dev):
         if cu_seqlens_host is not None:
             raise ValueError("cu_seqlens_host without cu_seqlens")
         return B, None
-    _fit(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
-    if cu_seqlens.numel() == 0:
+    n = cu_seqlens.numel()
+    _fit(cu_seqlens, "cu_seqlens", torch.int32, (n,), dev)
+    if n == 0:
         raise ValueError("cu_seqlens must hold at least one offset")
     host = cu_seqlens if cu_seqlens_host is None else cu_seqlens_host
-    if host.numel() != cu_seqlens.numel():
+    if host.numel() != n:
         raise ValueError("cu_seqlens_host does not mirror cu_seqlens")
-    if host.dtype != torch.int32 or host.device.type != "cpu" or not host.is_contiguous():
+    if host.is_cuda or host.dtype is not torch.int32 or not host.is_contiguous():
         host = host.to("cpu", torch.int32).contiguous()
-    return cu_seqlens.numel() - 1, host
+    return n - 1, host
 
 
 def _optional(t, name, dtype, shape, dev) -> None:
@@ -768,18 +769,29 @@ def glr_decode_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One token of the gated linear recurrence (kla_glr_decode_step): x, g [N, H, d];
     ``state`` [N, H, d] fp32 is updated in place.  Returns o [N, H, d]."""
-    dev = _device_of("glr_decode_step", x)
-    dtype = x.dtype
-    N, H, d = shape = _rank(x, "x", 3)
-    _fit(x, "x", dtype, shape, dev)
-    _fit(g, "g", dtype, shape, dev)
-    _fit(state, "state", torch.float32, shape, dev)
+    if not (isinstance(x, torch.Tensor) and isinstance(g, torch.Tensor) and isinstance(state, torch.Tensor)
+            and x.is_cuda and x.dtype in _DTYPES and g.dtype is x.dtype and state.dtype is torch.float32
+            and x.dim() == 3 and x.shape == g.shape == state.shape and x.device == g.device == state.device
+            and x.is_contiguous() and g.is_contiguous() and state.is_contiguous()):
+        _refuse_glr_step(x, g, state)
+    dev, (N, H, d) = x.device, x.shape
     if out is None:
         out = torch.empty_like(x)
     else:
-        _fit(out, "out", dtype, shape, dev)
-    _call("kla_glr_decode_step", dev, _ptr(x), _ptr(g), _ptr(state), _ptr(out), N, H, d, _DTYPES[dtype])
+        _fit(out, "out", x.dtype, x.shape, dev)
+    _call("kla_glr_decode_step", dev, x.data_ptr(), g.data_ptr(), state.data_ptr(), out.data_ptr(), N, H, d,
+          _DTYPES[x.dtype])
     return out
+
+
+# The single-token calls check their tensors in one expression, since their host time counts;
+# where it fails, these name what is wrong.
+def _refuse_glr_step(x, g, state) -> None:
+    dev = _device_of("glr_decode_step", x)
+    shape = _rank(x, "x", 3)
+    _need(x, "x", x.dtype, shape, dev)
+    _need(g, "g", x.dtype, shape, dev)
+    _need(state, "state", torch.float32, shape, dev)
 
 
 def attn_fwd(
@@ -839,15 +851,24 @@ def kv4_cache(num_pages: int, Hkv: int, page_size: int, D: int, device) -> Tuple
 
 
 def _cache_args(codes, scales, block_table, N: int, dev):
+    """Sizes of a cache and its block table: (num_pages, Hkv, page_size, D, max_pages)."""
+    if (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and isinstance(block_table, torch.Tensor)
+            and codes.dim() == 5 and block_table.dim() == 2):
+        P, two, H, page, half = codes.shape
+        M = block_table.shape[1]
+        if (two == 2 and scales.shape == (P, 2, H, page, half // 16) and block_table.shape[0] == N
+                and codes.dtype is scales.dtype is torch.uint8 and block_table.dtype is torch.int32
+                and codes.device == scales.device == block_table.device == dev
+                and codes.is_contiguous() and scales.is_contiguous() and block_table.is_contiguous()):
+            return P, H, page, 2 * half, M
     P, two, Hkv, page, half = _rank(codes, "codes", 5)
     if two != 2:
         raise ValueError(f"codes has shape {tuple(codes.shape)}, expected [num_pages, 2, Hkv, page_size, D/2]")
-    D = 2 * half
-    _fit(codes, "codes", torch.uint8, (P, 2, Hkv, page, half), dev)
-    _fit(scales, "scales", torch.uint8, (P, 2, Hkv, page, D // 32), dev)
+    _need(codes, "codes", torch.uint8, (P, 2, Hkv, page, half), dev)
+    _need(scales, "scales", torch.uint8, (P, 2, Hkv, page, half // 16), dev)
     _, M = _rank(block_table, "block_table", 2)
-    _fit(block_table, "block_table", torch.int32, (N, M), dev)
-    return P, Hkv, page, D, M
+    _need(block_table, "block_table", torch.int32, (N, M), dev)
+    return P, Hkv, page, 2 * half, M
 
 
 def kv4_append(
@@ -866,17 +887,19 @@ def kv4_append(
     int32 [N, max_pages]; start: int32 [N], the tokens that each sequence holds already;
     cu_seqlens as in chunk_fwd (None: N = B).
     """
-    dev = _device_of("kv4_append", k)
-    B, Hkv, T, D = shape = _rank(k, "k", 4)
-    _fit(k, "k", k.dtype, shape, dev)
-    _fit(v, "v", k.dtype, shape, dev)
+    if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.is_cuda and k.dtype in _DTYPES
+            and v.dtype is k.dtype and k.dim() == 4 and v.shape == k.shape and v.device == k.device
+            and k.is_contiguous() and v.is_contiguous()):
+        _need(k, "k", k.dtype, _rank(k, "k", 4), _device_of("kv4_append", k))
+        _need(v, "v", k.dtype, k.shape, k.device)
+    dev, (B, Hkv, T, D) = k.device, k.shape
     N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
     P, H, page, Dc, M = _cache_args(codes, scales, block_table, N, dev)
     if (H, Dc) != (Hkv, D):
         raise ValueError(f"k has {Hkv} heads of {D} channels, the cache {H} of {Dc}")
     _fit(start, "start", torch.int32, (N,), dev)
-    _call("kla_kv4_append", dev, _ptr(k), _ptr(v), _ptr(codes), _ptr(scales), _ptr(block_table), _ptr(start),
-          _ptr(cu_seqlens), _ptr(host), N, B, Hkv, T, D, P, page, M, _DTYPES[k.dtype])
+    _call("kla_kv4_append", dev, k.data_ptr(), v.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+          block_table.data_ptr(), start.data_ptr(), _ptr(cu_seqlens), _ptr(host), N, B, Hkv, T, D, P, page, M, _DTYPES[k.dtype])
 
 
 def kv4_read(
@@ -910,8 +933,8 @@ def kv4_read(
     else:
         _fit(out[0], "out[0]", dtype, shape, dev)
         _fit(out[1], "out[1]", dtype, shape, dev)
-    _call("kla_kv4_read", dev, _ptr(out[0]), _ptr(out[1]), _ptr(codes), _ptr(scales), _ptr(block_table), _ptr(start),
-          _ptr(cu_seqlens), _ptr(host), N, 1, Hkv, T, D, P, page, M, _DTYPES[dtype])
+    _call("kla_kv4_read", dev, out[0].data_ptr(), out[1].data_ptr(), codes.data_ptr(), scales.data_ptr(),
+          block_table.data_ptr(), start.data_ptr(), cu_seqlens.data_ptr(), host.data_ptr(), N, 1, Hkv, T, D, P, page, M, _DTYPES[dtype])
     return out
 
 
@@ -938,9 +961,10 @@ def attn_kv4_decode_step(
     scale: D ** -0.5 when None; max_len: a bound on seq_lens known to the host (the block
     table's room when None; a tight one makes fewer, fuller workgroups).  Returns o [N, Hq, D].
     """
-    dev = _device_of("attn_kv4_decode_step", q)
-    N, Hq, D = shape = _rank(q, "q", 3)
-    _fit(q, "q", q.dtype, shape, dev)
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dtype in _DTYPES and q.dim() == 3 and q.is_contiguous()):
+        _need(q, "q", q.dtype, _rank(q, "q", 3), _device_of("attn_kv4_decode_step", q))
+    dev, shape = q.device, q.shape
+    N, Hq, D = shape
     P, Hkv, page, Dc, M = _cache_args(codes, scales, block_table, N, dev)
     if Dc != D:
         raise ValueError(f"q has {D} channels, the cache {Dc}")
@@ -952,7 +976,7 @@ def attn_kv4_decode_step(
     max_len = M * page if max_len is None else int(max_len)
     dt = _DTYPES[q.dtype]
     ws = _scratch(workspace, lib().kla_attn_kv4_decode_workspace_bytes(N, Hq, Hkv, D, max_len, dt), dev)
-    _call("kla_attn_kv4_decode_step", dev, _ptr(q), _ptr(codes), _ptr(scales), _ptr(block_table), _ptr(seq_lens),
-          D ** -0.5 if scale is None else float(scale), _ptr(out), N, Hq, Hkv, D, P, page, M, max_len, dt, _ptr(ws),
+    _call("kla_attn_kv4_decode_step", dev, q.data_ptr(), codes.data_ptr(), scales.data_ptr(), block_table.data_ptr(),
+          seq_lens.data_ptr(), D ** -0.5 if scale is None else float(scale), out.data_ptr(), N, Hq, Hkv, D, P, page, M, max_len, dt, _ptr(ws),
           0 if ws is None else ws.numel())
     return out
