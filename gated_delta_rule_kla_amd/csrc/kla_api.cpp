@@ -15,6 +15,7 @@
 namespace {
 
 bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }  // int32 arrays
 
 // Enum-typed arguments come from C callers as plain ints and may hold any value; their
 // bytes are read as an int (a read as the C++ enum type is undefined outside the range
@@ -275,7 +276,8 @@ kla_status_t kv4_move(void *k, void *v, const void *codes, const void *scales, c
   if ((double)B * Hkv * T > (double)0x7fffffff) return KLA_ERR_SHAPE;
   if (num_seqs == 0 || (long long)B * T == 0) return KLA_OK;
   if (!k || !v || !codes || !scales || !table || !start) return KLA_ERR_NULL;
-  if (misaligned(k) || misaligned(v) || misaligned(codes) || misaligned(scales) || misaligned(table) || misaligned(start))
+  if (misaligned(k) || misaligned(v) || misaligned(codes) || misaligned(scales) || misaligned4(table) ||
+      misaligned4(start))
     return KLA_ERR_ALIGN;
   const kla::Kv4Cache c{const_cast<void *>(codes), const_cast<void *>(scales), table, num_pages, page_size, max_pages,
                         Hkv};
@@ -610,8 +612,8 @@ kla_status_t kla_attn_kv4_decode_step(const void *q, const void *codes, const vo
   if (!std::isfinite(scale)) return KLA_ERR_PARAM;
   if (N == 0) return KLA_OK;
   if (!q || !codes || !scales || !block_table || !seq_lens || !o) return KLA_ERR_NULL;
-  if (misaligned(q) || misaligned(codes) || misaligned(scales) || misaligned(block_table) || misaligned(seq_lens) ||
-      misaligned(o) || misaligned(workspace))
+  if (misaligned(q) || misaligned(codes) || misaligned(scales) || misaligned4(block_table) ||
+      misaligned4(seq_lens) || misaligned(o) || misaligned(workspace))
     return KLA_ERR_ALIGN;
   const size_t need = kla::kv4_decode_workspace_bytes(a);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KLA_ERR_WORKSPACE;

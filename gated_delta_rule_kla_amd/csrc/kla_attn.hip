@@ -102,7 +102,15 @@ __device__ void attend_one(const E *q, const E *k, const E *v, int n, const Attn
   for (int j0 = 0; j0 < n; j0 += 64) {
     float x = 0.f;
     const E *kr = k + (size_t)min(j0 + lane, n - 1) * D;
-    for (int d = 0; d < D; ++d) x = fmaf(Elem<E>::to_f32(q[d]) * sign, Elem<E>::to_f32(kr[d]), x);
+#pragma unroll 4
+    for (int d = 0; d < D; d += 16 / (int)sizeof(E)) {
+      const uint4 a = ldg16(q + d), b = ldg16(kr + d);
+      E ea[16 / sizeof(E)], eb[16 / sizeof(E)];
+      __builtin_memcpy(ea, &a, 16);
+      __builtin_memcpy(eb, &b, 16);
+#pragma unroll
+      for (unsigned i = 0; i < 16 / sizeof(E); ++i) x = fmaf(Elem<E>::to_f32(ea[i]) * sign, Elem<E>::to_f32(eb[i]), x);
+    }
     x = j0 + lane < n ? x * p.c : -INFINITY;
     float top = x;
 #pragma unroll

@@ -459,7 +459,8 @@ kla_status_t kla_pgdn_decode_step(const void *q, const void *k, const void *v,
  *                  A layer without heads passes H = 1 and its width as d.
  *   initial_state  [N, H, d] fp32, or NULL = zeros
  *   o              [B, H, T, d]  dtype, written for every token
- *   final_state    [N, H, d] fp32, or NULL = not written.  May alias initial_state.
+ *   final_state    [N, H, d] fp32, or NULL = not written.  May alias initial_state; no other
+ *                  aliasing is allowed.
  *   cu_seqlens, cu_seqlens_host, num_seqs (N), B, H, T: as kla_chunk_fwd, without its
  *                  limit on H
  *   workspace      kla_glr_chunk_workspace_bytes(...) bytes for the same arguments (16-byte
@@ -544,7 +545,8 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
  * Supported: D 64 or 128, either dtype.  Scores, softmax and sums are fp32; with BF16 the
  * weights are rounded to bf16 before they meet the values (half a step of 2^-8 each, as much
  * as o's own rounding).  Keys and values that a query does not see do not reach it, also
- * where they are infinite or NaN.  No workspace; results repeat bit for bit.  Status codes as
+ * where they are infinite or NaN (queries that such a value reaches are computed key by key,
+ * which is slow).  No workspace, no aliasing; results repeat bit for bit.  Status codes as
  * kla_chunk_fwd, KLA_ERR_PARAM for a scale that is not finite.
  */
 kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float scale, void *o, float *lse,
@@ -583,7 +585,8 @@ kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float sca
  * either's codes and scales, mixed: a place belongs to one token.
  *
  * Supported: D 64 or 128, page_size a multiple of 16 up to 2^20, either dtype; B * Hkv * T
- * below 2^31.  Other status codes as kla_chunk_fwd.  Pointers are 16-byte aligned.
+ * below 2^31.  Other status codes as kla_chunk_fwd.  block_table, start and seq_lens are
+ * 4-byte aligned, everything else 16-byte.
  */
 kla_status_t kla_kv4_append(const void *k, const void *v, void *codes, void *scales,
                             const int32_t *block_table, const int32_t *start,

@@ -255,6 +255,23 @@ def test_steps_in_a_graph_on_another_stream():
         now += 1
 
 
+def test_parts_of_a_batch():
+    """Slices of the block table, the lengths and the starts, which are aligned to 4 bytes only."""
+    lens = [40, 17, 33]
+    codes, scales, table, kv = fill(lens, 1, 64, 16)
+    assert table.shape[1] == 3
+    q = torch.randn(3, 4, 64, device=DEV).to(BF)
+    whole = kla.attn_kv4_decode_step(q, codes, scales, table, i32(lens))
+    part = kla.attn_kv4_decode_step(q[1:], codes, scales, table[1:], i32([0] + lens)[2:])
+    assert torch.equal(part, whole[1:])
+    k, v = make_kv([2, 2], 1, 64, BF, 5)
+    cu, host = packed([2, 2])
+    one, two = (codes.clone(), scales.clone()), (codes.clone(), scales.clone())
+    kla.kv4_append(k, v, *one, table[1:], i32([9, 17, 33])[1:], cu, host)
+    kla.kv4_append(k, v, *two, table[1:].clone(), i32([17, 33]), cu, host)
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1]) and not torch.equal(one[0], codes)
+
+
 def test_refusals():
     codes, scales = kla.kv4_cache(4, 2, 16, 64, DEV)
     q, k = torch.zeros(1, 4, 64, device=DEV), torch.zeros(1, 2, 1, 64, device=DEV)

@@ -100,7 +100,8 @@ def move(fn, **kw):
     (dict(dtype=5), -3), (dict(B=-1, N=-1), -2), (dict(Hkv=0), -2), (dict(T=-1), -2), (dict(P=0), -2),
     (dict(page=0), -2), (dict(M=0), -2), (dict(N=3), -2), (dict(D=96), -4), (dict(page=24), -4),
     (dict(page=1 << 21), -4), (dict(T=0x7fffffff), -2), (dict(T=1 << 28, Hkv=4), -2), (dict(k=None), -1),
-    (dict(codes=None), -1), (dict(start=None), -1), (dict(table=FAKE + 4), -8), (dict(scales=FAKE + 8), -8),
+    (dict(codes=None), -1), (dict(start=None), -1), (dict(table=FAKE + 2), -8), (dict(scales=FAKE + 8), -8),
+    (dict(start=FAKE + 1), -8),
     (dict(cu=FAKE, cuh=[0, 4, 9], B=1), -5), (dict(cu=FAKE, cuh=[0, 11, 10], B=1), -5), (dict(cu=FAKE, B=1), -1),
     (dict(cuh=[0, 4, 10]), -1), (dict(T=0, k=None), 0), (dict(B=0, N=0), 0),
 ])
@@ -121,7 +122,7 @@ def decode(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=5), -3), (dict(N=-1), -2), (dict(Hq=7), -2), (dict(Hq=0), -2), (dict(ml=-1), -2),
     (dict(ml=0x7fffffff), -2), (dict(D=32), -4), (dict(page=8), -4), (dict(scale=float("nan")), -11),
-    (dict(scale=float("inf")), -11), (dict(q=None), -1), (dict(lens=None), -1), (dict(q=FAKE + 2), -8),
+    (dict(scale=float("inf")), -11), (dict(q=None), -1), (dict(lens=None), -1), (dict(q=FAKE + 2), -8), (dict(lens=FAKE + 2), -8),
     (dict(ml=100000, M=10000), -7), (dict(ml=100000, M=10000, ws=FAKE, wsb=100), -7),
     (dict(N=1 << 20, Hq=1 << 14, Hkv=1 << 13), -2), (dict(N=0, q=None), 0),
 ])
