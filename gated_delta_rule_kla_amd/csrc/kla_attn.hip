@@ -242,11 +242,27 @@ __device__ __forceinline__ void finish(const AttnParams &p, const Span &s, int b
 #pragma unroll
     for (int j = 0; j < DB; ++j)
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        typedef E E4 __attribute__((ext_vector_type(4)));
-        const E4 w = {Elem<E>::from_f32(acc[j][i] * inv), Elem<E>::from_f32(acc[j][i + 1] * inv),
-                      Elem<E>::from_f32(acc[j][i + 2] * inv), Elem<E>::from_f32(acc[j][i + 3] * inv)};
-        *reinterpret_cast<E4 *>(O + 32 * j + 2 * i + 4 * h) = w;
+      for (int i = 0; i < 16; i += 8) {
+        if constexpr (sizeof(E) == 2) {
+          // channels 2 i + 4 h and 2 i + 8 + 4 h, four each: the halves change pieces, so that
+          // each stores eight in a row
+          u32x4 w;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bf16x2 lo = {(bf16)(acc[j][i + 2 * e] * inv), (bf16)(acc[j][i + 2 * e + 1] * inv)};
+            const bf16x2 hi = {(bf16)(acc[j][i + 4 + 2 * e] * inv), (bf16)(acc[j][i + 4 + 2 * e + 1] * inv)};
+            const auto c = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, lo),
+                                                            __builtin_bit_cast(unsigned, hi), false, false);
+            w[e] = c[0];
+            w[2 + e] = c[1];
+          }
+          *reinterpret_cast<u32x4 *>(O + 32 * j + 2 * i + 8 * h) = w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; e += 4)
+            *reinterpret_cast<f32x4 *>(O + 32 * j + 2 * (i + e) + 4 * h) =
+                f32x4{acc[j][i + e] * inv, acc[j][i + e + 1] * inv, acc[j][i + e + 2] * inv, acc[j][i + e + 3] * inv};
+        }
       }
     if (p.lse && h == 0)
       p.lse[(size_t)bh * p.Tq + s.q0 + qw + r] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
@@ -284,9 +300,6 @@ __global__ __launch_bounds__(64 * NW, NW / KS == 2 ? 1 : 2) void kla_attn_kernel
 
   const int qw = s.first + 32 * (wave % (NW / KS));  // this wave's first query
   const int qi = min(qw + r, s.lq - 1);              // this lane's (queries past the end repeat the last)
-  bf16x8 q[KJ];
-  load_q<D>(p, Q + (size_t)qi * D, h, q);
-
   f32x16 acc[DB];
 #pragma unroll
   for (int j = 0; j < DB; ++j)
@@ -310,6 +323,8 @@ __global__ __launch_bounds__(64 * NW, NW / KS == 2 ? 1 : 2) void kla_attn_kernel
   };
 
   if (steps > 0) fetch(0, 0);
+  bf16x8 q[KJ];
+  load_q<D>(p, Q + (size_t)qi * D, h, q);
   for (int t = 0; t < steps; ++t) {
     const int buf = t & 1;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
