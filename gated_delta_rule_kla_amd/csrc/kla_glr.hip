@@ -228,8 +228,9 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
   auto staged = [&](int t, int r) {
     return s.in[wave][t] + (r / P) * 1024 + ((r % P) * 16 + gw) * Lds::ROWB + cg * V * (int)sizeof(E);
   };
-  // a wave has rows in the tile from base on (all of them but in a sequence's last tile)
-  const int w0 = wave * GW * R;
+  // A wave has rows in the tile from base on, but in a sequence's last tile.  The branch pays
+  // where sequences may be short; in tiles of 1,024 rows, for long ones, it cost 4%.
+  const int w0 = R == 8 ? 0 : wave * GW * R;
   if (w0 < len) fetch(0);
 
   int buf = 0;
@@ -243,7 +244,7 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
       A[i] = 1.f;
       C[i] = 0.f;
     }
-    if (base + w0 < len) {
+    if (R == 8 || base + w0 < len) {
       if constexpr (PIECES) {
 #pragma unroll
         for (int i = 0; i < R / P; ++i)
@@ -344,7 +345,7 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
         }
       }
     }
-    if (MODE != GLR_MAPS && base + w0 < len) {
+    if (MODE != GLR_MAPS && (R == 8 || base + w0 < len)) {
       // the value before this thread's rows
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] = fmaf(row_shr<1>(1.f, A[i]), y[i], row_shr<1>(0.f, C[i]));

@@ -458,16 +458,17 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void kla_kv4_decode_ke
   }
 }
 
-// The runs of one (sequence, query head).  Eight groups of threads take every eighth run, four
-// channels to a thread, and meet in LDS: in one group's order the 512 runs of a sequence of
-// 131,072 tokens took 19 us, so 4.
-template <typename E, int D>
-__global__ __launch_bounds__(2 * D) void kla_kv4_join_kernel(KvDecodeParams p) {
-  constexpr int GROUPS = 8, LPG = D / 4;  // lanes of a group
+// The runs of one (sequence, query head): GROUPS groups of threads take every GROUPS-th run,
+// four channels to a thread, and meet in LDS.  Few runs: 8 groups over all channels; many: 32
+// groups over 32 channels of them (16 heads of 256 runs: 4.7 us against 5.9 with 8 groups,
+// and 19 run by run).
+template <typename E, int D, int GROUPS, int CH>
+__global__ __launch_bounds__(GROUPS *CH / 4) void kla_kv4_join_kernel(KvDecodeParams p) {
+  constexpr int LPG = CH / 4, PARTS = D / CH;  // lanes of a group, workgroups of a row
   __shared__ f32x4 s_o[GROUPS][LPG];
   __shared__ float s_l[GROUPS];
-  const size_t row = blockIdx.x;
-  const int g = threadIdx.x / LPG, lane = threadIdx.x % LPG;
+  const size_t row = blockIdx.x / PARTS;
+  const int g = threadIdx.x / LPG, lane = threadIdx.x % LPG, ch = (blockIdx.x % PARTS) * CH + 4 * lane;
   const float *ml = p.part_ml + row * p.splits * 2;
   float m = -INFINITY;
   for (int s = threadIdx.x % 64; s < p.splits; s += 64) m = fmaxf(m, ml[2 * s]);
@@ -476,7 +477,7 @@ __global__ __launch_bounds__(2 * D) void kla_kv4_join_kernel(KvDecodeParams p) {
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  const float *po = p.part_o + row * p.splits * D + 4 * lane;
+  const float *po = p.part_o + row * p.splits * D + ch;
 #pragma unroll 4
   for (int s = g; s < p.splits; s += GROUPS) {
     const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
@@ -497,7 +498,7 @@ __global__ __launch_bounds__(2 * D) void kla_kv4_join_kernel(KvDecodeParams p) {
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    ((E *)p.o)[row * D + 4 * lane + i] = Elem<E>::from_f32(l == 0.f ? 0.f : o[i] / l);
+    ((E *)p.o)[row * D + ch + i] = Elem<E>::from_f32(l == 0.f ? 0.f : o[i] / l);
 }
 
 template <typename E, bool READ>
@@ -513,8 +514,11 @@ template <typename E, int D>
 hipError_t launch_kv4_decode(const KvDecodeParams &p, hipStream_t st) {
   const long long grid = (long long)p.N * p.kv.Hkv * p.GB * p.splits;
   hipLaunchKernelGGL((kla_kv4_decode_kernel<E, D>), dim3((unsigned)grid), dim3(256), 0, st, p);
-  if (p.splits > 1)
-    hipLaunchKernelGGL((kla_kv4_join_kernel<E, D>), dim3((unsigned)((long long)p.N * p.Hq)), dim3(2 * D), 0, st, p);
+  const long long rows = (long long)p.N * p.Hq;
+  if (p.splits > 32)
+    hipLaunchKernelGGL((kla_kv4_join_kernel<E, D, 32, 32>), dim3((unsigned)(rows * (D / 32))), dim3(256), 0, st, p);
+  else if (p.splits > 1)
+    hipLaunchKernelGGL((kla_kv4_join_kernel<E, D, 8, D>), dim3((unsigned)rows), dim3(2 * D), 0, st, p);
   return hipGetLastError();
 }
 
@@ -523,12 +527,13 @@ KvParams kv_params(const Kv4Cache &c) {
 }
 
 // Runs of the sequences: as many as bring about 1,024 workgroups (64 ragged sequences of 4
-// heads: 75 us, with 512 workgroups 88, with 2,048 78), of 512 tokens at least (four tiles a
-// wave; one sequence of 131,072 tokens: 19.3 us, with 256 tokens 21.6) and KV_MAX_PER at most.
+// heads: 75 us, with 512 workgroups 88, with 2,048 78), of 384 tokens at least (three tiles a
+// wave; one sequence of 131,072 tokens, 2 heads: 16.6 us, with 256 tokens 19.0, with 512 18.2)
+// and KV_MAX_PER at most.
 void kv4_runs(const Kv4DecodeArgs &a, int *splits, int *per) {
   const long long GB = (a.Hq / a.c.Hkv + 15) / 16, base = (long long)a.N * a.c.Hkv * GB;
   long long want = std::max<long long>(1, 1024 / std::max<long long>(1, base));
-  want = std::min(want, std::max<long long>(1, a.max_len / 512));
+  want = std::min(want, std::max<long long>(1, a.max_len / 384));
   long long len = (a.max_len + want - 1) / want;
   len = std::min<long long>(KV_MAX_PER, std::max<long long>(128, (len + 127) / 128 * 128));
   *per = (int)len;
@@ -547,7 +552,7 @@ bool kv4_decode_grid_fits(const Kv4DecodeArgs &a) {
   int splits, per;
   kv4_runs(a, &splits, &per);
   return (long long)a.N * a.c.Hkv * ((a.Hq / a.c.Hkv + 15) / 16) * splits <= 0x7fffffffLL &&
-         (long long)a.N * a.Hq <= 0x7fffffffLL;
+         (long long)a.N * a.Hq * (a.D / 32) <= 0x7fffffffLL;
 }
 
 hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,
