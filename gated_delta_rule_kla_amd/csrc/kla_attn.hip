@@ -184,15 +184,15 @@ __device__ __forceinline__ void load_q(const AttnParams &p, const bf16 *row, int
 // only moves when a score exceeds it by 2^LAG: weights up to 2^LAG cost no precision (they are
 // floating point, and the sum too), and most tiles leave the output as it is.
 constexpr float LAG = 8.f;
-template <int DB>
+template <int DB, int KB>
 __device__ __forceinline__ void softmax_tile(const f32x16 *x, float c, float &m, float &l, f32x16 *acc, bf16x8 *pt) {
   float t4[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t4[i] = fmaxf(x[0][i], x[1][i]);
+  for (int i = 0; i < 4; ++i) t4[i] = x[0][i];
 #pragma unroll
-  for (int k = 4; k < 16; k += 4)
+  for (int k = 4; k < 16 * KB; k += 4)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(fmaxf(t4[i], x[0][k + i]), x[1][k + i]);
+    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(t4[i], x[k / 16][k % 16 + i]);
   float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
   {  // the other half's
     const auto w = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, top), __builtin_bit_cast(unsigned, top), false, false);
@@ -211,7 +211,7 @@ __device__ __forceinline__ void softmax_tile(const f32x16 *x, float c, float &m,
   const float base = m == -INFINITY ? 0.f : m;
   float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb)
+  for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float e = __builtin_amdgcn_exp2f(fmaf(x[kb][i], c, -base));
@@ -276,15 +276,15 @@ __device__ __forceinline__ void finish(const AttnParams &p, const Span &s, int b
   }
 }
 
-// KS = 2: two groups of NW / 2 waves share the queries and take every second tile of keys, and
-// join at the end, so that a workgroup's chain of tiles is half as long.
-template <int D, int NW, int KS>
-__global__ __launch_bounds__(64 * NW, NW / KS == 2 ? 1 : 2) void kla_attn_kernel(AttnParams p) {
-  constexpr int BM = 32 * NW / KS, BN = 64;
+// KS groups of NW / KS waves share the queries and take every KS-th tile of BN keys, and join at
+// the end, so that a workgroup's chain of tiles is as much shorter.
+template <int D, int NW, int KS, int BN>
+__global__ __launch_bounds__(64 * NW, 2) void kla_attn_kernel(AttnParams p) {
+  constexpr int BM = 32 * NW / KS, KB = BN / 32;  // queries, tiles of 32 keys
   constexpr int PPR = D / 8;         // 16-byte pieces of a row
   constexpr int RPI = 64 / PPR;      // rows of one direct load
   constexpr int KJ = D / 16, DB = D / 32;
-  __shared__ __attribute__((aligned(1024))) bf16 s_k[2][KS * BN * D], s_v[2][KS * BN * D];
+  __shared__ __attribute__((aligned(1024))) bf16 s_kv[2][2][KS * BN * D];  // K and V, two buffers each
 
   int bh, slot;
   place(p, blockIdx.x, &bh, &slot);
@@ -317,8 +317,8 @@ __global__ __launch_bounds__(64 * NW, NW / KS == 2 ? 1 : 2) void kla_attn_kernel
     for (int i = 0; i < KS * BN / RPI / NW; ++i) {
       const int r0 = (wave * (KS * BN / RPI / NW) + i) * RPI, row = r0 + lane / PPR, pc = lane % PPR;
       const size_t key = min(t * KS * BN + row, s.lk - 1);  // past the end: the last key, masked below
-      load_lds(K + key * D + 8 * (pc ^ (row & (PPR - 1))), s_k[buf] + r0 * D);
-      load_lds(V + key * D + 8 * (pc ^ ((row & 3) << 2 & (PPR - 1))), s_v[buf] + r0 * D);
+      load_lds(K + key * D + 8 * (pc ^ (row & (PPR - 1))), s_kv[0][buf] + r0 * D);
+      load_lds(V + key * D + 8 * (pc ^ ((row & 3) << 2 & (PPR - 1))), s_kv[1][buf] + r0 * D);
     }
   };
 
@@ -332,11 +332,11 @@ __global__ __launch_bounds__(64 * NW, NW / KS == 2 ? 1 : 2) void kla_attn_kernel
     if (t + 1 < steps) fetch(t + 1, buf ^ 1);
     const int key0 = (t * KS + group) * BN;
     if (key0 > last_key || qw >= s.lq) continue;
-    const bf16 *kt = s_k[buf] + group * BN * D, *vt = s_v[buf] + group * BN * D;
+    const bf16 *kt = s_kv[0][buf] + group * BN * D, *vt = s_kv[1][buf] + group * BN * D;
 
-    f32x16 x[2];
+    f32x16 x[KB];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[kb][i] = 0.f;
 #pragma unroll
@@ -345,42 +345,48 @@ __global__ __launch_bounds__(64 * NW, NW / KS == 2 ? 1 : 2) void kla_attn_kernel
     }
     if (key0 + BN - 1 > first_key) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (key0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 > qi + off) x[kb][i] = -INFINITY;
     }
-    bf16x8 pt[4];
-    softmax_tile<DB>(x, p.c, m, l, acc, pt);
+    bf16x8 pt[2 * KB];
+    softmax_tile<DB, KB>(x, p.c, m, l, acc, pt);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+    for (int kk = 0; kk < 2 * KB; ++kk)
 #pragma unroll
       for (int j = 0; j < DB; ++j)
         acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_operand<D>(vt, kk, j, lane), pt[kk], acc[j], 0, 0, 0);
   }
-  if constexpr (KS == 2) {
-    // the second group's results through LDS, lane to lane: the layouts are the same
-    f32x4 *ex = reinterpret_cast<f32x4 *>(wave % (NW / 2) < NW / 4 ? &s_k[0][0] : &s_v[0][0]) +
-                (wave % (NW / 4)) * (4 * DB + 1) * 64 + lane;
+  if constexpr (KS > 1) {
+    // the other groups' results through LDS, lane to lane: the layouts are the same
+    constexpr int WG = NW / KS, SIZE = (4 * DB + 1) * 64;  // waves of a group, f32x4 of a wave
+    static_assert((KS - 1) * WG * SIZE * 16 <= 4 * KS * BN * D * 2, "exchange");
+    f32x4 *const ex = reinterpret_cast<f32x4 *>(s_kv) + lane;
     __syncthreads();
-    if (group == 1) {
+    if (group > 0) {
+      f32x4 *const to = ex + (wave - WG) * SIZE;
 #pragma unroll
       for (int j = 0; j < DB; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ex[(4 * j + i) * 64] = f32x4{acc[j][4 * i], acc[j][4 * i + 1], acc[j][4 * i + 2], acc[j][4 * i + 3]};
-      ex[4 * DB * 64] = f32x4{m, l, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i) to[(4 * j + i) * 64] = f32x4{acc[j][4 * i], acc[j][4 * i + 1], acc[j][4 * i + 2], acc[j][4 * i + 3]};
+      to[4 * DB * 64] = f32x4{m, l, 0.f, 0.f};
     }
     __syncthreads();
-    if (group == 1) return;
-    const f32x4 ml = ex[4 * DB * 64];
-    const float mn = fmaxf(m, ml[0]), base = mn == -INFINITY ? 0.f : mn;
-    const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(ml[0] - base);
-    m = mn;
-    l = l * f0 + ml[1] * f1;
+    if (group > 0) return;
 #pragma unroll
-    for (int j = 0; j < DB; ++j)
+    for (int g = 1; g < KS; ++g) {
+      const f32x4 *const from = ex + (wave + (g - 1) * WG) * SIZE;
+      const f32x4 ml = from[4 * DB * 64];
+      const float mn = fmaxf(m, ml[0]), base = mn == -INFINITY ? 0.f : mn;
+      const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(ml[0] - base);
+      m = mn;
+      l = l * f0 + ml[1] * f1;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[j][i] = acc[j][i] * f0 + ex[(4 * j + i / 4) * 64][i % 4] * f1;
+      for (int j = 0; j < DB; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[j][i] = acc[j][i] * f0 + from[(4 * j + i / 4) * 64][i % 4] * f1;
+    }
   }
   finish<bf16, D>(p, s, bh, qw, acc, m, l, K, V);
 }
@@ -542,10 +548,10 @@ unsigned attn_grid(AttnParams *p, int BM) {
   return (unsigned)((long long)p->slots * p->B * p->Hq);
 }
 
-template <int D, int NW, int KS>
+template <int D, int NW, int KS, int BN>
 hipError_t launch_attn_t(AttnParams p, hipStream_t st) {
   const unsigned grid = attn_grid(&p, 32 * NW / KS);
-  hipLaunchKernelGGL((kla_attn_kernel<D, NW, KS>), dim3(grid), dim3(64 * NW), 0, st, p);
+  hipLaunchKernelGGL((kla_attn_kernel<D, NW, KS, BN>), dim3(grid), dim3(64 * NW), 0, st, p);
   return hipGetLastError();
 }
 
@@ -557,23 +563,31 @@ hipError_t launch_attn_f32(AttnParams p, hipStream_t st) {
 }
 
 // Which tiling, by the workgroups that tiles of 128 queries make:
-// - 64 queries, keys in two groups, where those are at most half the CUs (100 queries, 3,000
-//   keys, 16 heads: 41 us against 56 with 128 queries; 500 queries and keys, 4 heads: 12, 14);
+// - 32 queries, keys in four groups, where those are at most a quarter of the CUs (100 queries,
+//   3,000 keys, 16 heads: 32 us, with two groups 37; 1,000 tokens, 8 heads: 15.3, 16.0; at 128
+//   of them, 1,000 tokens of 16 heads, 21.5, 16.5);
+// - 64 queries, keys in two groups, where those are at most half the CUs (1,000 tokens, 16
+//   heads: 16.5 us, 128 queries 20.0), and up to one a CU for dense batches whose later queries
+//   see most keys, so that their work is uneven (2,048 tokens, 16 heads: 32.5 us, 128 queries
+//   36.6; 8 times 128 queries of 2,000 keys: 44.8, 40.6).  Two groups' tiles make 16 KB each of
+//   K and V: 32 keys of 128 channels (64: 18.1 us for 1,000 tokens), 64 of 64 (2,048 tokens
+//   20.3 us, 32 keys 23.7);
 // - 128 queries, keys in two groups, for dense batches of at most two of them a CU (4,096
-//   tokens, 16 heads: 81 us against 93; 2,048: 37, 41); packed sequences are uneven, and lose
-//   (8 of 1,000 to 8,000 tokens: 172 us against 154);
+//   tokens, 16 heads: 81 us against 93); packed sequences are uneven, and lose (8 of 1,000 to
+//   8,000 tokens: 172 us against 154);
 // - 256 queries where that still makes two workgroups a CU and sequences are long (16,384
-//   tokens, 16 heads: 1,002 us against 1,048; 4,096 tokens, 32 heads: 140, 154);
+//   tokens, 16 heads: 985 us against 1,048; 4,096 tokens, 32 heads: 140, 154);
 // - 128 queries else (12 packed sequences of 200 to 4,096 tokens, 16 heads: 95 us, with 256
-//   queries 102, with two groups 110).
+//   queries 97, with two groups 110).
 template <int D>
 hipError_t launch_attn_d(const AttnParams &p, hipStream_t st) {
   const long long seqs = p.cu_q ? p.N : 1, heads = (long long)p.B * p.Hq;
   const long long wgs = heads * (p.cu_q ? p.Tq / 128 + p.N : (p.Tq + 127) / 128);
-  if (wgs <= 128) return launch_attn_t<D, 4, 2>(p, st);
-  if (!p.cu_q && wgs <= 512) return launch_attn_t<D, 8, 2>(p, st);
-  if (heads * p.Tq >= 512 * 256 && p.Tq >= 2048 * seqs) return launch_attn_t<D, 8, 1>(p, st);
-  return launch_attn_t<D, 4, 1>(p, st);
+  if (wgs <= 64) return launch_attn_t<D, 4, 4, 32>(p, st);
+  if (wgs <= 128 || (!p.cu_q && wgs <= 256 && p.Tk < 2 * p.Tq)) return launch_attn_t<D, 4, 2, 4096 / D>(p, st);
+  if (!p.cu_q && wgs <= 512) return launch_attn_t<D, 8, 2, 64>(p, st);
+  if (heads * p.Tq >= 512 * 256 && p.Tq >= 2048 * seqs) return launch_attn_t<D, 8, 1, 64>(p, st);
+  return launch_attn_t<D, 4, 1, 64>(p, st);
 }
 
 }  // namespace
@@ -582,7 +596,7 @@ bool attn_supported(int dtype, int D) { return (dtype == 0 || dtype == 1) && (D 
 
 // The finest tiling's workgroups fit an int.
 bool attn_grid_fits(const AttnArgs &a) {
-  const long long slots = (a.cu_q ? a.num_seqs : 1) + (long long)a.Tq / 64;
+  const long long slots = (a.cu_q ? a.num_seqs : 1) + (long long)a.Tq / 32;
   return slots * a.B * a.Hq <= 0x7fffffffLL;
 }
 

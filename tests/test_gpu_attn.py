@@ -104,9 +104,12 @@ def test_large(dtype, Hq, T):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("B,Hq,T,cu", [(1, 16, 3000, None), (2, 32, 2100, None), (1, 16, 3000, [0, 700, 701, 3000])])
+@pytest.mark.parametrize("B,Hq,T,cu", [
+    (1, 8, 1000, None), (1, 16, 900, None), (1, 16, 2000, None), (1, 16, 3000, None), (2, 32, 2100, None),
+    (1, 8, 1000, [0, 1, 1, 34, 600, 1000]), (1, 4, 2500, [0, 1200, 1201, 2500]), (1, 16, 3000, [0, 700, 701, 3000])])
 def test_tilings(D, B, Hq, T, cu):
-    """128 queries with the keys in two groups, 256 queries, 128 queries."""
+    """32, 64, 64 and 128 queries with the keys in groups, 256 queries; packed: 64 queries with
+    the keys in groups twice, 128 queries."""
     q, k, v = inputs(BF, B, Hq, 2, T, T, D, 10)
     o, lse = kla.attn_fwd(q, k, v, cu_seqlens=None if cu is None else i32(cu))
     rows = [0, 1, 127, 128, 255, 256, T - 1] if cu is None else None
