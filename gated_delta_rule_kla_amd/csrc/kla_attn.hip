@@ -83,13 +83,12 @@ __device__ __forceinline__ void place(const AttnParams &p, unsigned id, int *bh,
   }
 }
 
-// 1 KB straight from global memory into LDS: lane i's 16 bytes land at dst + 16 i.  In asm,
-// since the compiler makes the next LDS read wait for the builtin's load, also where it goes to
-// the other buffer; the kernel itself waits (vmcnt) before the barrier that ends a tile.  It
-// has no output register.
-__device__ __forceinline__ void load_lds(const void *src, void *dst) {
-  const unsigned at = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)dst);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+// 1 KB straight from global memory, at a scalar address and each lane's byte offset, into LDS
+// at byte `at`: lane i's 16 bytes land 16 i behind.  In asm, since the compiler makes the next
+// LDS read wait for the builtin's load, also where it goes to the other buffer; the kernel
+// itself waits (vmcnt) before the barrier that ends a tile.  It has no output register.
+__device__ __forceinline__ void load_lds(const bf16 *src, unsigned lane_at, unsigned at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(lane_at), "s"(src) : "memory");
 }
 
 // One query against keys 0 .. n-1 by one wave, key by key.
@@ -312,13 +311,35 @@ __global__ __launch_bounds__(64 * NW, 2) void kla_attn_kernel(AttnParams p) {
   const int steps = seen > 0 ? (seen + KS * BN - 1) / (KS * BN) : 0;
   const int first_key = qw + off, last_key = min(qw + 31, s.lq - 1) + off;  // of the wave's first and last query
 
-  auto fetch = [&](int t, int buf) {
+  // Each wave brings NP pieces of 1 KB of K and of V.  In a whole tile their places are a scalar
+  // address and lane offsets that stay: worked out per load, they took a tenth of a tile's time.
+  constexpr int NP = KS * BN / RPI / NW;
+  static_assert(NP * RPI * NW == KS * BN, "pieces");
+  unsigned ko[NP], vo[NP];
 #pragma unroll
-    for (int i = 0; i < KS * BN / RPI / NW; ++i) {
-      const int r0 = (wave * (KS * BN / RPI / NW) + i) * RPI, row = r0 + lane / PPR, pc = lane % PPR;
-      const size_t key = min(t * KS * BN + row, s.lk - 1);  // past the end: the last key, masked below
-      load_lds(K + key * D + 8 * (pc ^ (row & (PPR - 1))), s_kv[0][buf] + r0 * D);
-      load_lds(V + key * D + 8 * (pc ^ ((row & 3) << 2 & (PPR - 1))), s_kv[1][buf] + r0 * D);
+  for (int i = 0; i < NP; ++i) {
+    const int row = (wave * NP + i) * RPI + lane / PPR, pc = lane % PPR;
+    ko[i] = 2 * (row * D + 8 * (pc ^ (row & (PPR - 1))));
+    vo[i] = 2 * (row * D + 8 * (pc ^ ((row & 3) << 2 & (PPR - 1))));
+  }
+  const unsigned lds = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)&s_kv[0][0][0] + wave * NP * 1024;
+  auto fetch = [&](int t, int buf) {
+    const bf16 *const kt = K + (size_t)t * KS * BN * D, *const vt = V + (size_t)t * KS * BN * D;
+    const int left = s.lk - t * KS * BN;
+    const unsigned to = lds + buf * KS * BN * D * 2;
+    if (left >= KS * BN) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        load_lds(kt, ko[i], to + i * 1024);
+        load_lds(vt, vo[i], to + 2 * KS * BN * D * 2 + i * 1024);
+      }
+    } else {  // past the end: the last key, masked below
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int row = (wave * NP + i) * RPI + lane / PPR, over = 2 * D * max(row - (left - 1), 0);
+        load_lds(kt, ko[i] - over, to + i * 1024);
+        load_lds(vt, vo[i] - over, to + 2 * KS * BN * D * 2 + i * 1024);
+      }
     }
   };
 
@@ -336,13 +357,29 @@ __global__ __launch_bounds__(64 * NW, 2) void kla_attn_kernel(AttnParams p) {
 
     f32x16 x[KB];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[kb][i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < KJ; ++j)
+    for (int j = 0; j < KJ; ++j)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
         x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_operand<D>(kt, kb, j, lane), q[j], x[kb], 0, 0, 0);
+    // eight operands are read ahead of the products, and the first of V's ahead of the softmax:
+    // left to the compiler, each product waits for its own read
+    constexpr int AHEAD = KJ * KB < 8 ? KJ * KB : 8, VA = KB == 1 ? 2 : 1;
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int j = 0; j < KJ * KB - AHEAD; ++j) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
+    bf16x8 va[VA][DB];
+#pragma unroll
+    for (int kk = 0; kk < VA; ++kk)
+#pragma unroll
+      for (int j = 0; j < DB; ++j) va[kk][j] = v_operand<D>(vt, kk, j, lane);
     if (key0 + BN - 1 > first_key) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
@@ -356,7 +393,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kla_attn_kernel(AttnParams p) {
     for (int kk = 0; kk < 2 * KB; ++kk)
 #pragma unroll
       for (int j = 0; j < DB; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_operand<D>(vt, kk, j, lane), pt[kk], acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kk < VA ? va[kk][j] : v_operand<D>(vt, kk, j, lane), pt[kk], acc[j], 0, 0, 0);
   }
   if constexpr (KS > 1) {
     // the other groups' results through LDS, lane to lane: the layouts are the same
