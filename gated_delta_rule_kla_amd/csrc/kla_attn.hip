@@ -5,8 +5,8 @@
 //
 // One pass over the keys with a running maximum and sum.  Each wave of a workgroup holds 32
 // queries of one head, their 32 x D output and statistics in registers, and all waves share
-// tiles of 64 keys and values in LDS, two of them: while one is used, the next arrives by
-// direct global-to-LDS loads.  Both products run transposed on v_mfma_f32_32x32x16_bf16: S^T =
+// tiles of 64 (or 32) keys and values in LDS, two of them: while one is used, the next arrives
+// by direct global-to-LDS loads.  Both products run transposed on v_mfma_f32_32x32x16_bf16: S^T =
 // K Q^T puts one query in each lane (pair), so maxima and sums need one exchange between the
 // two halves of a wave, and S^T's registers, rounded to bf16, are the right operand P^T of
 // O^T = V^T P^T as they stand: its contraction slots are taken in the order in which the
@@ -601,21 +601,21 @@ hipError_t launch_attn_f32(AttnParams p, hipStream_t st) {
 
 // Which tiling, by the workgroups that tiles of 128 queries make:
 // - 32 queries, keys in four groups, where those are at most a quarter of the CUs (100 queries,
-//   3,000 keys, 16 heads: 32 us, with two groups 37; 1,000 tokens, 8 heads: 15.3, 16.0; at 128
+//   3,000 keys, 16 heads: 33 us, with two groups 38; 1,000 tokens, 8 heads: 15.5, 16.1; at 128
 //   of them, 1,000 tokens of 16 heads, 21.5, 16.5);
 // - 64 queries, keys in two groups, where those are at most half the CUs (1,000 tokens, 16
-//   heads: 16.5 us, 128 queries 20.0), and up to one a CU for dense batches whose later queries
-//   see most keys, so that their work is uneven (2,048 tokens, 16 heads: 32.5 us, 128 queries
-//   36.6; 8 times 128 queries of 2,000 keys: 44.8, 40.6).  Two groups' tiles make 16 KB each of
-//   K and V: 32 keys of 128 channels (64: 18.1 us for 1,000 tokens), 64 of 64 (2,048 tokens
-//   20.3 us, 32 keys 23.7);
+//   heads: 16.5 us, 128 queries 19.0), and up to one a CU for dense batches whose later queries
+//   see most keys, so that their work is uneven (2,048 tokens, 16 heads: 30.7 us, 128 queries
+//   32.8; 8 times 128 queries of 2,000 keys: 42.1, 37.7).  Two groups' tiles make 16 KB each of
+//   K and V: 32 keys of 128 channels (64: 17.7 us for 1,000 tokens), 64 of 64 (2,048 tokens
+//   19.1 us, 32 keys 19.9);
 // - 128 queries, keys in two groups, for dense batches of at most two of them a CU (4,096
-//   tokens, 16 heads: 81 us against 93); packed sequences are uneven, and lose (8 of 1,000 to
-//   8,000 tokens: 172 us against 154);
+//   tokens, 16 heads: 74 us against 83); packed sequences are uneven, and lose (8 of 1,000 to
+//   8,000 tokens: 163 us against 140);
 // - 256 queries where that still makes two workgroups a CU and sequences are long (16,384
-//   tokens, 16 heads: 985 us against 1,048; 4,096 tokens, 32 heads: 140, 154);
-// - 128 queries else (12 packed sequences of 200 to 4,096 tokens, 16 heads: 95 us, with 256
-//   queries 97, with two groups 110).
+//   tokens, 16 heads: 937 us against 978; 4,096 tokens, 32 heads: 128, 139);
+// - 128 queries else (12 packed sequences of 200 to 4,096 tokens, 16 heads: 88 us, with 256
+//   queries 90, with two groups 99).
 template <int D>
 hipError_t launch_attn_d(const AttnParams &p, hipStream_t st) {
   const long long seqs = p.cu_q ? p.N : 1, heads = (long long)p.B * p.Hq;
