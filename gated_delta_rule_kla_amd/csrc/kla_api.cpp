@@ -234,7 +234,7 @@ kla_status_t check_glr(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host
                        int d, int dtype, kla::GlrArgs *a) {
   if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
   if (B < 0 || H <= 0 || T < 0 || T > kMaxTokens || d <= 0 || d > (1 << 24) || num_seqs < 0) return KLA_ERR_SHAPE;
-  if ((long long)B * H > 0x7fffffffLL || (long long)B * H * T > (1LL << 40)) return KLA_ERR_SHAPE;
+  if ((long long)B * H > 0x7fffffffLL || (double)B * H * T > (double)(1LL << 40)) return KLA_ERR_SHAPE;
   *a = kla::GlrArgs{};
   const kla_status_t st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, T, &a->longest);
   if (st != KLA_OK) return st;
@@ -273,7 +273,7 @@ kla_status_t kv4_move(void *k, void *v, const void *codes, const void *scales, c
   int longest;
   st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, T, &longest);
   if (st != KLA_OK) return st;
-  if ((double)B * Hkv * T > (double)0x7fffffff) return KLA_ERR_SHAPE;
+  if ((double)B * Hkv * T > (double)0x7fffffff || !kla::kv4_move_grid_fits(B, Hkv, T)) return KLA_ERR_SHAPE;
   if (num_seqs == 0 || (long long)B * T == 0) return KLA_OK;
   if (!k || !v || !codes || !scales || !table || !start) return KLA_ERR_NULL;
   if (misaligned(k) || misaligned(v) || misaligned(codes) || misaligned(scales) || misaligned4(table) ||
@@ -572,7 +572,7 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
   const int dtype = raw(dtype_);
   if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
   if (N < 0 || H <= 0 || d <= 0 || (long long)N * H > 0x7fffffffLL) return KLA_ERR_SHAPE;
-  if ((double)N * H * d > (double)(1LL << 38)) return KLA_ERR_SHAPE;  // 256 channels to a workgroup at least
+  if (!kla::glr_step_fits((size_t)N * H * d, dtype)) return KLA_ERR_SHAPE;
   if (N == 0) return KLA_OK;
   if (!x || !g || !state || !o) return KLA_ERR_NULL;
   if (misaligned(x) || misaligned(g) || misaligned(state) || misaligned(o)) return KLA_ERR_ALIGN;

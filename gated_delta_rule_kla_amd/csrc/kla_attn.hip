@@ -165,14 +165,11 @@ __device__ __forceinline__ void load_q(const AttnParams &p, const bf16 *row, int
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) q[j] = __builtin_bit_cast(bf16x8, ldg16(row + 16 * j + 8 * h));
   if (p.flip) {
-    const unsigned a = p.flip == 1 ? 0xffffffffu : 0u, x = p.flip == 1 ? 0x80008000u : 0u;
+    const float sign = p.flip == 1 ? -1.f : 0.f;
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      u32x4 u = __builtin_bit_cast(u32x4, q[j]);
+    for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = (u[i] & a) ^ x;
-      q[j] = __builtin_bit_cast(bf16x8, u);
-    }
+      for (int i = 0; i < 8; ++i) q[j][i] = (bf16)((float)q[j][i] * sign);
   }
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) asm volatile("" : "+v"(q[j]));
@@ -631,10 +628,11 @@ hipError_t launch_attn_d(const AttnParams &p, hipStream_t st) {
 
 bool attn_supported(int dtype, int D) { return (dtype == 0 || dtype == 1) && (D == 64 || D == 128); }
 
-// The finest tiling's workgroups fit an int.
+// Tiles of 128 queries, 256 threads each; finer ones are for few of them, tiles of 256 are as
+// many threads.
 bool attn_grid_fits(const AttnArgs &a) {
-  const long long slots = (a.cu_q ? a.num_seqs : 1) + (long long)a.Tq / 32;
-  return slots * a.B * a.Hq <= 0x7fffffffLL;
+  const double slots = (a.cu_q ? a.num_seqs : 1) + a.Tq / 128;
+  return launch_fits(slots * a.B * a.Hq, 512);
 }
 
 hipError_t launch_attn(const AttnArgs &a, hipStream_t st) {

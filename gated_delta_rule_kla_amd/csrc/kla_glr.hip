@@ -522,8 +522,10 @@ hipError_t launch_glr(const GlrParams &p, const GlrPlan &plan, hipStream_t st) {
 }  // namespace
 
 bool glr_grid_fits(const GlrArgs &a) {
-  // slices of 4 channels at least, in groups of up to 32, over a multiple of 8 groups
-  return ((double)a.num_seqs * a.H * (a.d / 4 + 33.0) + 8) * glr_plan(a).segs <= 0x7fffffff;
+  const GlrPlan plan = glr_plan(a);
+  const int e = a.dtype == 0 ? 2 : 4, V = plan.pieces ? (plan.narrow ? 8 : 16) / e : (a.d % (8 / e) == 0 ? 8 / e : 1);
+  const int inner = std::max(1, 128 / (4 * V * e)), lines = (a.d - 1) / (4 * V * inner) + 1;
+  return launch_fits(((double)a.num_seqs * a.H * lines * plan.segs + 7) * inner, 64 * plan.waves);
 }
 
 size_t glr_workspace_bytes(const GlrArgs &a) {
@@ -552,6 +554,11 @@ hipError_t launch_glr_chunk(const GlrArgs &a, bool bwd, hipStream_t st) {
   p.maps = (float *)a.workspace;
   if (a.dtype == 0) return bwd ? launch_glr<bf16, true>(p, plan, st) : launch_glr<bf16, false>(p, plan, st);
   return bwd ? launch_glr<float, true>(p, plan, st) : launch_glr<float, false>(p, plan, st);
+}
+
+bool glr_step_fits(size_t n, int dtype) {
+  const int V = dtype == 0 ? 8 : 4;
+  return launch_fits((double)n / (n % V == 0 ? V : 1) / 256 + 1, 256);
 }
 
 template <typename E>

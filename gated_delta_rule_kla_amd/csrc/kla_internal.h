@@ -130,6 +130,9 @@ hipError_t launch_seg_table(const SegFixParams &f, int *seg_first, hipStream_t s
 hipError_t launch_seg_finish(const SegFixParams &f, hipStream_t stream);
 bool seg_correct_mfma(int dtype, int dk, int dv);
 
+// A launch's threads are counted in 32 bits.
+inline bool launch_fits(double workgroups, int threads) { return workgroups * threads <= 4294967295.0; }
+
 // The gated linear recurrence (kla_glr.hip).  Forward: x in, o out, y0 / yend the initial
 // and final states.  Backward: x is dL/do, h the forward's output, y0 dL/dh_final, h0 the
 // initial state; o is dx, dg the gate's gradient, yend dL/dh_0.
@@ -144,8 +147,9 @@ struct GlrArgs {
   void *workspace;            // device, glr_workspace_bytes(*this) bytes
 };
 size_t glr_workspace_bytes(const GlrArgs &a);
-bool glr_grid_fits(const GlrArgs &a);  // the launch's workgroups fit an int
+bool glr_grid_fits(const GlrArgs &a);  // launch_fits
 hipError_t launch_glr_chunk(const GlrArgs &a, bool bwd, hipStream_t stream);
+bool glr_step_fits(size_t n, int dtype);  // n channels; launch_fits
 hipError_t launch_glr_step(const void *x, const void *g, float *state, void *o, size_t n, int dtype,
                            hipStream_t stream);
 
@@ -156,6 +160,7 @@ struct Kv4Cache {
   const int32_t *table;
   int num_pages, page, max_pages, Hkv;
 };
+bool kv4_move_grid_fits(int B, int Hkv, int T);
 hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,
                            int T, int D, int dtype, bool read, hipStream_t stream);
 struct Kv4DecodeArgs {

@@ -359,8 +359,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void kla_kv4_decode_ke
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint8_t *a = s_v[wave] + ((e & 4) * 4 + 4 * (e & 3) + c) * (D / 2);
-      if constexpr (D == 128) va[e] = *reinterpret_cast<const unsigned *>(a + 4 * r);
-      else va[e] = *reinterpret_cast<const unsigned short *>(a + 2 * r);
+      unsigned short half;
+      if constexpr (D == 128) __builtin_memcpy(&va[e], __builtin_assume_aligned(a + 4 * r, 4), 4);
+      else __builtin_memcpy(&half, __builtin_assume_aligned(a + 2 * r, 2), 2), va[e] = half;
       vf[e] = __builtin_bit_cast(float, (unsigned)sc8[4 * (32 + 16 * (e >> 2) + 4 * c + (e & 3)) + r * DW / 32] << 23);
     }
     if (id0 < 0 || id1 < 0 || t + 32 > hi) {
@@ -551,8 +552,12 @@ size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs &a) {
 bool kv4_decode_grid_fits(const Kv4DecodeArgs &a) {
   int splits, per;
   kv4_runs(a, &splits, &per);
-  return (long long)a.N * a.c.Hkv * ((a.Hq / a.c.Hkv + 15) / 16) * splits <= 0x7fffffffLL &&
-         (long long)a.N * a.Hq * (a.D / 32) <= 0x7fffffffLL;
+  return launch_fits((double)a.N * a.c.Hkv * ((a.Hq / a.c.Hkv + 15) / 16) * splits, 256) &&
+         launch_fits((double)a.N * a.Hq * (a.D / 32), 256);
+}
+
+bool kv4_move_grid_fits(int B, int Hkv, int T) {
+  return launch_fits(((double)B * T / KV_TOKENS + 1) * 2 * Hkv, 256);
 }
 
 hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,

@@ -624,11 +624,16 @@ def _device_of(fn: str, t: torch.Tensor) -> torch.device:
     return t.device
 
 
+_INT32 = 0x7FFFFFFF  # sizes go to the library as 32-bit integers
+
+
 def _rank(t: torch.Tensor, name: str, rank: int) -> tuple:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dim() != rank:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rank} dimensions")
+    if max(t.shape) > _INT32:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: a dimension of more than {_INT32}")
     return tuple(t.shape)
 
 
@@ -775,6 +780,8 @@ def glr_decode_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
             and x.is_contiguous() and g.is_contiguous() and state.is_contiguous()):
         _refuse_glr_step(x, g, state)
     dev, (N, H, d) = x.device, x.shape
+    if N > _INT32 or H > _INT32 or d > _INT32:
+        _refuse_glr_step(x, g, state)
     if out is None:
         out = torch.empty_like(x)
     else:
@@ -938,10 +945,13 @@ def kv4_read(
     return out
 
 
+_MAX_LEN = _INT32 - 65536  # the longest max_len
+
+
 def attn_kv4_decode_workspace_bytes(N: int, Hq: int, Hkv: int, D: int, max_len: int,
                                     dtype: torch.dtype = torch.bfloat16) -> int:
     """Workspace bytes attn_kv4_decode_step needs (kla_attn_kv4_decode_workspace_bytes)."""
-    return lib().kla_attn_kv4_decode_workspace_bytes(N, Hq, Hkv, D, int(max_len), _DTYPES[dtype])
+    return lib().kla_attn_kv4_decode_workspace_bytes(N, Hq, Hkv, D, min(int(max_len), _INT32), _DTYPES[dtype])
 
 
 def attn_kv4_decode_step(
@@ -973,7 +983,7 @@ def attn_kv4_decode_step(
         out = torch.empty_like(q)
     else:
         _fit(out, "out", q.dtype, shape, dev)
-    max_len = M * page if max_len is None else int(max_len)
+    max_len = min(M * page, _MAX_LEN) if max_len is None else min(int(max_len), _INT32)
     dt = _DTYPES[q.dtype]
     ws = _scratch(workspace, lib().kla_attn_kv4_decode_workspace_bytes(N, Hq, Hkv, D, max_len, dt), dev)
     _call("kla_attn_kv4_decode_step", dev, q.data_ptr(), codes.data_ptr(), scales.data_ptr(), block_table.data_ptr(),

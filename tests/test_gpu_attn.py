@@ -126,6 +126,19 @@ def test_scales(dtype, scale):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scale", [0.0, 0.125])
+def test_a_query_that_is_not_finite(dtype, scale):
+    q, k, v = inputs(dtype, 1, 2, 1, 150, 150, 64, 8)
+    q[0, 0, 70, 3], q[0, 1, 149, 9] = float("nan"), float("inf")
+    o, lse = kla.attn_fwd(q, k, v, scale)
+    q[0, 0, 70], q[0, 1, 149] = 0.0, 0.0
+    for h, t in ((0, 70), (1, 149)):
+        assert o[0, h, t].isnan().all() and lse[0, h, t].isnan()
+        o[0, h, t], lse[0, h, t] = kla.attn_fwd(q, k, v, scale)[0][0, h, t], kla.attn_fwd(q, k, v, scale)[1][0, h, t]
+    check(o, lse, q, k, v, scale, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_growing_scores(dtype):
     """Every later key beats the ones before, so the running maximum moves in every tile."""
     q, k, v = inputs(dtype, 1, 1, 1, 400, 400, 64, 6)

@@ -286,6 +286,8 @@ def test_refusals():
         kla.attn_kv4_decode_step(q, codes, scales, table.long(), one)
     with pytest.raises(kla.KlaError):
         kla.attn_kv4_decode_step(q[:, :3].contiguous(), codes, scales, table, one)
+    with pytest.raises(kla.KlaError):
+        kla.attn_kv4_decode_step(q, codes, scales, table, one, max_len=2 ** 32 + 1)
     with pytest.raises(ValueError):
         kla.kv4_append(k[:, :1].contiguous(), k, codes, scales, table, one)
     with pytest.raises(ValueError):

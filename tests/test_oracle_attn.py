@@ -99,7 +99,8 @@ def move(fn, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=5), -3), (dict(B=-1, N=-1), -2), (dict(Hkv=0), -2), (dict(T=-1), -2), (dict(P=0), -2),
     (dict(page=0), -2), (dict(M=0), -2), (dict(N=3), -2), (dict(D=96), -4), (dict(page=24), -4),
-    (dict(page=1 << 21), -4), (dict(T=0x7fffffff), -2), (dict(T=1 << 28, Hkv=4), -2), (dict(k=None), -1),
+    (dict(page=1 << 21), -4), (dict(T=0x7fffffff), -2), (dict(T=1 << 28, Hkv=4), -2),
+    (dict(T=1 << 28, Hkv=2), -2), (dict(k=None), -1),
     (dict(codes=None), -1), (dict(start=None), -1), (dict(table=FAKE + 2), -8), (dict(scales=FAKE + 8), -8),
     (dict(start=FAKE + 1), -8),
     (dict(cu=FAKE, cuh=[0, 4, 9], B=1), -5), (dict(cu=FAKE, cuh=[0, 11, 10], B=1), -5), (dict(cu=FAKE, B=1), -1),
@@ -124,7 +125,7 @@ def decode(**kw):
     (dict(ml=0x7fffffff), -2), (dict(D=32), -4), (dict(page=8), -4), (dict(scale=float("nan")), -11),
     (dict(scale=float("inf")), -11), (dict(q=None), -1), (dict(lens=None), -1), (dict(q=FAKE + 2), -8), (dict(lens=FAKE + 2), -8),
     (dict(ml=100000, M=10000), -7), (dict(ml=100000, M=10000, ws=FAKE, wsb=100), -7),
-    (dict(N=1 << 20, Hq=1 << 14, Hkv=1 << 13), -2), (dict(N=0, q=None), 0),
+    (dict(N=1 << 20, Hq=1 << 14, Hkv=1 << 13), -2), (dict(N=1 << 20, Hq=16, Hkv=16), -2), (dict(N=0, q=None), 0),
 ])
 def test_decode_refusals(kw, status):
     assert decode(**kw) == status
@@ -153,8 +154,8 @@ def attn(**kw):
     (dict(dtype=2), -3), (dict(B=-1, N=-1), -2), (dict(Hq=6), -2), (dict(Hkv=0), -2), (dict(Tq=-1), -2),
     (dict(Tk=-1), -2), (dict(Tk=0x7fffffff), -2), (dict(N=3), -2), (dict(D=0), -2), (dict(D=80), -4),
     (dict(B=1 << 20, N=1 << 20, Hq=1 << 12), -2), (dict(B=1 << 15, N=1 << 15, Hq=1 << 15, Tq=1 << 20), -2),
-    (dict(scale=float("nan")), -11), (dict(q=None), -1), (dict(k=None), -1), (dict(q=FAKE + 8), -8),
-    (dict(lse=FAKE + 4), -8), (dict(cu=FAKE, cuh=[0, 4, 10]), -2), (dict(cu=FAKE, cuh=[0, 4, 9], B=1), -5),
+    (dict(B=1 << 18, N=1 << 18, Hq=32), -2), (dict(scale=float("nan")), -11), (dict(q=None), -1), (dict(k=None), -1),
+    (dict(q=FAKE + 8), -8), (dict(lse=FAKE + 4), -8), (dict(cu=FAKE, cuh=[0, 4, 10]), -2), (dict(cu=FAKE, cuh=[0, 4, 9], B=1), -5),
     (dict(cu=FAKE, cuh=[0, 4, 10], B=1, Tk=11), -2), (dict(cu=FAKE, cuh=[0, 4, 10], ck=FAKE, B=1), -1),
     (dict(cu=FAKE, cuh=[0, 4, 10], ck=FAKE, ckh=[0, 4, 11], B=1), -5), (dict(ck=FAKE, ckh=[0, 4, 10]), -1),
     (dict(cu=FAKE, cuh=[0, 4, 10], ck=FAKE + 2, ckh=[0, 4, 10], B=1), -8), (dict(Tq=0, q=None), 0),

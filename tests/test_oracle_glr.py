@@ -116,7 +116,8 @@ def call(fn, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), -3), (dict(dtype=-1), -3), (dict(B=-1), -2), (dict(H=0), -2), (dict(T=-1), -2), (dict(d=0), -2),
     (dict(d=(1 << 24) + 1), -2), (dict(N=3), -2), (dict(N=-1), -2), (dict(T=0x7fffffff), -2),
-    (dict(H=1 << 20, B=1 << 12, N=1 << 12), -2), (dict(p=None), -1), (dict(p=FAKE + 8), -8), (dict(s=FAKE + 4), -8),
+    (dict(H=1 << 20, B=1 << 12, N=1 << 12), -2), (dict(H=64, B=1 << 20, N=1 << 20, T=1), -2),
+    (dict(H=1, B=1 << 24, N=1 << 24, T=1, d=1 << 10), -2), (dict(p=None), -1), (dict(p=FAKE + 8), -8), (dict(s=FAKE + 4), -8),
     (dict(cuh=[0, 100], N=1, B=1), -1), (dict(cu=FAKE, N=1, B=1), -1), (dict(cu=FAKE, cuh=[0, 50, 100], B=2), -2),
     (dict(cu=FAKE, cuh=[0, 50, 99], B=1), -5), (dict(cu=FAKE, cuh=[1, 50, 100], B=1), -5),
     (dict(cu=FAKE, cuh=[0, 101, 100], B=1), -5), (dict(cu=FAKE + 2, cuh=[0, 50, 100], B=1), -8),
@@ -129,7 +130,8 @@ def test_refusals(fn, kw, status):
 
 @pytest.mark.parametrize("kw,status", [(dict(dtype=9), -3), (dict(N=-1), -2), (dict(H=0), -2), (dict(d=0), -2),
                                        (dict(p=None), -1), (dict(s=FAKE + 4), -8), (dict(N=0), 0),
-                                       (dict(N=1 << 30, H=1, d=1 << 20), -2)])
+                                       (dict(N=1 << 30, H=1, d=1 << 20), -2), (dict(N=1 << 30, H=1, d=33), -2),
+                                       (dict(N=(1 << 30) + 1, H=1, d=5), -2)])
 def test_step_refusals(kw, status):
     assert call("step", **kw) == status
 
