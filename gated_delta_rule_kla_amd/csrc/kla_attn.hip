@@ -13,10 +13,12 @@
 // accumulator holds the keys (slot 8h + e of 16 keys is key 4h + e, or 8 + 4h + e - 4).  V^T
 // comes out of the row-major tile by transposing LDS reads.
 //
-// Measured: 16,384 tokens, 16 heads of 128 over 2: 1.00 ms, 1.1 PFLOP/s, where a bf16 product
-// of 8192^3 reaches 1.38 and the clock falls to 2.0 GHz under either.  The matrix cores are
-// busy 53% of the cycles and the vector ALU 49%; two groups of waves half a tile apart, a
-// barrier between their phases, took 1.06 ms, operands read ahead of their products 1.00.
+// Measured: 16,384 tokens, 16 heads of 128 over 2: 0.94 ms, 1.17 PFLOP/s, where a bf16 product
+// of 8192^3 reaches 1.38 and the clock falls below 2.0 GHz under either.  The matrix cores are
+// busy 59% of the cycles and the vector ALU 53%.  Tried on the way, at 0.98: two groups of
+// waves half a tile apart with a barrier between their phases 1.06 ms; the next tile's scores
+// beside this tile's weights within a wave 1.15 (registers spilled; slower with 32 keys too,
+// where none do); three or four tiles in LDS 0.99.
 //
 // LDS rows are D values long without padding (the direct loads write 1 KB runs); 16-byte
 // pieces are exchanged within a row instead, K's by the row's low bits, V's by its low two

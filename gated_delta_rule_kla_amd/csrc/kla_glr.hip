@@ -475,9 +475,8 @@ struct GlrShape {
 // bytes, 19 with segments), nor for tiles of 1,024 rows (5,000 channels, 1,500 tokens: 19 us
 // whole, 25 with 32 bytes).
 //
-// Tiles fit the longest sequence: one wave's 64 rows, four waves' 256 or eight waves' 512
-// (19 sequences of 2 to 7 tokens,
-// 16 heads of 2,560 channels: 37 us against 393 with 512 rows).
+// Tiles fit the longest sequence: one wave's 64 rows, four waves' 256 or eight waves' 512 (19
+// sequences of 2 to 7 tokens, 16 heads of 2,560 channels: 37 us against 393 with 512 rows).
 struct GlrPlan {
   bool pieces, narrow;
   int waves;
@@ -491,7 +490,7 @@ GlrPlan glr_plan(const GlrArgs &a) {
   const int V = pieces ? 16 / e : (a.d % (8 / e) == 0 ? 8 / e : 1);
   const long long wide = (long long)a.num_seqs * a.H * ((a.d + 4 * V - 1) / (4 * V));
   GlrPlan r{pieces, false, a.longest <= 64 ? 1 : (a.longest <= 256 ? 4 : 8), 1, 0};
-  if (wide >= 256 || a.longest <= 2048) return r;
+  if (wide == 0 || wide >= 256 || a.longest <= 2048) return r;
   if (pieces && (wide >= 128 || a.longest <= 3584)) {
     r.narrow = true;
     return r;

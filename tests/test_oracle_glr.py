@@ -122,7 +122,7 @@ def call(fn, **kw):
     (dict(cu=FAKE, cuh=[0, 50, 99], B=1), -5), (dict(cu=FAKE, cuh=[1, 50, 100], B=1), -5),
     (dict(cu=FAKE, cuh=[0, 101, 100], B=1), -5), (dict(cu=FAKE + 2, cuh=[0, 50, 100], B=1), -8),
     (dict(B=1, N=1, H=1, d=64, T=100000), -7), (dict(B=1, N=1, H=1, d=64, T=100000, ws=FAKE, wsb=16), -7),
-    (dict(B=0, N=0), 0), (dict(cu=FAKE, cuh=[0], N=0, B=1, T=0), 0),
+    (dict(B=0, N=0), 0), (dict(B=0, N=0, T=100000), 0), (dict(cu=FAKE, cuh=[0], N=0, B=1, T=0), 0),
 ])
 def test_refusals(fn, kw, status):
     assert call(fn, **kw) == status
