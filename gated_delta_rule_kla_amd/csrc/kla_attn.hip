@@ -16,9 +16,10 @@
 // Measured: 16,384 tokens, 16 heads of 128 over 2: 0.94 ms, 1.17 PFLOP/s, where a bf16 product
 // of 8192^3 reaches 1.38 and the clock falls below 2.0 GHz under either.  The matrix cores are
 // busy 59% of the cycles and the vector ALU 53%.  Tried on the way, at 0.98: two groups of
-// waves half a tile apart with a barrier between their phases 1.06 ms; the next tile's scores
-// beside this tile's weights within a wave 1.15 (registers spilled; slower with 32 keys too,
-// where none do); three or four tiles in LDS 0.99.
+// waves half a tile apart with a barrier between their phases 1.06 ms; three or four tiles in
+// LDS 0.99; the next tile's scores beside this tile's weights within a wave spilled (8,192
+// tokens, 32 heads: 0.99 ms against 0.49) and lost with tiles of 32 keys too, where nothing
+// did (0.63 against 0.53).
 //
 // LDS rows are D values long without padding (the direct loads write 1 KB runs); 16-byte
 // pieces are exchanged within a row instead, K's by the row's low bits, V's by its low two
