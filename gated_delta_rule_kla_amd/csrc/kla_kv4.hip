@@ -48,20 +48,21 @@ struct KvMoveParams {
   long long rows;             // B * Hkv * T
 };
 
-// eight channels as fp32
-template <typename E>
+// eight channels as fp32; ONCE: with the non-temporal hint, for what is not used again soon
+template <typename E, bool ONCE = false>
 __device__ __forceinline__ void ld8(const E *p, float *f) {
   constexpr int PER = 16 / sizeof(E);
 #pragma unroll
   for (int i = 0; i < 8; i += PER) {
-    const uint4 u = ldg16(p + i);
+    const u32x4 u = ONCE ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + i))
+                         : __builtin_bit_cast(u32x4, ldg16(p + i));
     E e[PER];
     __builtin_memcpy(e, &u, 16);
 #pragma unroll
     for (int j = 0; j < PER; ++j) f[i + j] = Elem<E>::to_f32(e[j]);
   }
 }
-template <typename E>
+template <typename E, bool ONCE>
 __device__ __forceinline__ void st8(E *p, const float *f) {
   constexpr int PER = 16 / sizeof(E);
 #pragma unroll
@@ -69,27 +70,27 @@ __device__ __forceinline__ void st8(E *p, const float *f) {
     E e[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) e[j] = Elem<E>::from_f32(f[i + j]);
-    uint4 u;
+    u32x4 u;
     __builtin_memcpy(&u, e, 16);
-    stg16(p + i, u);
+    if constexpr (ONCE) __builtin_nontemporal_store(u, reinterpret_cast<u32x4 *>(p + i));
+    else *reinterpret_cast<u32x4 *>(p + i) = u;
   }
 }
 
-// A workgroup moves 64 consecutive tokens of one head's keys or values: the first wave finds
+// A workgroup moves TOKENS consecutive tokens of one head's keys or values: as many threads find
 // their places (sequence, position, page) while the other loads are in flight, then D / 8 lanes
-// move a row.  With one row per 16 lanes and the search in each of them, 146,000 tokens of 4
-// heads took 170 us one way; with four rows a thread in flight 90.
-constexpr int KV_TOKENS = 64, KV_CU = 1024;  // tokens of a workgroup; offsets searched in LDS
+// move a row.  Many tokens: 256 to a workgroup, and their rows past the caches (ONCE).
+constexpr int KV_CU = 1024;  // offsets searched in LDS
 
-template <typename E, int D, bool READ>
+template <typename E, int D, bool READ, int TOKENS, bool ONCE>
 __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
-  constexpr int LPR = D / 8, RPT = KV_TOKENS * LPR / 256;  // lanes of a row, rows of a thread
-  __shared__ long long s_row[KV_TOKENS];
+  constexpr int LPR = D / 8, RPT = TOKENS * LPR / 256;  // lanes of a row, rows of a thread
+  __shared__ long long s_row[TOKENS];
   __shared__ int s_cu[KV_CU];
   const int tid = threadIdx.x, lane = tid % LPR;
   const unsigned jh = blockIdx.x % (2 * p.kv.Hkv);
   const int j = jh / p.kv.Hkv, head = jh % p.kv.Hkv;
-  const long long tok0 = (long long)(blockIdx.x / (2 * p.kv.Hkv)) * KV_TOKENS, toks = p.rows / p.kv.Hkv;  // B * T
+  const long long tok0 = (long long)(blockIdx.x / (2 * p.kv.Hkv)) * TOKENS, toks = p.rows / p.kv.Hkv;  // B * T
   E *const base = (E *)(j ? p.v : p.k);
 
   auto x_of = [&](int i) {  // row i of the workgroup (the last one's again past the end)
@@ -99,14 +100,14 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
   float f[RPT][8];
   if constexpr (!READ) {
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) ld8((const E *)x_of(tid / LPR + 256 / LPR * r), f[r]);
+    for (int r = 0; r < RPT; ++r) ld8<E, ONCE>((const E *)x_of(tid / LPR + 256 / LPR * r), f[r]);
   }
   const bool near = p.cu && p.N < KV_CU;
   if (near) {
     for (int i = tid; i <= p.N; i += 256) s_cu[i] = p.cu[i];
     __syncthreads();
   }
-  if (tid < KV_TOKENS) {
+  if (tid < TOKENS) {
     const long long tok = tok0 + tid;
     long long row = -1;
     if (tok < toks) {
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
       const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u[r], s, 3);
       const float y[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
       const int i = tid / LPR + 256 / LPR * r;
-      if (tok0 + i < toks) st8(x_of(i), y);
+      if (tok0 + i < toks) st8<E, ONCE>(x_of(i), y);
     }
   } else {
 #pragma unroll
@@ -502,13 +503,31 @@ __global__ __launch_bounds__(GROUPS *CH / 4) void kla_kv4_join_kernel(KvDecodePa
     ((E *)p.o)[row * D + ch + i] = Elem<E>::from_f32(l == 0.f ? 0.f : o[i] / l);
 }
 
-template <typename E, bool READ>
-hipError_t launch_move(const KvMoveParams &p, int D, hipStream_t st) {
-  const long long toks = p.rows / p.kv.Hkv;
-  const dim3 grid((unsigned)((toks + KV_TOKENS - 1) / KV_TOKENS * 2 * p.kv.Hkv));
-  if (D == 128) hipLaunchKernelGGL((kla_kv4_move_kernel<E, 128, READ>), grid, dim3(256), 0, st, p);
-  else hipLaunchKernelGGL((kla_kv4_move_kernel<E, 64, READ>), grid, dim3(256), 0, st, p);
+template <typename E, int D, bool READ, int TOKENS, bool ONCE>
+hipError_t launch_move_t(const KvMoveParams &p, hipStream_t st) {
+  const long long groups = (p.rows / p.kv.Hkv + TOKENS - 1) / TOKENS;
+  hipLaunchKernelGGL((kla_kv4_move_kernel<E, D, READ, TOKENS, ONCE>), dim3((unsigned)(groups * 2 * p.kv.Hkv)), dim3(256), 0,
+                     st, p);
   return hipGetLastError();
+}
+
+// Tokens of a workgroup, and whether the rows go past the caches, by the bytes of k and v.  From
+// 96 MB on (what the caches keep between calls) more tokens hide the search for their places,
+// and bf16 rows, written in whole lines, leave the caches to the codes: 131,000 tokens of 4 heads
+// of 128 (268 MB) append 66 us against 75 with 64 tokens, read 73 to 78 against 104; 96,000
+// tokens 49 and 41 us against 55 and 76; 32,000 tokens append 18.6 us against 19.8, read 23.3
+// against 20.5.  Reads below 256 MB do better with 128 tokens (96,000 tokens: 41 us against 47;
+// 256,000: 171 against 163).  fp32 rows are written in half lines, which must meet in the caches
+// (64,000 tokens: 83 us, 108 past them, 69 with 256 tokens); their appends take 61 us either way.
+template <typename E, int D, bool READ>
+hipError_t launch_move(const KvMoveParams &p, hipStream_t st) {
+  constexpr bool ONCE = sizeof(E) == 2;
+  const long long mb = p.rows * D * 2 * (long long)sizeof(E) >> 20;
+  if constexpr (READ && ONCE)
+    if (mb >= 96 && mb < 256) return launch_move_t<E, D, READ, 128, ONCE>(p, st);
+  if constexpr (READ || ONCE)
+    if (mb >= 96) return launch_move_t<E, D, READ, 256, ONCE>(p, st);
+  return launch_move_t<E, D, READ, 64, false>(p, st);
 }
 
 template <typename E, int D>
@@ -557,15 +576,19 @@ bool kv4_decode_grid_fits(const Kv4DecodeArgs &a) {
 }
 
 bool kv4_move_grid_fits(int B, int Hkv, int T) {
-  return launch_fits(((double)B * T / KV_TOKENS + 1) * 2 * Hkv, 256);
+  return launch_fits(((double)B * T / 256 + 4) * 2 * Hkv, 256);
 }
 
 hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,
                            int T, int D, int dtype, bool read, hipStream_t st) {
   const KvMoveParams p{kv_params(c), k, v, start, cu, N, T, (long long)B * c.Hkv * T};
   if (p.rows == 0) return hipSuccess;
-  if (dtype == 0) return read ? launch_move<bf16, true>(p, D, st) : launch_move<bf16, false>(p, D, st);
-  return read ? launch_move<float, true>(p, D, st) : launch_move<float, false>(p, D, st);
+  if (dtype == 0) {
+    if (D == 128) return read ? launch_move<bf16, 128, true>(p, st) : launch_move<bf16, 128, false>(p, st);
+    return read ? launch_move<bf16, 64, true>(p, st) : launch_move<bf16, 64, false>(p, st);
+  }
+  if (D == 128) return read ? launch_move<float, 128, true>(p, st) : launch_move<float, 128, false>(p, st);
+  return read ? launch_move<float, 64, true>(p, st) : launch_move<float, 64, false>(p, st);
 }
 
 hipError_t launch_attn_kv4_decode(const Kv4DecodeArgs &a, void *workspace, hipStream_t st) {

@@ -82,6 +82,35 @@ def test_store_and_read(dtype, D, page, Hkv):
     assert (scales.cpu().permute(0, 3, 1, 2, 4)[rest] == 0x77).all()
 
 
+@pytest.mark.parametrize("dtype,D,Hkv,T", [(BF, 128, 4, 50000), (BF, 128, 4, 132000), (BF, 64, 8, 51000),
+                                           (F32, 128, 4, 26000), (F32, 64, 4, 50000)])
+def test_many_tokens(dtype, D, Hkv, T):
+    """Larger workgroups, and rows that go past the caches: the same as sequence by sequence,
+    and the oracle's values at sampled tokens."""
+    lens, page = [3, T // 3, 1, T - T // 3 - T // 8 - 11, T // 8 + 7], 64
+    start = [0, 70, 5, 1, 64]
+    table, P = pages([a + b for a, b in zip(start, lens)], page)
+    whole, parts = kla.kv4_cache(P, Hkv, page, D, DEV), kla.kv4_cache(P, Hkv, page, D, DEV)
+    k, v = make_kv(lens, Hkv, D, dtype)
+    cu, host = packed(lens)
+    kla.kv4_append(k, v, *whole, table, i32(start), cu, host)
+    out = [torch.full((Hkv * T + 1, D), 7.0, dtype=dtype, device=DEV) for _ in range(2)]
+    view = tuple(t[:-1].view(1, Hkv, T, D) for t in out)
+    kla.kv4_read(*whole, table, i32(start), cu, dtype, host, out=view)
+    for n, (a, z) in enumerate(zip(host[:-1].tolist(), host[1:].tolist())):
+        for b in range(a, z, 4000):  # small calls
+            e = min(b + 4000, z)
+            at, c, h = i32([start[n] + b - a]), i32([0, e - b]), torch.tensor([0, e - b], dtype=torch.int32)
+            kla.kv4_append(k[:, :, b:e].contiguous(), v[:, :, b:e].contiguous(), *parts, table[n:n + 1], at, c, h)
+            one = kla.kv4_read(*parts, table[n:n + 1], at, c, dtype, h)
+            assert torch.equal(one[0], view[0][:, :, b:e]) and torch.equal(one[1], view[1][:, :, b:e])
+    assert torch.equal(whole[0], parts[0]) and torch.equal(whole[1], parts[1])
+    some = torch.cat([host[1:].long() - 1, torch.arange(0, T, T // 50)])
+    for x, y in ((k, view[0]), (v, view[1])):
+        np.testing.assert_array_equal(f64(y[:, :, some.to(DEV)]), values(*quantise(f64(x[:, :, some.to(DEV)]))))
+    assert (out[0][-1] == 7).all() and (out[1][-1] == 7).all()
+
+
 def test_dense_batch_and_padding():
     """One new token for each of four sequences; the second is padding (negative start), the
     third has no page there, the fourth's page is outside the cache."""
