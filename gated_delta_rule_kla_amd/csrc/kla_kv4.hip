@@ -48,14 +48,20 @@ struct KvMoveParams {
   long long rows;             // B * Hkv * T
 };
 
-// eight channels as fp32; ONCE: with the non-temporal hint, for what is not used again soon
+// 16 bytes; ONCE: with the non-temporal hint, for what is not used again soon
+template <bool ONCE>
+__device__ __forceinline__ u32x4 ld16(const void *p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+  else return *reinterpret_cast<const u32x4 *>(p);
+}
+
+// eight channels as fp32
 template <typename E, bool ONCE = false>
 __device__ __forceinline__ void ld8(const E *p, float *f) {
   constexpr int PER = 16 / sizeof(E);
 #pragma unroll
   for (int i = 0; i < 8; i += PER) {
-    const u32x4 u = ONCE ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + i))
-                         : __builtin_bit_cast(u32x4, ldg16(p + i));
+    const u32x4 u = ld16<ONCE>(p + i);
     E e[PER];
     __builtin_memcpy(e, &u, 16);
 #pragma unroll
@@ -223,7 +229,7 @@ __device__ __forceinline__ void cvt8(unsigned u, float s, unsigned *r) {
   r[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, s, 3));
 }
 
-template <typename E, int D>
+template <typename E, int D, bool ONCE>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void kla_kv4_decode_kernel(KvDecodeParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;  // bf16 terms of q and P
   constexpr int KJ = D / 32;                  // products over the channels, 8 channels a lane
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void kla_kv4_decode_ke
   constexpr int LPR = D / 32;          // lanes of a row of V
   struct Tile {
     unsigned k[2][KJ];
-    uint4 v[VP];
+    u32x4 v[VP];
     unsigned sc;
     int id0, id1;
   } next;
@@ -305,17 +311,20 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void kla_kv4_decode_ke
     for (int h = 0; h < 2; ++h) {
       const uint8_t *a = p.kv.codes + ((h ? r1 : r0) + r) * (D / 2) + c * (D / 8);
       if constexpr (D == 128) {
-        const uint4 u = ldg16(a);
-        x.k[h][0] = u.x, x.k[h][1] = u.y, x.k[h][2] = u.z, x.k[h][3] = u.w;
+        const u32x4 u = ld16<ONCE>(a);
+        x.k[h][0] = u[0], x.k[h][1] = u[1], x.k[h][2] = u[2], x.k[h][3] = u[3];
       } else {
-        const uint2 u = *reinterpret_cast<const uint2 *>(a);
-        x.k[h][0] = u.x, x.k[h][1] = u.y;
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        u32x2 u;
+        if constexpr (ONCE) u = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(a));
+        else u = *reinterpret_cast<const u32x2 *>(a);
+        x.k[h][0] = u[0], x.k[h][1] = u[1];
       }
     }
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
       const int key = lane / LPR + 64 / LPR * i;
-      x.v[i] = ldg16(p.kv.codes + ((key < 16 ? r0 : r1) + pg + key % 16) * (D / 2) + 16 * (lane % LPR));
+      x.v[i] = ld16<ONCE>(p.kv.codes + ((key < 16 ? r0 : r1) + pg + key % 16) * (D / 2) + 16 * (lane % LPR));
     }
     const uint8_t *a = p.kv.scales + ((lane & 16 ? r1 : r0) + (lane & 15) + (lane & 32 ? pg : 0)) * (D / 32);
     if constexpr (D == 128) x.sc = *reinterpret_cast<const unsigned *>(a);
@@ -332,7 +341,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void kla_kv4_decode_ke
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
       const int key = lane / LPR + 64 / LPR * i, slot = (key & 16) + 4 * (key & 3) + ((key >> 2) & 3);
-      *reinterpret_cast<uint4 *>(s_v[wave] + slot * (D / 2) + 16 * (lane % LPR)) = x0.v[i];
+      *reinterpret_cast<u32x4 *>(s_v[wave] + slot * (D / 2) + 16 * (lane % LPR)) = x0.v[i];
     }
     s_sc[wave][lane] = x0.sc;
     const uint8_t *sc8 = reinterpret_cast<const uint8_t *>(s_sc[wave]);
@@ -533,7 +542,13 @@ hipError_t launch_move(const KvMoveParams &p, hipStream_t st) {
 template <typename E, int D>
 hipError_t launch_kv4_decode(const KvDecodeParams &p, hipStream_t st) {
   const long long grid = (long long)p.N * p.kv.Hkv * p.GB * p.splits;
-  hipLaunchKernelGGL((kla_kv4_decode_kernel<E, D>), dim3((unsigned)grid), dim3(256), 0, st, p);
+  // The codes go past the caches where the cache is larger than what those keep from step to step
+  // (64 sequences, 326 MB: 66 us, 74 through them; 32 of 30,000 tokens: 100, 113; 16 of 4,000
+  // with 8 heads, 70 MB: 23.1, 22.3).
+  if ((double)p.N * p.kv.Hkv * p.max_len * (D + D / 16) >= 96 << 20)
+    hipLaunchKernelGGL((kla_kv4_decode_kernel<E, D, true>), dim3((unsigned)grid), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((kla_kv4_decode_kernel<E, D, false>), dim3((unsigned)grid), dim3(256), 0, st, p);
   const long long rows = (long long)p.N * p.Hq;
   if (p.splits > 32)
     hipLaunchKernelGGL((kla_kv4_join_kernel<E, D, 32, 32>), dim3((unsigned)(rows * (D / 32))), dim3(256), 0, st, p);
