@@ -197,12 +197,13 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
 // applies the scale too) and exchange halves (v_perm) into pairs of keys, and MFMA j takes
 // channel r D/16 + j of every lane.
 //
-// Measured (64 sequences of 4,096 to 16,384 tokens, 16 heads over 4, D = 128, 326 MB): 73 us a
-// step, 4.5 TB/s, where 4 KB reads in any order reach 5.8; of it the joining kernel is 5.  With
+// Measured (64 sequences of 4,096 to 16,384 tokens, 16 heads over 4, D = 128, 326 MB): 66 us a
+// step, 4.9 TB/s, where 4 KB reads in any order reach 5.8; of it the joining kernel is 5.  With
 // V's dwords and scale bytes loaded straight into that layout, and the runs of a sequence side
-// by side in the grid, it took 107; a second tile in flight, or two or four workgroups on a CU
-// for three, change nothing: what is left is spread over the conversions (37% of the issue
-// slots), the latency of one tile's chain and the lengths' unevenness.
+// by side in the grid, it took 107, with the codes through the caches 74; a second tile in
+// flight, or two or four workgroups on a CU for three, change nothing: what is left is spread
+// over the conversions (37% of the issue slots), the latency of one tile's chain and the
+// lengths' unevenness.
 //
 // Queries in fp32 run the same products with q and P split into three bf16 terms (24 bits),
 // exact against the cache's values.
@@ -562,7 +563,9 @@ KvParams kv_params(const Kv4Cache &c) {
 }
 
 // Runs of the sequences: as many as bring about 1,024 workgroups (64 ragged sequences of 4
-// heads: 73 us, with 512 workgroups 88, with 2,048 78), of 384 tokens at least (three tiles a
+// heads: 66 us, with 512 workgroups 84, with 768 78, with 2,048 73; sequences that all reach
+// max_len would do better with 768, one round: 32 of 30,000 tokens 90 us against 98, but the
+// lengths are the device's), of 384 tokens at least (three tiles a
 // wave; one sequence of 131,072 tokens, 2 heads: 16.6 us, with 256 tokens 19.0, with 512 18.2)
 // and KV_MAX_PER at most.
 void kv4_runs(const Kv4DecodeArgs &a, int *splits, int *per) {
