@@ -593,8 +593,9 @@ bool kv4_decode_grid_fits(const Kv4DecodeArgs &a) {
          launch_fits((double)a.N * a.Hq * (a.D / 32), 256);
 }
 
-bool kv4_move_grid_fits(int B, int Hkv, int T) {
-  return launch_fits(((double)B * T / 256 + 4) * 2 * Hkv, 256);
+bool kv4_move_grid_fits(int B, int Hkv, int T, int dtype, bool read) {
+  // large batches: 256 tokens to a workgroup but for appends in fp32
+  return launch_fits(((double)B * T / (read || dtype == 0 ? 256 : 64) + 1) * 2 * Hkv, 256);
 }
 
 hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,

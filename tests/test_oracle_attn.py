@@ -100,7 +100,7 @@ def move(fn, **kw):
     (dict(dtype=5), -3), (dict(B=-1, N=-1), -2), (dict(Hkv=0), -2), (dict(T=-1), -2), (dict(P=0), -2),
     (dict(page=0), -2), (dict(M=0), -2), (dict(N=3), -2), (dict(D=96), -4), (dict(page=24), -4),
     (dict(page=1 << 21), -4), (dict(T=0x7fffffff), -2), (dict(T=1 << 28, Hkv=4), -2),
-    (dict(T=1 << 28, Hkv=2), -2), (dict(k=None), -1),
+    (dict(T=(1 << 28) - 1, Hkv=4), -2), (dict(k=None), -1),
     (dict(codes=None), -1), (dict(start=None), -1), (dict(table=FAKE + 2), -8), (dict(scales=FAKE + 8), -8),
     (dict(start=FAKE + 1), -8),
     (dict(cu=FAKE, cuh=[0, 4, 9], B=1), -5), (dict(cu=FAKE, cuh=[0, 11, 10], B=1), -5), (dict(cu=FAKE, B=1), -1),
