@@ -206,6 +206,17 @@ def test_decode_in_several_runs(dtype, lens):
         assert torch.equal(o, kla.attn_kv4_decode_step(q, codes, scales, table, i32(lens), scale=0.2, max_len=max(lens)))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,Hkv", [(128, 1), (64, 4)])
+def test_decode_of_a_large_cache(dtype, D, Hkv):
+    """A bound on the lengths that stands for a cache past what the device keeps: its codes are
+    read past the caches, and most runs are empty."""
+    lens = [1, 33, 700, 0, 2000, 1664, 1665, 3400]
+    codes, scales, table, kv = fill(lens, Hkv, D, 64)
+    q = torch.randn(len(lens), 4, D, device=DEV).to(dtype)
+    check(kla.attn_kv4_decode_step(q, codes, scales, table, i32(lens), max_len=200000), q, kv, D ** -0.5, dtype)
+
+
 def test_many_short_sequences():
     lens = [int(n) for n in np.random.default_rng(0).integers(0, 90, 700)]
     codes, scales, table, kv = fill(lens, 2, 64, 16)
