@@ -239,6 +239,7 @@ kla_status_t check_glr(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host
   const kla_status_t st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, T, &a->longest);
   if (st != KLA_OK) return st;
   a->cu_seqlens = cu_seqlens;
+  a->cu_seqlens_host = cu_seqlens_host;
   a->num_seqs = num_seqs;
   a->H = H;
   a->T = T;

@@ -11,7 +11,7 @@
 //
 // The forward reads x and g and writes o once (6 bytes per element in bf16), the backward
 // reads g, o and do and writes dx and dg (10 bytes): both are bound by HBM.  One workgroup of
-// eight waves owns a slice of 64 (or 32) bytes of the rows of one (sequence, head) and walks
+// eight waves owns a slice of 64 (or 32, or 128) bytes of the rows of one (sequence, head) and walks
 // its tokens in tiles of 512 (1,024) rows, the next tile's 16-byte loads in flight in
 // registers.  A tile goes through LDS from the loads' order (consecutive lanes along a row) to
 // the scan's (lane = 16 channel groups' row groups): each lane composes R consecutive rows of V
@@ -19,7 +19,7 @@
 // channel), the waves' maps meet in LDS behind the one barrier of a tile, and the outputs go
 // back through LDS into whole row pieces.  Every byte is read once and no workgroup waits for
 // another.  Measured on B=4 H=16 T=4096 d=128: forward 46 us (4.4 TB/s; a copy of 1 GiB
-// reaches 5.2), 32 packed sequences of 268 M elements backward 613 us (4.4 TB/s); a first form
+// reaches 5.2), 32 packed sequences of 268 M elements backward 564 us (4.8 TB/s); a first form
 // with the scan's steps as lane shuffles in the loads' order took 56 and 790 us.
 //
 // Where few channels leave most CUs idle, sequences are cut into segments: a first pass forms
@@ -35,6 +35,8 @@ namespace kla {
 
 namespace {
 
+constexpr int GLR_ORDER = 64;  // sequences that are put in order
+
 struct GlrParams {
   const void *x, *g;         // x: the forward's input, the backward's do
   const void *h;             // backward: the forward's output o
@@ -47,6 +49,8 @@ struct GlrParams {
   int lines, inner;          // 128-byte lines of a head's channels, slices of one
   int segs, nseg, seg_rows;  // segments of a sequence at most, of this launch, tokens in one
   float *maps;               // [N,H,segs,2,d]: the segments' maps (A then C)
+  int ordered;               // the sequences start in `order`, the longest first
+  int order[GLR_ORDER];
 };
 
 // exp of the log-decay: one base-2 exponential for bf16 gates, whose own spacing is 2^-8 of
@@ -85,6 +89,12 @@ __device__ __forceinline__ void ldf(float *r, const float *p) {
   }
 }
 
+// 16 bytes; ONCE: with the non-temporal hint, for whole lines, which no other workgroup wants
+template <bool ONCE>
+__device__ __forceinline__ uint4 ldq(const void *p) {
+  if constexpr (ONCE) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p)));
+  else return ldg16(p);
+}
 enum { GLR_WHOLE = 0, GLR_MAPS = 1, GLR_CARRIED = 2 };
 
 // v of the lane S before this one in its row of 16; the row's first S lanes keep `old`.
@@ -93,39 +103,46 @@ __device__ __forceinline__ float row_shr(float old, float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v),
                                                                0x110 + S, 0xF, 0xF, false));
 }
-template <int S, int V>
-__device__ __forceinline__ void scan_step(float *A, float *C) {
+// the same among GW lanes, this one number gw of them
+template <int S, int GW>
+__device__ __forceinline__ float group_shr(float old, float v, int gw) {
+  const float x = row_shr<S>(old, v);
+  return GW == 16 || gw >= S ? x : old;
+}
+template <int S, int V, int GW>
+__device__ __forceinline__ void scan_step(float *A, float *C, int gw) {
+  if (S >= GW) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    // the map S lanes before, then this one; in front of the row's first lanes the identity
-    C[i] = fmaf(row_shr<S>(0.f, C[i]), A[i], C[i]);
-    A[i] = row_shr<S>(1.f, A[i]) * A[i];
+    // the map S lanes before, then this one; in front of the group's first lanes the identity
+    C[i] = fmaf(group_shr<S, GW>(0.f, C[i], gw), A[i], C[i]);
+    A[i] = group_shr<S, GW>(1.f, A[i], gw) * A[i];
   }
 }
 
 // LDS of a workgroup: per wave its rows of the tensors it reads, and a row set on its way out.
-template <typename E, int V, int NW, int R, bool BWD, int MODE, bool PIECES>
+template <typename E, int V, int NW, int R, bool BWD, int MODE, bool PIECES, int CG>
 struct GlrLds {
-  static constexpr int CG = 4, CW = CG * V;
+  static constexpr int CW = CG * V, GW = 64 / CG;
   static constexpr int NT = BWD && MODE != GLR_MAPS ? 3 : 2;
-  static constexpr int ROWB = CW * (int)sizeof(E), P = 64 / (ROWB < 64 ? ROWB : 64);  // row sets to 1 KB
-  static constexpr int STAGE = PIECES ? R * 16 * ROWB : 16;
+  static constexpr int ROWB = CW * (int)sizeof(E), P = CG == 8 ? 1 : 64 / (ROWB < 64 ? ROWB : 64);  // row sets to 1 KB
+  static constexpr int STAGE = PIECES ? R * GW * ROWB : 16;
   float map[2][NW][2][CW], carry[2][2][CW];
   __attribute__((aligned(1024))) char in[NW][NT][STAGE];
   __attribute__((aligned(1024))) char out[NW][BWD ? 2 : 1][PIECES ? 1024 : 16];
 };
 
-template <typename E, int V, int NW, int R, bool BWD, int MODE, bool PIECES>
+template <typename E, int V, int NW, int R, bool BWD, int MODE, bool PIECES, int CG>
 __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
-  using Lds = GlrLds<E, V, NW, R, BWD, MODE, PIECES>;
-  constexpr int CG = 4, GW = 16;      // channel groups; row groups of a wave
+  using Lds = GlrLds<E, V, NW, R, BWD, MODE, PIECES, CG>;
+  constexpr int GW = 64 / CG;         // CG channel groups, GW row groups of a wave
   constexpr int ROWS = NW * GW * R;   // rows of a tile
   constexpr int CW = CG * V, P = Lds::P, NT = Lds::NT;
   constexpr bool HV = NT == 3;
   __shared__ Lds s;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int cg = lane >> 4, gw = lane & 15;
+  const int cg = lane / GW, gw = lane % GW;
   // workgroups go round the eight XCDs: the slices of one 128-byte line stay on one, side by
   // side in time, so that its L2 reads the line once
   const unsigned u = blockIdx.x / (8 * p.inner) * 8 + blockIdx.x % 8, in = blockIdx.x / 8 % p.inner;
@@ -133,8 +150,10 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
   const int slice = (u % p.lines) * p.inner + in;
   const int head = b % p.H;
   b /= p.H;
-  const int seq = b % p.N, seg = b / p.N;
+  int seq = b % p.N;
+  const int seg = b / p.N;
   if (seg >= p.nseg || slice * CW >= p.d) return;
+  if (MODE == GLR_WHOLE && p.ordered) seq = p.order[seq];
 
   // the tokens of this sequence (device cu_seqlens clamped to [0, T]), then of the segment
   int t0 = 0, t1 = p.T;
@@ -189,7 +208,7 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
   auto low = [&](int base, int n) { return BWD ? t1 - skip - base - n : t0 + skip + base; };
   // PIECES: this lane's 16 bytes of a row, row set and row group (P row sets to a load)
   constexpr int LPR = PIECES ? Lds::ROWB / 16 : 1;
-  const int piece = lane % LPR, slot = lane / LPR, dgw = slot % 16, dr = slot / 16;
+  const int piece = lane % LPR, slot = lane / LPR, dgw = slot % GW, dr = slot / GW;
   const int dc = slice * CW + piece * (16 / (int)sizeof(E));
   const bool dlive = dc < p.d;
   const unsigned dcol = (dlive ? dc : 0) * (unsigned)sizeof(E);
@@ -209,9 +228,9 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
       for (int i = 0; i < R / P; ++i) {
         const int j = min(dj + i * P, n - 1), k = BWD ? n - 1 - j : j;  // past the end: the last
         const unsigned off = (unsigned)k * pitch + dcol;
-        pre[0][i] = ldg16((const char *)x + off);
-        pre[1][i] = ldg16((const char *)g + off);
-        if constexpr (HV) pre[2][i] = ldg16((const char *)h + ((unsigned)max(k - back, 0) * pitch + dcol));
+        pre[0][i] = ldq<CG == 8>((const char *)x + off);
+        pre[1][i] = ldq<CG == 8>((const char *)g + off);
+        if constexpr (HV) pre[2][i] = ldq<CG == 8>((const char *)h + ((unsigned)max(k - back, 0) * pitch + dcol));
       }
     } else {
 #pragma unroll
@@ -226,7 +245,7 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
   };
   // this lane's row r of a tensor in the stage
   auto staged = [&](int t, int r) {
-    return s.in[wave][t] + (r / P) * 1024 + ((r % P) * 16 + gw) * Lds::ROWB + cg * V * (int)sizeof(E);
+    return s.in[wave][t] + (r / P) * 1024 + ((r % P) * GW + gw) * Lds::ROWB + cg * V * (int)sizeof(E);
   };
   // A wave has rows in the tile from base on, but in a sequence's last tile.  The branch pays
   // where sequences may be short; in tiles of 1,024 rows, for long ones, it cost 4%.
@@ -299,10 +318,10 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
           C[i] = BWD ? a[r][i] * (C[i] + x) : fmaf(a[r][i], C[i], x);
           A[i] *= a[r][i];
         }
-      scan_step<1, V>(A, C);
-      scan_step<2, V>(A, C);
-      scan_step<4, V>(A, C);
-      scan_step<8, V>(A, C);
+      scan_step<1, V, GW>(A, C, gw);
+      scan_step<2, V, GW>(A, C, gw);
+      scan_step<4, V, GW>(A, C, gw);
+      scan_step<8, V, GW>(A, C, gw);
     }
     if (gw == GW - 1) {
 #pragma unroll
@@ -348,7 +367,7 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
     if (MODE != GLR_MAPS && (R == 8 || base + w0 < len)) {
       // the value before this thread's rows
 #pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = fmaf(row_shr<1>(1.f, A[i]), y[i], row_shr<1>(0.f, C[i]));
+      for (int i = 0; i < V; ++i) y[i] = fmaf(group_shr<1, GW>(1.f, A[i], gw), y[i], group_shr<1, GW>(0.f, C[i], gw));
       const int n = min(ROWS, len - base);
       const size_t first = (row0 + low(base, n)) * p.d;
       // rows r of all lanes: through LDS into whole rows (PIECES), or each lane its own piece
@@ -357,7 +376,7 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
           Vec<E, V> w;
 #pragma unroll
           for (int i = 0; i < V; ++i) w.v[i] = Elem<E>::from_f32(f[i]);
-          char *at = s.out[wave][t] + ((r % P) * 16 + gw) * Lds::ROWB + cg * V * (int)sizeof(E);
+          char *at = s.out[wave][t] + ((r % P) * GW + gw) * Lds::ROWB + cg * V * (int)sizeof(E);
           __builtin_memcpy(__builtin_assume_aligned(at, V * sizeof(E)), &w, V * sizeof(E));
           if (r % P == P - 1) {
             const uint4 q = *reinterpret_cast<const uint4 *>(s.out[wave][t] + 16 * lane);
@@ -435,9 +454,9 @@ __global__ __launch_bounds__(256) void kla_glr_step_kernel(const E *__restrict__
   st<E, V>(o + i, h);
 }
 
-template <typename E, int V, int NW, int R, bool BWD, bool PIECES>
+template <typename E, int V, int NW, int R, bool BWD, bool PIECES, int CG = 4>
 struct GlrShape {
-  static constexpr int ROWS = NW * 16 * R, CW = 4 * V;
+  static constexpr int CW = CG * V;
   static constexpr int INNER = 128 / (CW * (int)sizeof(E)) > 1 ? 128 / (CW * (int)sizeof(E)) : 1;
   template <int MODE>
   static void go(GlrParams p, long long segs, hipStream_t st) {
@@ -446,7 +465,7 @@ struct GlrShape {
     p.lines = (p.d + CW * p.inner - 1) / (CW * p.inner);
     const long long units = (long long)p.N * p.H * p.lines * segs;
     const long long grid = (units + 7) / 8 * 8 * p.inner;
-    hipLaunchKernelGGL((kla_glr_kernel<E, V, NW, R, BWD, MODE, PIECES>), dim3((unsigned)grid), dim3(64 * NW), 0, st, p);
+    hipLaunchKernelGGL((kla_glr_kernel<E, V, NW, R, BWD, MODE, PIECES, CG>), dim3((unsigned)grid), dim3(64 * NW), 0, st, p);
   }
   static hipError_t whole(const GlrParams &p, hipStream_t st) {
     go<GLR_WHOLE>(p, 1, st);
@@ -475,10 +494,18 @@ struct GlrShape {
 // bytes, 19 with segments), nor for tiles of 1,024 rows (5,000 channels, 1,500 tokens: 19 us
 // whole, 25 with 32 bytes).
 //
+// Slices of a whole line (8 channel groups for 4, a wave's rows half as many) where they fill the
+// CUs: no other workgroup wants their lines, which then go past the caches.  A workgroup takes
+// most of a CU's LDS, so the last round must not be much emptier than the others: dense batches
+// whose lines fill five sixths of their rounds (128 sequences and heads of d=128, T=4096: backward
+// 120 us against 148 with 64 bytes, 256 forward 143 against 174, in fp32 138 against 197; 192:
+// 136 against 129), packed ones from 640 lines on (20 of 300 to 3,000 tokens, 16 heads: 55 us
+// against 69; 16 of 512 to 16,384 tokens 171 against 139).
+//
 // Tiles fit the longest sequence: one wave's 64 rows, four waves' 256 or eight waves' 512 (19
 // sequences of 2 to 7 tokens, 16 heads of 2,560 channels: 37 us against 393 with 512 rows).
 struct GlrPlan {
-  bool pieces, narrow;
+  bool pieces, narrow, line;
   int waves;
   int segs, seg_rows;
 };
@@ -489,7 +516,11 @@ GlrPlan glr_plan(const GlrArgs &a) {
   const bool pieces = a.d * (long long)e % 16 == 0 && (long long)a.d * e <= (1 << 20);
   const int V = pieces ? 16 / e : (a.d % (8 / e) == 0 ? 8 / e : 1);
   const long long wide = (long long)a.num_seqs * a.H * ((a.d + 4 * V - 1) / (4 * V));
-  GlrPlan r{pieces, false, a.longest <= 64 ? 1 : (a.longest <= 256 ? 4 : 8), 1, 0};
+  GlrPlan r{pieces, false, false, a.longest <= 64 ? 1 : (a.longest <= 256 ? 4 : 8), 1, 0};
+  const long long lines = (long long)a.num_seqs * a.H * a.d * e / 128;
+  r.line = pieces && (long long)a.d * e % 128 == 0 && r.waves == 8 &&
+           (a.cu_seqlens ? lines >= 640 : lines >= 256 && (lines + 255) / 256 * 256 * 5 <= lines * 6);
+  if (r.line) return r;
   if (wide == 0 || wide >= 256 || a.longest <= 2048) return r;
   if (pieces && (wide >= 128 || a.longest <= 3584)) {
     r.narrow = true;
@@ -512,6 +543,7 @@ hipError_t launch_glr_v(const GlrParams &p, const GlrPlan &plan, hipStream_t st)
 template <typename E, bool BWD>
 hipError_t launch_glr(const GlrParams &p, const GlrPlan &plan, hipStream_t st) {
   constexpr int V = 16 / sizeof(E);
+  if (plan.line) return GlrShape<E, V, 8, 4, BWD, true, 8>::whole(p, st);
   if (plan.narrow) return GlrShape<E, V / 2, 8, 8, BWD, true>::whole(p, st);
   if (plan.pieces) return launch_glr_v<E, V, BWD, true>(p, plan, st);
   if (p.d % (V / 2) == 0) return launch_glr_v<E, V / 2, BWD, false>(p, plan, st);
@@ -523,7 +555,7 @@ hipError_t launch_glr(const GlrParams &p, const GlrPlan &plan, hipStream_t st) {
 bool glr_grid_fits(const GlrArgs &a) {
   const GlrPlan plan = glr_plan(a);
   const int e = a.dtype == 0 ? 2 : 4, V = plan.pieces ? (plan.narrow ? 8 : 16) / e : (a.d % (8 / e) == 0 ? 8 / e : 1);
-  const int inner = std::max(1, 128 / (4 * V * e)), lines = (a.d - 1) / (4 * V * inner) + 1;
+  const int inner = plan.line ? 1 : std::max(1, 128 / (4 * V * e)), lines = (a.d - 1) / ((plan.line ? 8 : 4) * V * inner) + 1;
   return launch_fits(((double)a.num_seqs * a.H * lines * plan.segs + 7) * inner, 64 * plan.waves);
 }
 
@@ -551,6 +583,15 @@ hipError_t launch_glr_chunk(const GlrArgs &a, bool bwd, hipStream_t st) {
   p.segs = plan.segs;
   p.seg_rows = plan.seg_rows;
   p.maps = (float *)a.workspace;
+  // Packed sequences of several tiles start in the order of their lengths, the longest first (32
+  // of 512 to 16,384 tokens, 16 heads of d=128, backward: 564 us against 627 as they come).  The
+  // order is the host's lengths'; other lengths on the device cost time alone.
+  p.ordered = a.cu_seqlens && a.num_seqs > 1 && a.num_seqs <= GLR_ORDER && plan.waves == 8 && plan.segs == 1;
+  if (p.ordered) {
+    for (int n = 0; n < a.num_seqs; ++n) p.order[n] = n;
+    const int32_t *cu = a.cu_seqlens_host;
+    std::stable_sort(p.order, p.order + a.num_seqs, [cu](int i, int j) { return cu[i + 1] - cu[i] > cu[j + 1] - cu[j]; });
+  }
   if (a.dtype == 0) return bwd ? launch_glr<bf16, true>(p, plan, st) : launch_glr<bf16, false>(p, plan, st);
   return bwd ? launch_glr<float, true>(p, plan, st) : launch_glr<float, false>(p, plan, st);
 }

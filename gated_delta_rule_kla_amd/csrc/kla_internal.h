@@ -141,7 +141,7 @@ struct GlrArgs {
   const float *y0, *h0;
   void *o, *dg;
   float *yend;
-  const int32_t *cu_seqlens;  // device, or nullptr
+  const int32_t *cu_seqlens, *cu_seqlens_host;  // device and host, or nullptr
   int num_seqs, H, T, d, dtype;
   int longest;                // tokens of the longest sequence
   void *workspace;            // device, glr_workspace_bytes(*this) bytes

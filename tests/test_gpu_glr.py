@@ -82,6 +82,25 @@ def test_long_with_few_channels(dtype, d, cu):
     check(dtype, 1, 1, 5200, d, cu, seed=d, slow=0.02)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,H,T,cu,lines", [(4, 64, 600, None, 1), (2, 64, 1100, None, 2),
+                                            (1, 64, 3500, [0, 0, 700, 701, 1000, 1020, 1600, 1620, 2900, 2990, 3500], 1)])
+def test_whole_lines(dtype, B, H, T, cu, lines):
+    """Many heads of one or two 128-byte lines; packed, the longest sequences start first."""
+    check(dtype, B, H, T, lines * (64 if dtype == BF else 32), cu, seed=T, slow=0.05)
+
+
+def test_order_of_other_lengths():
+    """The launch's order is the host's lengths'; a replayed graph may hold others."""
+    x, g, h0, *_ = (t.to(DEV) for t in inputs(BF, 1, 64, 3000, 64, [0, 1, 2], seed=11))
+    h0 = h0[:1].expand(10, 64, 64).contiguous()
+    host = torch.arange(0, 3001, 300, dtype=torch.int32)
+    cu = torch.tensor([0, 10, 900, 901, 1500, 1500, 1600, 2000, 2900, 2950, 3000], dtype=torch.int32)
+    want = kla.glr_chunk_fwd(x, g, h0, cu.to(DEV), cu_seqlens_host=cu)
+    got = kla.glr_chunk_fwd(x, g, h0, cu.to(DEV), cu_seqlens_host=host)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("T", [4, 3000])
 def test_without_states(T):
     check(F32, 1, 1, T, 16, states=False)
