@@ -24,7 +24,8 @@
 //
 // Where few channels leave most CUs idle, sequences are cut into segments: a first pass forms
 // each segment's map, and the second starts every segment from the maps of those before it; it
-// reads x and g twice (glr_plan has the rule).
+// reads x and g twice (glr_plan has the rule).  Plans go by the host's lengths, tokens by the
+// device's: where those differ, results are the device's and only time is lost.
 #include <algorithm>
 
 #include "kla_common.h"
@@ -167,7 +168,9 @@ __global__ __launch_bounds__(64 * NW) void kla_glr_kernel(GlrParams p) {
   const int len_seq = t1 - t0;
   const int skip = MODE == GLR_WHOLE ? 0 : seg * p.seg_rows;  // scan steps before this segment
   if (MODE != GLR_WHOLE && seg > 0 && skip >= len_seq) return;
-  const int len = MODE == GLR_WHOLE ? len_seq : min(len_seq - skip, p.seg_rows);
+  // the last segment takes the rest: the host's lengths set the segments, the device's may be longer
+  const bool rest = MODE == GLR_WHOLE || (MODE == GLR_CARRIED && seg == p.nseg - 1);
+  const int len = rest ? len_seq - skip : min(len_seq - skip, p.seg_rows);
   const bool last_seg = skip + len == len_seq;
 
   const int c = slice * CW + cg * V;

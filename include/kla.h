@@ -462,7 +462,10 @@ kla_status_t kla_pgdn_decode_step(const void *q, const void *k, const void *v,
  *   final_state    [N, H, d] fp32, or NULL = not written.  May alias initial_state; no other
  *                  aliasing is allowed.
  *   cu_seqlens, cu_seqlens_host, num_seqs (N), B, H, T: as kla_chunk_fwd, without its
- *                  limit on H
+ *                  limit on H.  The mirror only sets how the call runs: with other offsets on
+ *                  the device (a captured call that is replayed with other lengths; not
+ *                  decreasing, within [0, T]) results are theirs, and rows that belong to no
+ *                  sequence are left as they were
  *   workspace      kla_glr_chunk_workspace_bytes(...) bytes for the same arguments (16-byte
  *                  aligned, no initialisation needed; NULL when that is 0)
  *
