@@ -85,8 +85,10 @@ __device__ __forceinline__ void st8(E *p, const float *f) {
 
 // A workgroup moves TOKENS consecutive tokens of one head's keys or values: as many threads find
 // their places (sequence, position, page) while the other loads are in flight, then D / 8 lanes
-// move a row.  Many tokens: 256 to a workgroup, and their rows past the caches (ONCE).
+// move a row.  A token that the device's offsets give to no sequence (a padded batch) is not
+// moved.  Many tokens: 256 to a workgroup, and their rows past the caches (ONCE).
 constexpr int KV_CU = 1024;  // offsets searched in LDS
+constexpr int KV_NO_PLACE = -1, KV_NO_SEQ = -2;  // rows: outside the table's pages, of no sequence
 
 template <typename E, int D, bool READ, int TOKENS, bool ONCE>
 __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
@@ -115,9 +117,10 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
   }
   if (tid < TOKENS) {
     const long long tok = tok0 + tid;
-    long long row = -1;
+    long long row = KV_NO_SEQ;
     if (tok < toks) {
       int n = (int)(tok / p.T), at = (int)(tok % p.T);
+      bool in = true;
       if (p.cu) {
         // the last sequence that starts at or before the token (its offsets not decreasing)
         int lo = 0, hi = p.N;
@@ -126,10 +129,12 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
           if ((near ? s_cu[mid] : p.cu[mid]) <= at) lo = mid; else hi = mid;
         }
         n = lo;
-        at -= max(near ? s_cu[n] : p.cu[n], 0);
+        const int first = near ? s_cu[n] : p.cu[n], end = near ? s_cu[n + 1] : p.cu[n + 1];
+        in = at >= first && at < end;
+        at -= max(first, 0);
       }
       const long long pos = (long long)p.start[n] + at;
-      if (pos >= 0 && pos <= 0x7fffffffLL) row = kv_row(p.kv, n, (int)pos, j, head);
+      if (in) row = pos >= 0 && pos <= 0x7fffffffLL ? kv_row(p.kv, n, (int)pos, j, head) : KV_NO_PLACE;
     }
     s_row[tid] = row;
   }
@@ -154,7 +159,7 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
       const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u[r], s, 3);
       const float y[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
       const int i = tid / LPR + 256 / LPR * r;
-      if (tok0 + i < toks) st8<E, ONCE>(x_of(i), y);
+      if (s_row[i] != KV_NO_SEQ) st8<E, ONCE>(x_of(i), y);
     }
   } else {
 #pragma unroll

@@ -583,7 +583,9 @@ kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float sca
  *
  * kla_kv4_append stores k and v at their positions, kla_kv4_read writes the stored values of
  * those positions to k and v (a prompt that is continued after cached tokens attends to them
- * with kla_attn_fwd).  A position outside the block table, or whose page is outside
+ * with kla_attn_fwd).  The mirror sizes the launch, places go by the device's offsets: a token in
+ * front of the first sequence or behind the last (a padded batch) is not stored, and its row of
+ * a read is left as it was.  A position outside the block table, or whose page is outside
  * [0, num_pages), is not stored and reads as zero (a negative page or start marks padding);
  * nothing else of the cache is touched.  Two tokens of one call that share a place leave
  * either's codes and scales, mixed: a place belongs to one token.
