@@ -133,8 +133,10 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
         in = at >= first && at < end;
         at -= max(first, 0);
       }
-      const long long pos = (long long)p.start[n] + at;
-      if (in) row = pos >= 0 && pos <= 0x7fffffffLL ? kv_row(p.kv, n, (int)pos, j, head) : KV_NO_PLACE;
+      // a negative start: all of the sequence is padding
+      const int start = p.start[n];
+      const long long pos = (long long)start + at;
+      if (in) row = start >= 0 && pos <= 0x7fffffffLL ? kv_row(p.kv, n, (int)pos, j, head) : KV_NO_PLACE;
     }
     s_row[tid] = row;
   }

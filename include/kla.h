@@ -586,8 +586,9 @@ kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float sca
  * with kla_attn_fwd).  The mirror sizes the launch, places go by the device's offsets: a token in
  * front of the first sequence or behind the last (a padded batch) is not stored, and its row of
  * a read is left as it was.  A position outside the block table, or whose page is outside
- * [0, num_pages), is not stored and reads as zero (a negative page or start marks padding);
- * nothing else of the cache is touched.  Two tokens of one call that share a place leave
+ * [0, num_pages), is not stored and reads as zero, and so are all tokens of a sequence whose
+ * start is negative (a negative page or start marks padding); nothing else of the cache is
+ * touched.  Two tokens of one call that share a place leave
  * either's codes and scales, mixed: a place belongs to one token.
  *
  * Supported: D 64 or 128, page_size a multiple of 16 up to 2^20, either dtype; B * Hkv * T

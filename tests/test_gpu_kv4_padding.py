@@ -43,3 +43,27 @@ def test_tokens_of_no_sequence(dtype, N):
     for x, y in ((k, out[0]), (v, out[1])):
         assert (y[:, :, :2] == 7).all() and (y[:, :, 3 * N:] == 7).all()
         np.testing.assert_array_equal(f64(y[:, :, 2:3 * N]), values(*quantise(f64(x[:, :, 2:3 * N]))))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dense", [False, True])
+def test_a_negative_start_is_padding(dtype, dense):
+    """For all tokens of the sequence, also those that would come to lie at position 0 and up."""
+    start = torch.tensor([3, -1, -5, -2 ** 31], dtype=torch.int32, device=DEV)
+    table = torch.arange(8, dtype=torch.int32, device=DEV).reshape(4, 2)
+    k, v = make_kv([24], 2, 64, dtype, 2)
+    codes, scales = kla.kv4_cache(8, 2, 16, 64, DEV)
+    host = torch.tensor([0, 6, 12, 18, 24], dtype=torch.int32)
+    if dense:
+        rows = [t.view(2, 4, 6, 64).transpose(0, 1).contiguous() for t in (k[0], v[0])]
+        kla.kv4_append(*rows, codes, scales, table, start)
+    else:
+        kla.kv4_append(k, v, codes, scales, table, start, host.to(DEV), host)
+    assert codes[0, :, :, 3:9].any(-1).all()
+    codes[0, :, :, 3:9], scales[0, :, :, 3:9] = 0, 0
+    assert not codes.any() and not scales.any()
+    codes.fill_(0x22)  # ones, times 2^0
+    scales.fill_(127)
+    y = kla.kv4_read(codes, scales, table, start, host.to(DEV), dtype, host)
+    for t in y:
+        assert (t[:, :, :6] == 1).all() and not t[:, :, 6:].any()
