@@ -89,10 +89,16 @@ __device__ __forceinline__ void place(const AttnParams &p, unsigned id, int *bh,
 // 1 KB straight from global memory, at a scalar address and each lane's byte offset, into LDS
 // at byte `at`: lane i's 16 bytes land 16 i behind.  In asm, since the compiler makes the next
 // LDS read wait for the builtin's load, also where it goes to the other buffer; the kernel
-// itself waits (vmcnt) before the barrier that ends a tile.  It has no output register.
+// itself waits (vmcnt) before the barrier that ends a tile.  It has no output register.  m0 is
+// listed so that no value which the compiler keeps there lives across it; the compiler warns of
+// every reserved register in such a list.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds(const bf16 *src, unsigned lane_at, unsigned at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(lane_at), "s"(src) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(lane_at), "s"(src)
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // One query against keys 0 .. n-1 by one wave, key by key.
 template <typename E, int D>
