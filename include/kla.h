@@ -544,7 +544,8 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
  *   cu_seqlens, cu_seqlens_host, num_seqs (N), B, Tq: the queries' sequences, as kla_chunk_fwd's
  *   cu_seqlens_k, cu_seqlens_k_host  the keys' (N + 1 offsets to Tk), for packed sequences
  *              only; NULL: the queries' offsets (Tk = Tq).  Dense batches: Tq queries and Tk
- *              keys in every row.
+ *              keys in every row.  As for kla_glr_chunk_fwd, the device's offsets decide, and
+ *              queries of no sequence keep what o and lse hold.
  *
  * Supported: D 64 or 128, either dtype.  Scores, softmax and sums are fp32; with BF16 the
  * weights are rounded to bf16 before they meet the values (half a step of 2^-8 each, as much
