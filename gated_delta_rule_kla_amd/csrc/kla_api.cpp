@@ -305,6 +305,9 @@ kla_status_t check_kv4_decode(int N, int Hq, int Hkv, int D, int num_pages, int 
   return kla::kv4_decode_grid_fits(*a) ? KLA_OK : KLA_ERR_SHAPE;
 }
 
+// Attention's scale, also as the kernels take it: times log2(e).
+bool good_scale(float scale) { return std::isfinite(scale * 1.44269504f); }
+
 float band_log(float band) { return band == 1.f ? 0.f : std::log(band); }
 
 }  // namespace
@@ -387,7 +390,7 @@ const char *kla_status_str(kla_status_t s) {
     case KLA_ERR_ALIGN: return "data pointers must be 16-byte aligned";
     case KLA_ERR_WORKSPACE: return "workspace missing or smaller than kla_chunk_workspace_bytes()";
     case KLA_ERR_HIP: return "HIP runtime error";
-    case KLA_ERR_PARAM: return "gain must be a kla_gain_t and band finite and >= 1; an attention scale finite";
+    case KLA_ERR_PARAM: return "gain must be a kla_gain_t and band finite and >= 1; an attention scale finite, up to 2.3e38";
     case KLA_ERR_SCRATCH: return "the call needs more scratch than kla_chunk_fwd_noalloc's fixed buffer holds";
   }
   return "unknown status";
@@ -610,7 +613,7 @@ kla_status_t kla_attn_kv4_decode_step(const void *q, const void *codes, const vo
   const kla_status_t st =
       check_kv4_decode(N, Hq, Hkv, D, num_pages, page_size, max_pages, max_len, raw(dtype_), &a);
   if (st != KLA_OK) return st;
-  if (!std::isfinite(scale)) return KLA_ERR_PARAM;
+  if (!good_scale(scale)) return KLA_ERR_PARAM;
   if (N == 0) return KLA_OK;
   if (!q || !codes || !scales || !block_table || !seq_lens || !o) return KLA_ERR_NULL;
   if (misaligned(q) || misaligned(codes) || misaligned(scales) || misaligned4(block_table) ||
@@ -639,7 +642,7 @@ kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float sca
     return KLA_ERR_SHAPE;
   if (!kla::attn_supported(dtype, D)) return KLA_ERR_UNSUPPORTED;
   if ((long long)B * Hq > 0x7fffffffLL) return KLA_ERR_SHAPE;
-  if (!std::isfinite(scale)) return KLA_ERR_PARAM;
+  if (!good_scale(scale)) return KLA_ERR_PARAM;
   int longest;
   kla_status_t st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, Tq, &longest);
   if (st != KLA_OK) return st;

@@ -66,7 +66,7 @@ typedef enum {
     KLA_ERR_HIP = -9,         /* the HIP runtime rejected a launch               */
     KLA_ERR_SCRATCH = -10,    /* kla_chunk_fwd_noalloc: more scratch than its fixed buffer */
     KLA_ERR_PARAM = -11       /* PGDN: gain not a kla_gain_t, or band not finite and >= 1;
-                                 attention: scale not finite                     */
+                                 attention: scale not finite, or beyond 2.3e38   */
 } kla_status_t;
 
 /* The update coefficient ("gain") of the preconditioned variant (kla_pgdn_*). */
@@ -539,7 +539,7 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
  *
  *   q, o       [B, Hq, Tq, D]   dtype; Hq a multiple of Hkv
  *   k, v       [B, Hkv, Tk, D]  dtype
- *   scale      finite (1 / sqrt(D) in most models)
+ *   scale      finite, up to 2.3e38 in magnitude (1 / sqrt(D) in most models)
  *   lse        [B, Hq, Tq] fp32, or NULL (not written)
  *   cu_seqlens, cu_seqlens_host, num_seqs (N), B, Tq: the queries' sequences, as kla_chunk_fwd's
  *   cu_seqlens_k, cu_seqlens_k_host  the keys' (N + 1 offsets to Tk), for packed sequences
@@ -552,7 +552,7 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
  * as o's own rounding).  Keys and values that a query does not see do not reach it, also
  * where they are infinite or NaN (queries that such a value reaches are computed key by key,
  * which is slow).  No workspace, no aliasing; results repeat bit for bit.  Status codes as
- * kla_chunk_fwd, KLA_ERR_PARAM for a scale that is not finite.
+ * kla_chunk_fwd, KLA_ERR_PARAM for another scale.
  */
 kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float scale, void *o, float *lse,
                           const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
@@ -616,7 +616,7 @@ kla_status_t kla_kv4_read(void *k, void *v, const void *codes, const void *scale
  *   q, o        [N, Hq, D] dtype; Hq a multiple of Hkv
  *   seq_lens    device int32 [N]: cached tokens of each sequence, the new one's among them
  *               (append it first).  0: o is zero.
- *   scale       finite (1 / sqrt(D) in most models)
+ *   scale       finite, up to 2.3e38 in magnitude (1 / sqrt(D) in most models)
  *   max_len     host bound on seq_lens, which sizes the launch and the workspace; a longer
  *               sequence is read up to max_len, and none beyond its block table
  *   workspace   kla_attn_kv4_decode_workspace_bytes(...) bytes, as kla_chunk_fwd's
