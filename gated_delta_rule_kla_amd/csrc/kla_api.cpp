@@ -388,7 +388,7 @@ const char *kla_status_str(kla_status_t s) {
     case KLA_ERR_SEQLENS: return "cu_seqlens must be non-decreasing from 0 to T";
     case KLA_ERR_EPS: return "eps must be finite and >= 0";
     case KLA_ERR_ALIGN: return "data pointers must be 16-byte aligned";
-    case KLA_ERR_WORKSPACE: return "workspace missing or smaller than kla_chunk_workspace_bytes()";
+    case KLA_ERR_WORKSPACE: return "workspace missing or smaller than the entry point's _workspace_bytes function says";
     case KLA_ERR_HIP: return "HIP runtime error";
     case KLA_ERR_PARAM: return "gain must be a kla_gain_t and band finite and >= 1; an attention scale finite, up to 2.3e38";
     case KLA_ERR_SCRATCH: return "the call needs more scratch than kla_chunk_fwd_noalloc's fixed buffer holds";

@@ -61,7 +61,8 @@ typedef enum {
     KLA_ERR_UNSUPPORTED = -4, /* valid but not compiled: see supported shapes    */
     KLA_ERR_SEQLENS = -5,     /* cu_seqlens not 0 = c0 <= c1 <= ... <= cN = T    */
     KLA_ERR_EPS = -6,         /* eps < 0, NaN or infinite                        */
-    KLA_ERR_WORKSPACE = -7,   /* workspace NULL or below kla_chunk_workspace_bytes */
+    KLA_ERR_WORKSPACE = -7,   /* workspace NULL or below the entry point's
+                                 _workspace_bytes function                       */
     KLA_ERR_ALIGN = -8,       /* a data pointer is not 16-byte aligned           */
     KLA_ERR_HIP = -9,         /* the HIP runtime rejected a launch               */
     KLA_ERR_SCRATCH = -10,    /* kla_chunk_fwd_noalloc: more scratch than its fixed buffer */

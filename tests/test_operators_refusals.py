@@ -33,3 +33,14 @@ def test_scales_beyond_fp32_in_base_two(call, scale):
 @pytest.mark.parametrize("scale", [2.3e38, -2.3e38, 0.0, 1e-45])
 def test_scales_that_are_taken(call, scale):
     assert call(scale, q=None) == NULL  # past the scale's check
+
+
+def test_a_missing_workspace_names_no_other_operators_function():
+    """The status is shared: its text must not send a caller of the recurrence or of the decode step
+    to kla_chunk_workspace_bytes."""
+    lib = kla.lib()
+    st = lib.kla_attn_kv4_decode_step(FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, FAKE, 2, 8, 4, 128, 8, 16, 10000, 100000, 0,
+                                      None, 0, None)
+    assert st == WORKSPACE
+    text = lib.kla_status_str(st).decode()
+    assert "workspace" in text and "kla_chunk" not in text
