@@ -88,7 +88,6 @@ __device__ __forceinline__ void st8(E *p, const float *f) {
 // move a row.  A token that the device's offsets give to no sequence (a padded batch) is not
 // moved.  Many tokens: 256 to a workgroup, and their rows past the caches (ONCE).
 constexpr int KV_CU = 1024;  // offsets searched in LDS
-constexpr int KV_NO_PLACE = -1, KV_NO_SEQ = -2;  // rows: outside the table's pages, of no sequence
 
 template <typename E, int D, bool READ, int TOKENS, bool ONCE>
 __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
@@ -102,8 +101,8 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
   E *const base = (E *)(j ? p.v : p.k);
 
   auto x_of = [&](int i) {  // row i of the workgroup (the last one's again past the end)
-    const long long tok = min(tok0 + i, toks - 1);
-    return base + (((tok / p.T) * p.kv.Hkv + head) * p.T + tok % p.T) * D + 8 * lane;
+    const long long tok = min(tok0 + i, toks - 1), b = p.cu ? 0 : tok / p.T;  // packed: one row of the batch
+    return base + ((b * p.kv.Hkv + head) * p.T + (tok - b * p.T)) * D + 8 * lane;
   };
   float f[RPT][8];
   if constexpr (!READ) {
@@ -115,12 +114,20 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
     for (int i = tid; i <= p.N; i += 256) s_cu[i] = p.cu[i];
     __syncthreads();
   }
+  // The workgroup's tokens that belong to sequences; a read writes no other rows.  Their bounds
+  // are compared, not kept with each place: a flag read back per row took fp32 reads of 131,000
+  // tokens from 147 to 172 us.
+  auto within = [&](long long tok) { return (int)max(min(tok - tok0, (long long)TOKENS), 0LL); };
+  int from = 0, to = within(toks);
+  if (p.cu) {
+    from = within(near ? s_cu[0] : p.cu[0]);
+    to = min(to, within(near ? s_cu[p.N] : p.cu[p.N]));
+  }
   if (tid < TOKENS) {
     const long long tok = tok0 + tid;
-    long long row = KV_NO_SEQ;
-    if (tok < toks) {
-      int n = (int)(tok / p.T), at = (int)(tok % p.T);
-      bool in = true;
+    long long row = -1;
+    if (tid >= from && tid < to) {
+      int n = p.cu ? 0 : (int)(tok / p.T), at = (int)(tok - (long long)n * p.T);
       if (p.cu) {
         // the last sequence that starts at or before the token (its offsets not decreasing)
         int lo = 0, hi = p.N;
@@ -129,14 +136,12 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
           if ((near ? s_cu[mid] : p.cu[mid]) <= at) lo = mid; else hi = mid;
         }
         n = lo;
-        const int first = near ? s_cu[n] : p.cu[n], end = near ? s_cu[n + 1] : p.cu[n + 1];
-        in = at >= first && at < end;
-        at -= max(first, 0);
+        at -= max(near ? s_cu[n] : p.cu[n], 0);
       }
       // a negative start: all of the sequence is padding
       const int start = p.start[n];
       const long long pos = (long long)start + at;
-      if (in) row = start >= 0 && pos <= 0x7fffffffLL ? kv_row(p.kv, n, (int)pos, j, head) : KV_NO_PLACE;
+      if (start >= 0 && pos <= 0x7fffffffLL) row = kv_row(p.kv, n, (int)pos, j, head);
     }
     s_row[tid] = row;
   }
@@ -161,7 +166,7 @@ __global__ __launch_bounds__(256) void kla_kv4_move_kernel(KvMoveParams p) {
       const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u[r], s, 3);
       const float y[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
       const int i = tid / LPR + 256 / LPR * r;
-      if (s_row[i] != KV_NO_SEQ) st8<E, ONCE>(x_of(i), y);
+      if (i >= from && i < to) st8<E, ONCE>(x_of(i), y);
     }
   } else {
 #pragma unroll
