@@ -274,7 +274,7 @@ kla_status_t kv4_move(void *k, void *v, const void *codes, const void *scales, c
   int longest;
   st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, T, &longest);
   if (st != KLA_OK) return st;
-  if ((double)B * Hkv * T > (double)0x7fffffff || !kla::kv4_move_grid_fits(B, Hkv, T, dtype, read)) return KLA_ERR_SHAPE;
+  if ((double)B * Hkv * T > (double)0x7fffffff || !kla::kv4_move_grid_fits(B, Hkv, T, D, dtype, read)) return KLA_ERR_SHAPE;
   if (num_seqs == 0 || (long long)B * T == 0) return KLA_OK;
   if (!k || !v || !codes || !scales || !table || !start) return KLA_ERR_NULL;
   if (misaligned(k) || misaligned(v) || misaligned(codes) || misaligned(scales) || misaligned4(table) ||

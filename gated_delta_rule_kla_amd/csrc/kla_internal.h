@@ -160,7 +160,7 @@ struct Kv4Cache {
   const int32_t *table;
   int num_pages, page, max_pages, Hkv;
 };
-bool kv4_move_grid_fits(int B, int Hkv, int T, int dtype, bool read);
+bool kv4_move_grid_fits(int B, int Hkv, int T, int D, int dtype, bool read);
 hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,
                            int T, int D, int dtype, bool read, hipStream_t stream);
 struct Kv4DecodeArgs {

@@ -536,19 +536,20 @@ hipError_t launch_move_t(const KvMoveParams &p, hipStream_t st) {
 // Tokens of a workgroup, and whether the rows go past the caches, by the bytes of k and v.  From
 // 96 MB on (what the caches keep between calls) more tokens hide the search for their places,
 // and bf16 rows, written in whole lines, leave the caches to the codes: 131,000 tokens of 4 heads
-// of 128 (268 MB) append 66 us against 75 with 64 tokens, read 73 to 78 against 104; 96,000
-// tokens 49 and 41 us against 55 and 76; 32,000 tokens append 18.6 us against 19.8, read 23.3
-// against 20.5.  Reads below 256 MB do better with 128 tokens (96,000 tokens: 41 us against 47;
-// 256,000: 171 against 163).  fp32 rows are written in half lines, which must meet in the caches
-// (64,000 tokens: 83 us, 108 past them, 69 with 256 tokens); their appends take 61 us either way.
+// of 128 (268 MB) append 64 us against 75 with 64 tokens, 96,000 49 against 55; 32,000 the other
+// way 19.8 against 18.6.  A thread of a read holds eight rows: 128 tokens of 128 channels (96,000
+// tokens read in 41 us, with 256 tokens 46; 131,000 in 53, 60, with 64 tokens 104; 256,000 in 95,
+// 103), 256 tokens of 64 channels (8 heads: 96,000 in 41 us either way; 131,000 in 51, with 128
+// tokens 54; 256,000 in 95, 99; 400,000 in 145, 155).  fp32 rows are written in half lines, which
+// must meet in the caches (64,000 tokens past them 108 us, 63 to 69 with 256 tokens and 83 with
+// 64; 131,000 147, with 128 tokens 159); their appends take the same time either way.
 template <typename E, int D, bool READ>
 hipError_t launch_move(const KvMoveParams &p, hipStream_t st) {
   constexpr bool ONCE = sizeof(E) == 2;
+  constexpr int MANY = READ && ONCE ? 16384 / D : 256;
   const long long mb = p.rows * D * 2 * (long long)sizeof(E) >> 20;
-  if constexpr (READ && ONCE)
-    if (mb >= 96 && mb < 256) return launch_move_t<E, D, READ, 128, ONCE>(p, st);
   if constexpr (READ || ONCE)
-    if (mb >= 96) return launch_move_t<E, D, READ, 256, ONCE>(p, st);
+    if (mb >= 96) return launch_move_t<E, D, READ, MANY, ONCE>(p, st);
   return launch_move_t<E, D, READ, 64, false>(p, st);
 }
 
@@ -605,9 +606,10 @@ bool kv4_decode_grid_fits(const Kv4DecodeArgs &a) {
          launch_fits((double)a.N * a.Hq * (a.D / 32), 256);
 }
 
-bool kv4_move_grid_fits(int B, int Hkv, int T, int dtype, bool read) {
-  // large batches: 256 tokens to a workgroup but for appends in fp32
-  return launch_fits(((double)B * T / (read || dtype == 0 ? 256 : 64) + 1) * 2 * Hkv, 256);
+bool kv4_move_grid_fits(int B, int Hkv, int T, int D, int dtype, bool read) {
+  // a large batch's tokens to a workgroup: launch_move
+  const int tokens = read && dtype == 0 ? 16384 / D : (read || dtype == 0 ? 256 : 64);
+  return launch_fits(((double)B * T / tokens + 1) * 2 * Hkv, 256);
 }
 
 hipError_t launch_kv4_move(const Kv4Cache &c, void *k, void *v, const int32_t *start, const int32_t *cu, int N, int B,
