@@ -11,16 +11,17 @@
 //
 // The forward reads x and g and writes o once (6 bytes per element in bf16), the backward
 // reads g, o and do and writes dx and dg (10 bytes): both are bound by HBM.  One workgroup of
-// eight waves owns a slice of 64 (or 32, or 128) bytes of the rows of one (sequence, head) and walks
-// its tokens in tiles of 512 (1,024) rows, the next tile's 16-byte loads in flight in
-// registers.  A tile goes through LDS from the loads' order (consecutive lanes along a row) to
-// the scan's (lane = 16 channel groups' row groups): each lane composes R consecutive rows of V
-// channels, DPP row shifts compose the 16 row groups of a wave (two instructions a step and
-// channel), the waves' maps meet in LDS behind the one barrier of a tile, and the outputs go
-// back through LDS into whole row pieces.  Every byte is read once and no workgroup waits for
-// another.  Measured on B=4 H=16 T=4096 d=128: forward 46 us (4.4 TB/s; a copy of 1 GiB
-// reaches 5.2), 32 packed sequences of 268 M elements backward 564 us (4.8 TB/s); a first form
-// with the scan's steps as lane shuffles in the loads' order took 56 and 790 us.
+// eight waves owns a slice of 64 (or 32, or 128) bytes of the rows of one (sequence, head) and
+// walks its tokens in tiles of 512 rows (1,024 with 32 bytes, 256 with 128; 256 or 64 by four
+// waves or one for short sequences), the next tile's 16-byte loads in flight in registers.  A tile
+// goes through LDS from the loads' order (consecutive lanes along a row) to the scan's (a wave's
+// lanes are 4 groups of V channels times 16 row groups; with 128 bytes 8 times 8): each lane
+// composes R consecutive rows of its V channels, DPP row shifts compose the row groups of a wave
+// (two instructions a step and channel), the waves' maps meet in LDS behind the one barrier of a
+// tile, and the outputs go back through LDS into whole row pieces.  Every byte is read once and no
+// workgroup waits for another.  Measured on B=4 H=16 T=4096 d=128: forward 45 to 49 us (4.1 to 4.5
+// TB/s; a copy of 1 GiB reaches 5.2), 32 packed sequences of 268 M elements backward 564 us (4.8
+// TB/s); a first form with the scan's steps as lane shuffles in the loads' order took 56 and 790 us.
 //
 // Where few channels leave most CUs idle, sequences are cut into segments: a first pass forms
 // each segment's map, and the second starts every segment from the maps of those before it; it

@@ -470,12 +470,14 @@ kla_status_t kla_pgdn_decode_step(const void *q, const void *k, const void *v,
  *   workspace      kla_glr_chunk_workspace_bytes(...) bytes for the same arguments (16-byte
  *                  aligned, no initialisation needed; NULL when that is 0)
  *
- * Any d in [1, 2^24] and either dtype; d a multiple of 8 (BF16) or 4 (F32) moves 16 bytes at
- * a time, another d runs the same kernel an element at a time.  Sums and states are fp32.
+ * Any d in [1, 2^24] and either dtype.  Rows of a multiple of 16 bytes, up to 1 MiB, move 16
+ * bytes at a time; others run the same kernel with 8 bytes (d a multiple of 4 in BF16, of 2 in
+ * F32) or one element at a time.  Sums and states are fp32.
  * Decays are composed as products over runs of tokens: where g > 0 makes such a product
  * overflow fp32, outputs are not finite even if the recurrence would be.  Here and in the
  * functions below, sizes whose launch would have more than 2^32 threads are refused
- * (KLA_ERR_SHAPE): some 2^25 sequences and heads of one token.  Kernels run on `stream` only; results repeat bit for bit.  Status codes as kla_chunk_fwd.
+ * (KLA_ERR_SHAPE): some 2^25 sequences and heads of one token.  Kernels run on `stream` only;
+ * results repeat bit for bit.  Status codes as kla_chunk_fwd.
  */
 kla_status_t kla_glr_chunk_fwd(const void *x, const void *g, const float *initial_state,
                                void *o, float *final_state,

@@ -76,3 +76,10 @@ def test_closed_gates(dtype, plan):
     near(d0, r0, e0, F32, "dh0")
     shut = torch.isinf(g).to(DEV)
     assert not dg[shut].any()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 600000), (BF, 540001), (F32, 270002)])
+def test_rows_of_more_than_a_mebibyte(dtype, d):
+    """Whose offsets within a tile would pass 32 bits: they go 8 bytes or one element at a time."""
+    check(dtype, 1, 1, 9, d, seed=d, slow=0.3)
+    check(dtype, 1, 2, 5, d, cu=[0, 0, 2, 5], seed=d, slow=0.3)
