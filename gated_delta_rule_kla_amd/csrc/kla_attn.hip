@@ -273,7 +273,9 @@ __device__ __forceinline__ void finish(const AttnParams &p, const Span &s, int b
       p.lse[(size_t)bh * p.Tq + s.q0 + qw + r] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
   }
   // A value that is not finite, times the zero weight of a query that does not see it, is NaN
-  // in the matrix product: such queries are computed again from the keys that they see alone.
+  // in the matrix product: such queries are computed again from the keys that they see alone, one
+  // by one, also where they do see it (4,096 tokens of 16 heads, an infinity in an early value of
+  // eight: 21 ms against 0.08; 16,384: 0.27 s against 0.96 ms).
   for (unsigned left = again; left; left &= left - 1) {
     const int i = qw + __builtin_ctz(left);
     const size_t row = (size_t)bh * p.Tq + s.q0 + i;
@@ -436,8 +438,11 @@ __global__ __launch_bounds__(64 * NW, 2) void kla_attn_kernel(AttnParams p) {
 
 // fp32: the same two products with every operand split into three bf16 terms (24 bits), the
 // six products of terms that reach 2^-24 summed in fp32: 6 / 16 of the fp32 matrix
-// instructions' cycles for the same sums.  Tiles of 32 keys, split on their way from registers
-// (the next tile's loads in flight) into one LDS buffer.
+// instructions' cycles for the same sums.  A term ends at 2^-133, so numbers below 2^-109 keep
+// fewer bits.  Tiles of 32 keys, split on their way from registers (the next tile's loads in
+// flight) into one LDS buffer; the split of each tile, by every workgroup that reads it, and the two
+// barriers stand between the products.  4,096 tokens of 16 heads over 2: 443 us (six products at
+// a bf16 product's rate: 299), 64 channels 255; 16,384 tokens 6.5 ms (4.8).
 template <int D>
 __global__ __launch_bounds__(256, 1) void kla_attn_f32_kernel(AttnParams p) {
   constexpr int NW = 4, BM = 32 * NW, BN = 32;

@@ -575,12 +575,14 @@ KvParams kv_params(const Kv4Cache &c) {
   return KvParams{(uint8_t *)c.codes, (uint8_t *)c.scales, c.table, c.num_pages, c.page, c.max_pages, c.Hkv};
 }
 
-// Runs of the sequences: as many as bring about 1,024 workgroups (64 ragged sequences of 4
-// heads: 66 us, with 512 workgroups 84, with 768 78, with 2,048 73; sequences that all reach
-// max_len would do better with 768, one round: 32 of 30,000 tokens 90 us against 98, but the
-// lengths are the device's), of 384 tokens at least (three tiles a
-// wave; one sequence of 131,072 tokens, 2 heads: 16.6 us, with 256 tokens 19.0, with 512 18.2)
-// and KV_MAX_PER at most.
+// Runs of the sequences: as many as bring about 1,024 workgroups.  That is for sequences of
+// uneven lengths, 4 heads of D = 128: 64 of 4,096 to 16,384 tokens 66 us (with 512 workgroups 84,
+// with 768 78, with 1,536 77, with 2,048 73), 64 of 1,000 to 8,000 37 (768: 44, 1,536: 42), 24 of
+// 2,000 to 40,000 62 (71, 64); 10 of 8,000 to 60,000 with 8 heads 65 (64, 62).  Sequences that all
+// reach max_len do better with 768, one round, by 3 to 9%: 32 of 30,000 tokens 95 us against 92, 64
+// of 8,000 54 against 50, 8 of 8,000 with 8 heads 21.8 against 20.1; but the lengths are the
+// device's.  A run has 384 tokens at least (three tiles a wave; one sequence of 131,072 tokens,
+// 2 heads: 16.6 us, with 256 tokens 19.0, with 512 18.2) and KV_MAX_PER at most.
 void kv4_runs(const Kv4DecodeArgs &a, int *splits, int *per) {
   const long long GB = (a.Hq / a.c.Hkv + 15) / 16, base = (long long)a.N * a.c.Hkv * GB;
   long long want = std::max<long long>(1, 1024 / std::max<long long>(1, base));
