@@ -13,9 +13,9 @@
 // accumulator holds the keys (slot 8h + e of 16 keys is key 4h + e, or 8 + 4h + e - 4).  V^T
 // comes out of the row-major tile by transposing LDS reads.
 //
-// Measured: 16,384 tokens, 16 heads of 128 over 2: 0.94 to 0.97 ms, up to 1.17 PFLOP/s, where a bf16 product
+// Measured: 16,384 tokens, 16 heads of 128 over 2: 0.91 to 0.98 ms, up to 1.2 PFLOP/s, where a bf16 product
 // of 8192^3 reaches 1.38 and the clock falls below 2.0 GHz under either.  The matrix cores are
-// busy 59% of the cycles and the vector ALU 53%.  Tried on the way, at 0.98: two groups of
+// busy 60% of the cycles and the vector ALU 54%.  Tried on the way, at 0.98: two groups of
 // waves half a tile apart with a barrier between their phases 1.06 ms; three or four tiles in
 // LDS 0.99; the next tile's scores beside this tile's weights within a wave spilled (8,192
 // tokens, 32 heads: 0.99 ms against 0.49) and lost with tiles of 32 keys too, where nothing

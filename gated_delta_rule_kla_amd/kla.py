@@ -709,7 +709,8 @@ def glr_chunk_fwd(
 
     x, g: [B, H, T, d], bf16 or fp32; initial_state: [N, H, d] fp32 or None; cu_seqlens: int32
     [N + 1] on the GPU (B must be 1) or None, with its host mirror to avoid a copy back.
-    Returns (o, final_state); ``final_state`` may be passed as the same tensor as
+    The mirror sizes the call, the offsets on the GPU decide: a captured call may be replayed with
+    others.  Returns (o, final_state); ``final_state`` may be passed as the same tensor as
     ``initial_state``.
     """
     dev = _device_of("glr_chunk_fwd", x)
@@ -891,8 +892,9 @@ def kv4_append(
     """Store keys and values in a 4-bit cache (kla_kv4_append), in place.
 
     k, v: [B, Hkv, T, D], bf16 or fp32; codes, scales: as kv4_cache makes them; block_table:
-    int32 [N, max_pages]; start: int32 [N], the tokens that each sequence holds already;
-    cu_seqlens as in chunk_fwd (None: N = B).
+    int32 [N, max_pages]; start: int32 [N], the tokens that each sequence holds already (negative:
+    the sequence is padding); cu_seqlens as in chunk_fwd (None: N = B).  Rows behind the last
+    sequence of the offsets on the GPU are not stored.
     """
     if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.is_cuda and k.dtype in _DTYPES
             and v.dtype is k.dtype and k.dim() == 4 and v.shape == k.shape and v.device == k.device
@@ -921,7 +923,8 @@ def kv4_read(
 ) -> Tuple[torch.Tensor, torch.Tensor]:
     """The values that a 4-bit cache holds (kla_kv4_read): k, v [1, Hkv, T, D] of positions
     start[n] ... start[n] + length of sequence n, packed by cu_seqlens (int32 [N + 1], T its
-    last).  With ``out`` (k, v) nothing is copied from the GPU."""
+    last; its host mirror avoids a copy back).  ``out``: (k, v) to write to, whose rows behind the
+    last sequence of the offsets on the GPU stay as they are."""
     if not isinstance(codes, torch.Tensor) or codes.device.type != "cuda":
         raise ValueError("kla.kv4_read needs GPU tensors")
     if dtype not in _DTYPES:
