@@ -255,6 +255,28 @@ kla_status_t run_glr(kla::GlrArgs &a, bool bwd, void *workspace, size_t workspac
   return from_hip(kla::launch_glr_chunk(a, bwd, reinterpret_cast<hipStream_t>(stream)));
 }
 
+// Linear attention's sizes and decays (one of g and decay); a's are set where they are fine.
+kla_status_t check_la(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B, int H, int T,
+                      int dk, int dv, int dtype, kla::LaArgs *a) {
+  if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
+  if (B < 0 || H <= 0 || T < 0 || T > kMaxTokens || dk <= 0 || dv <= 0 || num_seqs < 0) return KLA_ERR_SHAPE;
+  if (!kla::la_supported(dk, dv)) return KLA_ERR_UNSUPPORTED;
+  if ((long long)B * H > 0x7fffffffLL || (long long)num_seqs * H > 0x7fffffffLL ||
+      (double)B * H * T > (double)(1LL << 40))
+    return KLA_ERR_SHAPE;
+  *a = kla::LaArgs{};
+  const kla_status_t st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, T, &a->longest);
+  if (st != KLA_OK) return st;
+  a->cu_seqlens = cu_seqlens;
+  a->num_seqs = num_seqs;
+  a->H = H;
+  a->T = T;
+  a->dk = dk;
+  a->dv = dv;
+  a->dtype = dtype;
+  return kla::la_grid_fits(*a) ? KLA_OK : KLA_ERR_SHAPE;
+}
+
 // The 4-bit cache's own arguments.
 kla_status_t check_kv4(int Hkv, int D, int num_pages, int page_size, int max_pages, int N, int dtype) {
   if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
@@ -581,6 +603,95 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
   if (!x || !g || !state || !o) return KLA_ERR_NULL;
   if (misaligned(x) || misaligned(g) || misaligned(state) || misaligned(o)) return KLA_ERR_ALIGN;
   return from_hip(kla::launch_glr_step(x, g, state, o, (size_t)N * H * d, dtype, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t kla_la_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B,
+                                    int H, int T, int dk, int dv, kla_dtype_t dtype_) {
+  kla::LaArgs a;
+  if (check_la(cu_seqlens, cu_seqlens_host, num_seqs, B, H, T, dk, dv, raw(dtype_), &a) != KLA_OK) return 0;
+  return num_seqs == 0 ? 0 : kla::la_workspace_bytes(a, false);
+}
+
+size_t kla_la_chunk_bwd_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs,
+                                        int B, int H, int T, int dk, int dv, kla_dtype_t dtype_) {
+  kla::LaArgs a;
+  if (check_la(cu_seqlens, cu_seqlens_host, num_seqs, B, H, T, dk, dv, raw(dtype_), &a) != KLA_OK) return 0;
+  return num_seqs == 0 ? 0 : kla::la_workspace_bytes(a, true);
+}
+
+kla_status_t kla_la_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const float *decay,
+                              const float *initial_state, void *o, float *final_state, const int32_t *cu_seqlens,
+                              const int32_t *cu_seqlens_host, int num_seqs, int B, int H, int T, int dk, int dv,
+                              kla_dtype_t dtype_, void *workspace, size_t workspace_bytes, void *stream) {
+  kla::LaArgs a;
+  const kla_status_t st = check_la(cu_seqlens, cu_seqlens_host, num_seqs, B, H, T, dk, dv, raw(dtype_), &a);
+  if (st != KLA_OK) return st;
+  if (g && decay) return KLA_ERR_PARAM;
+  if (num_seqs == 0) return KLA_OK;
+  if ((long long)B * T > 0 && (!q || !k || !v || !o || (!g && !decay))) return KLA_ERR_NULL;
+  if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(g) || misaligned4(decay) ||
+      misaligned(initial_state) || misaligned(o) || misaligned(final_state) || misaligned(workspace))
+    return KLA_ERR_ALIGN;
+  const size_t need = kla::la_workspace_bytes(a, false);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KLA_ERR_WORKSPACE;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.gfix = decay;
+  a.initial_state = initial_state;
+  a.o = o;
+  a.final_state = final_state;
+  a.workspace = workspace;
+  return from_hip(kla::launch_la_fwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+kla_status_t kla_la_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const float *decay,
+                              const float *initial_state, const void *dout, const float *dfinal_state, void *dq,
+                              void *dk_, void *dv_, void *dg, float *dinitial_state, const int32_t *cu_seqlens,
+                              const int32_t *cu_seqlens_host, int num_seqs, int B, int H, int T, int dk, int dv,
+                              kla_dtype_t dtype_, void *workspace, size_t workspace_bytes, void *stream) {
+  kla::LaArgs a;
+  const kla_status_t st = check_la(cu_seqlens, cu_seqlens_host, num_seqs, B, H, T, dk, dv, raw(dtype_), &a);
+  if (st != KLA_OK) return st;
+  if (g && decay) return KLA_ERR_PARAM;
+  if (num_seqs == 0 && !decay) return KLA_OK;
+  if ((long long)B * T > 0 && (!q || !k || !v || (!g && !decay) || !dout || !dq || !dk_ || !dv_ || !dg))
+    return KLA_ERR_NULL;
+  if (decay && !dg) return KLA_ERR_NULL;
+  if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(g) || misaligned4(decay) ||
+      misaligned(initial_state) || misaligned(dout) || misaligned(dfinal_state) || misaligned(dq) ||
+      misaligned(dk_) || misaligned(dv_) || misaligned(dg) || misaligned(dinitial_state) || misaligned(workspace))
+    return KLA_ERR_ALIGN;
+  const size_t need = num_seqs == 0 ? 0 : kla::la_workspace_bytes(a, true);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KLA_ERR_WORKSPACE;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.gfix = decay;
+  a.initial_state = initial_state;
+  a.workspace = workspace;
+  const kla::LaGrads b{dout, dfinal_state, dq, dk_, dv_, dg, dinitial_state};
+  return from_hip(kla::launch_la_bwd(a, b, reinterpret_cast<hipStream_t>(stream)));
+}
+
+kla_status_t kla_la_decode_step(const void *q, const void *k, const void *v, const void *g, const float *decay,
+                                float *state, void *o, int N, int H, int dk, int dv, kla_dtype_t dtype_,
+                                void *stream) {
+  const int dtype = raw(dtype_);
+  if (dtype != KLA_DT_BF16 && dtype != KLA_DT_F32) return KLA_ERR_DTYPE;
+  if (N < 0 || H <= 0 || dk <= 0 || dv <= 0) return KLA_ERR_SHAPE;
+  if (!kla::la_supported(dk, dv)) return KLA_ERR_UNSUPPORTED;
+  if (!kla::la_step_fits((long long)N * H, dv)) return KLA_ERR_SHAPE;
+  if (g && decay) return KLA_ERR_PARAM;
+  if (N == 0) return KLA_OK;
+  if (!q || !k || !v || (!g && !decay) || !state || !o) return KLA_ERR_NULL;
+  if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(g) || misaligned4(decay) || misaligned(state) ||
+      misaligned(o))
+    return KLA_ERR_ALIGN;
+  return from_hip(kla::launch_la_step(q, k, v, g, decay, state, o, N, H, dk, dv, dtype,
+                                      reinterpret_cast<hipStream_t>(stream)));
 }
 
 kla_status_t kla_kv4_append(const void *k, const void *v, void *codes, void *scales, const int32_t *block_table,

@@ -153,6 +153,32 @@ bool glr_step_fits(size_t n, int dtype);  // n channels; launch_fits
 hipError_t launch_glr_step(const void *x, const void *g, float *state, void *o, size_t n, int dtype,
                            hipStream_t stream);
 
+// Linear attention with a decay per head (kla_la.hip).  gfix: log-decays per head in place of g.
+struct LaArgs {
+  const void *q, *k, *v, *g;
+  const float *gfix, *initial_state;
+  void *o;
+  float *final_state;
+  const int32_t *cu_seqlens;  // device, or nullptr
+  int num_seqs, H, T, dk, dv, dtype;
+  int longest;                // tokens of the longest sequence
+  void *workspace;            // device, la_workspace_bytes(*this, ...) bytes
+};
+struct LaGrads {
+  const void *dout;
+  const float *dfinal_state;  // or nullptr (zero)
+  void *dq, *dk, *dv, *dg;    // dg: as g, or fp32 [H] for gfix
+  float *dinitial_state;      // or nullptr
+};
+bool la_supported(int dk, int dv);
+bool la_grid_fits(const LaArgs &a);
+size_t la_workspace_bytes(const LaArgs &a, bool bwd);
+hipError_t launch_la_fwd(const LaArgs &a, hipStream_t stream);
+hipError_t launch_la_bwd(const LaArgs &a, const LaGrads &b, hipStream_t stream);
+bool la_step_fits(long long nh, int dv);
+hipError_t launch_la_step(const void *q, const void *k, const void *v, const void *g, const float *gfix, float *state,
+                          void *o, int N, int H, int dk, int dv, int dtype, hipStream_t stream);
+
 // The 4-bit key/value cache (kla_kv4.hip): codes [num_pages, 2, Hkv, page, D/2], scales
 // [num_pages, 2, Hkv, page, D/32], block table [N, max_pages].
 struct Kv4Cache {

@@ -1,0 +1,1009 @@
+// kla_la.hip -- linear attention with a decay per head (gfx950): prompts, gradients, single tokens.
+//
+//   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t      (include/kla.h, kla_la_chunk_fwd)
+//
+// In chunks of C tokens, with c_t the sum of the chunk's log-decays up to token t, S the state at
+// the chunk's start and tot = c_{C-1}:
+//
+//   o_t = exp(c_t) S^T q_t + sum_{s <= t} exp(c_t - c_s) (q_t . k_s) v_s
+//   S'  = exp(tot) S + sum_s exp(tot - c_s) k_s v_s^T
+//
+// Log-decays are summed in 64 bits and kept as two floats in base two, so that c_t - c_s is as
+// exact behind a token that forgets everything (g = -inf counts as 2^-65536) as elsewhere.
+// Operands of the products are in the element type: the scores and the state (where outputs are
+// read from it) are rounded to it once, as the outputs are; the state itself is fp32, and the
+// scaled v_s that enter it are two bf16 terms (16 bits), since a final state is fp32 as well.
+//
+// Backward, with M the gradient of the state at a chunk's end (dL/dS_final at the last):
+//
+//   dq_t = exp(c_t) S do_t + sum_{s <= t} D_ts (do_t . v_s) k_s        D_ts = exp(c_t - c_s)
+//   dk_s = exp(tot - c_s) M v_s + sum_{t >= s} D_ts (do_t . v_s) q_t
+//   dv_s = exp(tot - c_s) M^T k_s + sum_{t >= s} D_ts (q_t . k_s) do_t
+//   M'   = exp(tot) M + sum_t exp(c_t) q_t do_t^T                      (at the chunk's start)
+//   dg_t = what passes token t: from the writes before it to the reads from it on,
+//          sum_{i >= t > j} D_ij (q_i . k_j)(do_i . v_j) + sum_{i >= t} (the state's part of q_i . dq_i)
+//          + sum_{j < t} (the later chunks' part of k_j . dk_j) + exp(tot) <M, S>
+//
+// (in dg every term is a sum of products that belong to it; the shorter form, q . dq - k . dk
+// summed from t to the sequence's end, loses what the terms have in common, and with operands of
+// eight bits little is left of it).
+#include <algorithm>
+
+#include "kla_common.h"
+#include "kla_internal.h"
+#include "kla_ops.h"
+
+namespace kla {
+
+namespace {
+
+constexpr int LA_NV = 32;         // state columns of a scan workgroup
+constexpr float LA_FORGET = -65536.f;  // log2 of the smallest decay
+
+// Chunks and operands by element type.  A 16-byte operand holds VL contraction values of a row
+// (or column), four of them (KG values) make a product.
+template <typename E> struct La;
+template <> struct La<bf16> {
+  static constexpr int C = 64, KG = 32, VL = 8, TERMS = 2;
+  typedef bf16x8 Op;
+  static __device__ __forceinline__ Op nat(const bf16 *row, int kb, int g) {
+    return *reinterpret_cast<const bf16x8 *>(row + kb + 8 * g);
+  }
+  static __device__ __forceinline__ Op grp(const bf16 *row, int kb, int g) { return Ops<bf16>::ldg_grp(row, kb, g); }
+  // column c16 + (lane & 15) of rows kb .. kb + 31, in the order of accumulator tiles
+  static __device__ __forceinline__ Op tr(const bf16 *M, int ld, int kb, int c16, int lane) {
+    const int g = lane >> 4, x = (lane >> 2) & 3, a = lane & 3;
+    const bf16 *p = M + (kb + 4 * g + x) * ld + c16 + 4 * a;
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)p);
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)(p + 16 * ld));
+    return Op{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  }
+  static __device__ __forceinline__ Op cvt(uint4 v) { return __builtin_bit_cast(Op, v); }
+};
+template <> struct La<float> {
+  static constexpr int C = 32, KG = 16, VL = 4, TERMS = 1;
+  typedef f32x4 Op;
+  static __device__ __forceinline__ Op nat(const float *row, int kb, int g) {
+    return *reinterpret_cast<const f32x4 *>(row + kb + 4 * g);
+  }
+  static __device__ __forceinline__ Op grp(const float *row, int kb, int g) { return nat(row, kb, g); }
+  static __device__ __forceinline__ Op tr(const float *M, int ld, int kb, int c16, int lane) {
+    const float *p = M + (kb + 4 * (lane >> 4)) * ld + c16 + (lane & 15);
+    return Op{p[0], p[ld], p[2 * ld], p[3 * ld]};
+  }
+  static __device__ __forceinline__ Op cvt(uint4 v) { return __builtin_bit_cast(Op, v); }
+};
+
+// four consecutive elements of a row as fp32
+__device__ __forceinline__ f32x4 load4(const bf16 *p) {
+  const bf16x4 v = *reinterpret_cast<const bf16x4 *>(p);
+  return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+__device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+
+// Inclusive prefix sum of doubles over the lanes of a wave (row shifts, then the rows' totals).
+template <int CTRL>
+__device__ __forceinline__ double dpp_shr(double v) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+  const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, 0xF, 0xF, false);
+  const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_double(double v, int src) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+  const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)u, src);
+  const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(u >> 32), src);
+  return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+__device__ __forceinline__ double scan_double(double v) {
+  v += dpp_shr<0x111>(v);
+  v += dpp_shr<0x112>(v);
+  v += dpp_shr<0x114>(v);
+  v += dpp_shr<0x118>(v);
+  const double r0 = lane_double(v, 15), r1 = lane_double(v, 31), r2 = lane_double(v, 47);
+  const int row = (threadIdx.x & 63) >> 4;
+  return v + ((row >= 1 ? r0 : 0.0) + (row >= 2 ? r1 : 0.0) + (row >= 3 ? r2 : 0.0));
+}
+
+// A chunk's decays: c_t in base two as hi + lo, exp(c_t), exp(tot - c_t), exp(tot), tot.
+template <int C>
+struct Decays {
+  float hi[C], lo[C], out[C], left[C];
+  float all;
+  double tot;
+};
+
+// by one wave; g: the lane's log-decay (0 past the chunk's tokens)
+template <int C>
+__device__ __forceinline__ void scan_decays(Decays<C> *d, float g) {
+  const int lane = threadIdx.x & 63;
+  double x = (double)g * 1.4426950408889634;
+  x = x < LA_FORGET ? LA_FORGET : x;  // a NaN stays
+  if (lane >= C) x = 0.0;
+  const double c = scan_double(x), tot = lane_double(c, 63);
+  if (lane < C) {
+    const float hi = (float)c;
+    d->hi[lane] = hi;
+    d->lo[lane] = (float)(c - (double)hi);
+    d->out[lane] = __builtin_amdgcn_exp2f((float)c);
+    d->left[lane] = __builtin_amdgcn_exp2f((float)(tot - c));
+  }
+  if (lane == 0) {
+    d->all = __builtin_amdgcn_exp2f((float)tot);
+    d->tot = tot;
+  }
+}
+
+struct LaParams {
+  const void *q, *x, *y, *g;  // x, y: the factors of the state's updates (k, v; reverse: q, dout)
+  const float *gfix;          // [H] log-decays in place of g, or nullptr
+  const float *s0;            // state at the first processed chunk, or nullptr
+  void *o, *states;
+  float *send;                // state behind the last, or nullptr
+  const int32_t *cu;          // device offsets, or nullptr
+  int N, H, T, dk, dv;
+  int slices, segs, seg_chunks;
+  float *seg_s;               // [N H segs, dk, dv] states behind all segments but the last; in the last's
+                              // place the initial state (final_state may be the same memory)
+  double *seg_g;              // [N H segs] log2 of their decays
+  int slots;                  // chunk slots of a head (states)
+};
+
+// Sequence n: its first row among a head's, its length, and its first chunk's slot.
+__device__ __forceinline__ void la_span(const int32_t *cu, int n, int T, int C, int *t0, int *len, int *slot0) {
+  if (!cu) {
+    *t0 = 0, *len = T, *slot0 = n * ((T + C - 1) / C);
+    return;
+  }
+  const int a = min(max(cu[n], 0), T), z = min(max(cu[n + 1], a), T);
+  *t0 = a, *len = z - a, *slot0 = a / C + n;
+}
+
+// The scan over a sequence's chunks.  A workgroup (four waves) holds LA_NV columns of the state,
+// each wave a quarter of its rows, in fp32, and a copy in the element type in LDS, from which all
+// waves read.  Of the outputs a wave computes 16 rows (bf16: of all columns; fp32, 32 tokens to a
+// chunk: of half of them).  x, y and q arrive in registers a chunk ahead, and go to LDS a chunk
+// ahead of their use, with y's scaled copy for the state; one barrier per chunk.
+//
+// OUT: outputs and the final state.  ENDS: a segment's end state only, where few sequences leave
+// CUs idle and are cut: all segments but the last are scanned once for that, and OUT starts each
+// from those before it.  STORE: the state at each chunk's start (REV: the state's gradient
+// at its end), for the gradients.
+enum { LA_OUT, LA_ENDS, LA_STORE };
+
+template <typename E, int DK, int MODE, bool REV>
+__global__ __launch_bounds__(256) void kla_la_scan_kernel(LaParams p) {
+  using L = La<E>;
+  using Op = typename L::Op;
+  constexpr int C = L::C, KG = L::KG, VL = L::VL, NV = LA_NV;
+  constexpr int PAD = LdsPad<E>::V, LDX = DK + PAD, LDY = NV + PAD;
+  constexpr int XP = C * DK / VL / 256, YP = C * NV / VL / 256;  // 16-byte pieces of a thread
+  constexpr int RT = DK / 64;                                  // row tiles of a wave
+  constexpr int NC = NV / 16, NS = C / 16, CT = NC * NS / 4;   // column tiles, strips, a wave's output tiles
+  constexpr int KS = DK / KG;
+  static_assert(XP * 256 * VL == C * DK && YP * 256 * VL == C * NV && CT * 4 == NC * NS, "tiles");
+  __shared__ __attribute__((aligned(16))) E s_x[2][C * LDX];
+  __shared__ __attribute__((aligned(16))) E s_y[MODE == LA_OUT ? 2 : 1][C * LDY];
+  __shared__ __attribute__((aligned(16))) E s_w[2][L::TERMS][C * LDY];  // y scaled
+  __shared__ __attribute__((aligned(16))) E s_s[MODE == LA_ENDS ? 1 : 2][MODE == LA_ENDS ? 16 : NV * LDX];  // S^T
+  __shared__ Decays<C> s_d[3];
+
+  // workgroup ids go round the eight XCDs: the slices of a sequence and head, which read the
+  // same rows, stay on one
+  const unsigned rest = blockIdx.x >> 3;
+  const int slice = rest % p.slices;
+  const long long pair = (long long)(rest / p.slices) * 8 + (blockIdx.x & 7);
+  if (pair >= (long long)p.N * p.H * p.segs) return;
+  const int seg = pair % p.segs;
+  const long long nh = pair / p.segs;
+  const int n = nh / p.H, h = nh % p.H;
+  int t0, len, slot0;
+  la_span(p.cu, n, p.T, C, &t0, &len, &slot0);
+  const int nch = (len + C - 1) / C;
+  // the chunks in processed order
+  const int c0 = seg * p.seg_chunks, c1 = seg == p.segs - 1 ? nch : min(nch, c0 + p.seg_chunks);
+  if (seg > 0 && c0 >= nch) return;
+  if (MODE == LA_ENDS && c1 >= nch) return;
+  const size_t row0 = ((size_t)(p.cu ? 0 : n) * p.H + h) * p.T + t0;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, li = lane & 15;
+  const int col0 = slice * NV;
+  const int strip = wave % NS, ct0 = wave / NS * CT;
+
+  auto first_token = [&](int j) { return (REV ? nch - 1 - j : j) * C; };
+  uint4 xr[XP], yr[YP];
+  auto load = [&](int j) {
+    const int t = first_token(j), rows = min(C, len - t);
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc((const E *)p.x + (row0 + t) * p.dk, rows * p.dk * (int)sizeof(E));
+    const __amdgpu_buffer_rsrc_t ry = buffer_rsrc((const E *)p.y + (row0 + t) * p.dv, rows * p.dv * (int)sizeof(E));
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      const int pc = tid + 256 * i, r = pc / (DK / VL), c = pc % (DK / VL) * VL;
+      xr[i] = buffer_ld16(rx, c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000);
+    }
+#pragma unroll
+    for (int i = 0; i < YP; ++i) {
+      const int pc = tid + 256 * i, r = pc / (NV / VL), c = col0 + pc % (NV / VL) * VL;
+      yr[i] = buffer_ld16(ry, c < p.dv ? (r * p.dv + c) * (int)sizeof(E) : 0x40000000);
+    }
+  };
+  auto put = [&](int j) {  // chunk j's rows from registers
+    E *const dx = s_x[j & 1];
+    const Decays<C> &d = s_d[j % 3];
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      const int pc = tid + 256 * i;
+      *reinterpret_cast<uint4 *>(dx + pc / (DK / VL) * LDX + pc % (DK / VL) * VL) = xr[i];
+    }
+#pragma unroll
+    for (int i = 0; i < YP; ++i) {
+      const int pc = tid + 256 * i, r = pc / (NV / VL), at = r * LDY + pc % (NV / VL) * VL;
+      const float f = REV ? d.out[r] : d.left[r];
+      E e[VL], w[L::TERMS][VL];
+      __builtin_memcpy(e, &yr[i], 16);
+#pragma unroll
+      for (int u = 0; u < VL; ++u) {
+        float v = Elem<E>::to_f32(e[u]) * f;
+#pragma unroll
+        for (int k = 0; k < L::TERMS; ++k) {
+          w[k][u] = Elem<E>::from_f32(v);
+          v -= Elem<E>::to_f32(w[k][u]);
+        }
+      }
+      if constexpr (MODE == LA_OUT) *reinterpret_cast<uint4 *>(s_y[j & 1] + at) = yr[i];
+#pragma unroll
+      for (int k = 0; k < L::TERMS; ++k) {
+        uint4 v;
+        __builtin_memcpy(&v, w[k], 16);
+        *reinterpret_cast<uint4 *>(s_w[j & 1][k] + at) = v;
+      }
+    }
+  };
+  auto load_g = [&](int j) {  // the lane's log-decay
+    const int t = first_token(j) + lane;
+    if (lane >= C || t >= len) return 0.f;
+    return p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + t]);
+  };
+  Op q[MODE == LA_OUT ? KS : 1];
+  auto load_q = [&](int j) {
+    if constexpr (MODE == LA_OUT) {
+      const int t = first_token(j), rows = min(C, len - t);
+      const __amdgpu_buffer_rsrc_t rq = buffer_rsrc((const E *)p.q + (row0 + t) * p.dk, rows * p.dk * (int)sizeof(E));
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int c = k * KG + VL * g;
+        q[k] = L::cvt(buffer_ld16(rq, c < p.dk ? ((16 * strip + li) * p.dk + c) * (int)sizeof(E) : 0x40000000));
+      }
+    }
+  };
+
+  // this wave's rows of the state: tile i, element e is row 16 (wave RT + i) + 4 g + e
+  f32x4 acc[RT][NC];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[i][c] = zero4();
+  auto each = [&](auto f) {  // element = f(element, offset in a [dk, dv] state)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * (wave * RT + i) + 4 * g + e, col = col0 + 16 * c + li;
+          if (r < p.dk && col < p.dv) acc[i][c][e] = f(acc[i][c][e], (size_t)r * p.dv + col);
+        }
+  };
+  const size_t ssize = (size_t)p.dk * p.dv;
+  if (c0 < c1) {
+    load(c0);
+    load_q(c0);
+    if (wave == 0) scan_decays<C>(&s_d[c0 % 3], load_g(c0));
+    if (wave == 1 && c0 + 1 < c1) scan_decays<C>(&s_d[(c0 + 1) % 3], load_g(c0 + 1));
+  }
+  if (seg == 0) {
+    const bool copied = MODE == LA_OUT && p.segs > 1 && c1 < nch;
+    const float *s0 = p.s0 ? (copied ? p.seg_s + (nh * p.segs + p.segs - 1) * ssize : p.s0 + nh * ssize) : nullptr;
+    if (s0) each([&](float, size_t at) { return s0[at]; });
+    if (MODE == LA_ENDS && s0) {
+      float *const copy = p.seg_s + (nh * p.segs + p.segs - 1) * ssize;
+      each([&](float a, size_t at) { return copy[at] = a; });
+    }
+  } else if (MODE != LA_ENDS) {
+    for (int i = 0; i < seg; ++i) {  // the segments before this one, in order
+      const float f = __builtin_amdgcn_exp2f((float)p.seg_g[nh * p.segs + i]);
+      const float *const d = p.seg_s + (nh * p.segs + i) * ssize;
+      each([&](float a, size_t at) { return (i ? f * a : 0.f) + d[at]; });
+    }
+  }
+  auto publish = [&](int j) {  // the state in front of chunk j
+    if constexpr (MODE != LA_ENDS) {
+      E *const d = s_s[j & 1];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) store4(d + (16 * c + li) * LDX + 16 * (wave * RT + i) + 4 * g, acc[i][c]);
+    }
+  };
+  double total = 0.0;
+  float gn = 0.f;
+  if (c0 < c1) {
+    lds_barrier();
+    put(c0);
+    publish(c0);
+    if (c0 + 1 < c1) load(c0 + 1);
+    if (c0 + 2 < c1) gn = load_g(c0 + 2);
+  }
+
+  for (int j = c0; j < c1; ++j) {
+    lds_barrier();
+    if (j + 1 < c1) put(j + 1);
+    if (j + 2 < c1) {
+      load(j + 2);
+      if (wave == (j & 3)) scan_decays<C>(&s_d[(j + 2) % 3], gn);
+    }
+    if (j + 3 < c1) gn = load_g(j + 3);
+    const E *const X = s_x[j & 1];
+    const Decays<C> &d = s_d[j % 3];
+    if (MODE == LA_ENDS) total += d.tot;
+
+    if constexpr (MODE == LA_STORE) {
+      // S^T as it stands in LDS, rows of dk elements
+      E *const to = (E *)p.states + ((size_t)h * p.slots + slot0 + first_token(j) / C) * ssize + (size_t)col0 * p.dk;
+      const int per = p.dk / VL, pieces = min(NV, p.dv - col0) * per;
+      for (int i = tid; i < pieces; i += 256) {
+        const int r = i / per, c = i % per * VL;
+        stg16(to + (size_t)r * p.dk + c, *reinterpret_cast<const uint4 *>(s_s[j & 1] + r * LDX + c));
+      }
+    }
+    if constexpr (MODE == LA_OUT) {
+      const E *const Y = s_y[j & 1], *const S = s_s[j & 1];
+      // P^T: keys 16 kt + 4 g + e against the strip's query li
+      f32x4 pt[NS];
+      const float th = d.hi[16 * strip + li], tl = d.lo[16 * strip + li];
+#pragma unroll
+      for (int kt = 0; kt < NS; ++kt) {
+        pt[kt] = zero4();
+        if (kt <= strip) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            pt[kt] = Ops<E>::mma_grp(L::nat(X + (16 * kt + li) * LDX, k * KG, g), q[k], pt[kt]);
+          const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * kt + 4 * g]);
+          const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * kt + 4 * g]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            pt[kt][e] = kt < strip || 4 * g + e <= li
+                            ? pt[kt][e] * __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) : 0.f;
+        }
+      }
+      f32x4 o[CT];  // o^T: columns 4 g + e of query li
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        o[c] = zero4();
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          o[c] = Ops<E>::mma_grp(L::nat(S + (16 * (ct0 + c) + li) * LDX, k * KG, g), q[k], o[c]);
+        const float f = d.out[16 * strip + li];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][e] *= f;
+      }
+      if (j + 1 < c1) load_q(j + 1);
+#pragma unroll
+      for (int kb = 0; kb < C; kb += KG)
+        if (kb / 16 <= strip) {
+          const Op w = Ops<E>::b_from_d(&pt[kb / 16]);
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+            o[c] = Ops<E>::mma_grp(L::tr(Y, LDY, kb, 16 * (ct0 + c), lane), w, o[c]);
+        }
+      const int t = first_token(j) + 16 * strip + li;
+      if (t < len) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const int col = col0 + 16 * (ct0 + c) + 4 * g;
+          if (col < p.dv) store4((E *)p.o + (row0 + t) * p.dv + col, o[c]);
+        }
+      }
+    }
+    const float f = d.all;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][c][e] *= f;
+#pragma unroll
+    for (int kb = 0; kb < C; kb += KG) {
+      Op w[L::TERMS][NC];
+#pragma unroll
+      for (int k = 0; k < L::TERMS; ++k)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) w[k][c] = L::tr(s_w[j & 1][k], LDY, kb, 16 * c, lane);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const Op a = L::tr(X, LDX, kb, 16 * (wave * RT + i), lane);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int k = 0; k < L::TERMS; ++k) acc[i][c] = Ops<E>::mma_grp(a, w[k][c], acc[i][c]);
+      }
+    }
+    if (j + 1 < c1) publish(j + 1);
+  }
+  if constexpr (MODE == LA_ENDS) {
+    float *const to = p.seg_s + (nh * p.segs + seg) * ssize;
+    each([&](float a, size_t at) { return to[at] = a; });
+    if (tid == 0 && slice == 0) p.seg_g[nh * p.segs + seg] = total;
+  } else if (p.send && c1 >= nch) {
+    float *const to = p.send + nh * ssize;
+    each([&](float a, size_t at) { return to[at] = a; });
+  }
+}
+
+// The gradients of one chunk and head from its rows, the state at its start and the state's
+// gradient at its end.  Wave w owns 16 tokens, as queries (dq) and as keys (dk, dv); the
+// products' accumulators hold gradients transposed (channels in a lane, tokens along lanes), and
+// the scores that the second products take are accumulator tiles as they stand: (do . v)
+// transposed for dq, (do . v) and (q . k) for dk and dv.  The values' channels come in slices of
+// LA_NV.
+struct LaGradParams {
+  const void *q, *k, *v, *g, *dout, *states, *dstates;
+  const float *gfix;
+  void *dq, *dk_, *dv_, *dg;
+  float *dg_chunk;  // [H, slots] sums over a chunk's tokens, where decays are fixed
+  const int32_t *cu;
+  int N, B, H, T, dk, dv, slots;
+};
+
+template <typename E, int DK>
+__global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams p) {
+  using L = La<E>;
+  using Op = typename L::Op;
+  constexpr int C = L::C, KG = L::KG, VL = L::VL, NV = LA_NV, NS = C / 16, NT = 64 * NS;
+  constexpr int PAD = LdsPad<E>::V, LDX = DK + PAD, LDY = NV + PAD;
+  constexpr int KS = DK / KG, RB = DK / 16, NC = NV / 16;
+  __shared__ __attribute__((aligned(16))) E s_q[C * LDX], s_k[C * LDX], s_v[C * LDY], s_o[C * LDY], s_s[NV * LDX], s_m[NV * LDX];
+  __shared__ Decays<C> s_d;
+  __shared__ float s_row[NS][C], s_read[C], s_write[C], s_dot[NS];
+
+  const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, li = lane & 15;
+  int n = 0;
+  if (p.cu) {
+    int lo = 0, hi = p.N;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (min(max(p.cu[mid], 0), p.T) / C + mid <= slot) lo = mid; else hi = mid;
+    }
+    n = lo;
+  } else {
+    n = slot / ((p.T + C - 1) / C);
+  }
+  int t0, len, slot0;
+  la_span(p.cu, n, p.T, C, &t0, &len, &slot0);
+  const int first = (slot - slot0) * C, rows = min(C, len - first);
+  if (first < 0 || rows <= 0) {
+    if (p.dg_chunk && tid == 0) p.dg_chunk[(size_t)h * p.slots + slot] = 0.f;
+    return;
+  }
+  const size_t row0 = ((size_t)(p.cu ? 0 : n) * p.H + h) * p.T + t0 + first;
+
+  {
+    const __amdgpu_buffer_rsrc_t rq = buffer_rsrc((const E *)p.q + row0 * p.dk, rows * p.dk * (int)sizeof(E));
+    const __amdgpu_buffer_rsrc_t rk = buffer_rsrc((const E *)p.k + row0 * p.dk, rows * p.dk * (int)sizeof(E));
+    constexpr int NP = C * DK / VL / NT;
+    uint4 a[NP], b[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int pc = tid + NT * i, r = pc / (DK / VL), c = pc % (DK / VL) * VL;
+      const int at = c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000;
+      a[i] = buffer_ld16(rq, at);
+      b[i] = buffer_ld16(rk, at);
+    }
+    if (wave == 0) {
+      float gl = 0.f;
+      if (lane < rows) gl = p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + lane]);
+      scan_decays<C>(&s_d, gl);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int pc = tid + NT * i, at = pc / (DK / VL) * LDX + pc % (DK / VL) * VL;
+      *reinterpret_cast<uint4 *>(s_q + at) = a[i];
+      *reinterpret_cast<uint4 *>(s_k + at) = b[i];
+    }
+  }
+
+  f32x4 dq[RB], dk[RB];  // transposed: channels 16 i + 4 g + e of token 16 wave + li
+#pragma unroll
+  for (int i = 0; i < RB; ++i) dq[i] = dk[i] = zero4();
+  f32x4 w[NS], wt[NS];  // do . v: tokens 16 i + 4 g + e against key li; keys 16 i + 4 g + e against query li
+  f32x4 sc[NS];         // q . k as w
+#pragma unroll
+  for (int i = 0; i < NS; ++i) w[i] = wt[i] = sc[i] = zero4();
+  Op pv[C / KG];        // the decayed scores for dv
+  float dot = 0.f;
+  const int me = 16 * wave + li;
+
+  for (int c0 = 0; c0 < p.dv; c0 += NV) {
+    const int cols = min(NV, p.dv - c0);
+    {
+      const __amdgpu_buffer_rsrc_t rv = buffer_rsrc((const E *)p.v + row0 * p.dv, rows * p.dv * (int)sizeof(E));
+      const __amdgpu_buffer_rsrc_t ro = buffer_rsrc((const E *)p.dout + row0 * p.dv, rows * p.dv * (int)sizeof(E));
+      const size_t at0 = ((size_t)h * p.slots + slot) * p.dk * p.dv + (size_t)c0 * p.dk;
+      const __amdgpu_buffer_rsrc_t rs = buffer_rsrc((const E *)p.states + at0, cols * p.dk * (int)sizeof(E));
+      const __amdgpu_buffer_rsrc_t rm = buffer_rsrc((const E *)p.dstates + at0, cols * p.dk * (int)sizeof(E));
+      constexpr int YP = C * NV / VL / NT, XP = NV * DK / VL / NT;
+      uint4 v[YP], o[YP], s[XP], m[XP];
+#pragma unroll
+      for (int i = 0; i < YP; ++i) {
+        const int pc = tid + NT * i, r = pc / (NV / VL), c = c0 + pc % (NV / VL) * VL;
+        const int at = c < p.dv ? (r * p.dv + c) * (int)sizeof(E) : 0x40000000;
+        v[i] = buffer_ld16(rv, at);
+        o[i] = buffer_ld16(ro, at);
+      }
+#pragma unroll
+      for (int i = 0; i < XP; ++i) {
+        const int pc = tid + NT * i, r = pc / (DK / VL), c = pc % (DK / VL) * VL;
+        const int at = c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000;
+        s[i] = buffer_ld16(rs, at);
+        m[i] = buffer_ld16(rm, at);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < YP; ++i) {
+        const int pc = tid + NT * i, at = pc / (NV / VL) * LDY + pc % (NV / VL) * VL;
+        *reinterpret_cast<uint4 *>(s_v + at) = v[i];
+        *reinterpret_cast<uint4 *>(s_o + at) = o[i];
+      }
+#pragma unroll
+      for (int i = 0; i < XP; ++i) {
+        const int pc = tid + NT * i, at = pc / (DK / VL) * LDX + pc % (DK / VL) * VL;
+        *reinterpret_cast<uint4 *>(s_s + at) = s[i];
+        *reinterpret_cast<uint4 *>(s_m + at) = m[i];
+        E a[VL], b[VL];
+        __builtin_memcpy(a, &s[i], 16);
+        __builtin_memcpy(b, &m[i], 16);
+#pragma unroll
+        for (int e = 0; e < VL; ++e) dot = fmaf(Elem<E>::to_f32(a[e]), Elem<E>::to_f32(b[e]), dot);
+      }
+      __syncthreads();
+    }
+    if (c0 == 0) {  // the scores of the wave's keys, once
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i >= wave) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            sc[i] = Ops<E>::mma_grp(L::nat(s_q + (16 * i + li) * LDX, k * KG, g), L::nat(s_k + me * LDX, k * KG, g), sc[i]);
+          const f32x4 th = *reinterpret_cast<const f32x4 *>(&s_d.hi[16 * i + 4 * g]);
+          const f32x4 tl = *reinterpret_cast<const f32x4 *>(&s_d.lo[16 * i + 4 * g]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[i][e] = i > wave || 4 * g + e >= li
+                           ? sc[i][e] * __builtin_amdgcn_exp2f((th[e] - s_d.hi[me]) + (tl[e] - s_d.lo[me])) : 0.f;
+        }
+#pragma unroll
+      for (int kb = 0; kb < C; kb += KG) pv[kb / KG] = Ops<E>::b_from_d(&sc[kb / 16]);
+    }
+    // do . v, both ways round
+#pragma unroll
+    for (int kb = 0; kb < NV; kb += KG) {
+      const Op v = L::nat(s_v + me * LDY, kb, g), o = L::nat(s_o + me * LDY, kb, g);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if (i >= wave) w[i] = Ops<E>::mma_grp(L::nat(s_o + (16 * i + li) * LDY, kb, g), v, w[i]);
+        if (i <= wave) wt[i] = Ops<E>::mma_grp(L::nat(s_v + (16 * i + li) * LDY, kb, g), o, wt[i]);
+      }
+    }
+    // the states' parts of dq and dk
+#pragma unroll
+    for (int kb = 0; kb < NV; kb += KG) {
+      const Op v = L::grp(s_v + me * LDY, kb, g), o = L::grp(s_o + me * LDY, kb, g);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        dq[i] = Ops<E>::mma_grp(L::tr(s_s, LDX, kb, 16 * i, lane), o, dq[i]);
+        dk[i] = Ops<E>::mma_grp(L::tr(s_m, LDX, kb, 16 * i, lane), v, dk[i]);
+      }
+    }
+    // dv, whole for these channels
+    f32x4 dv[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      dv[c] = zero4();
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        dv[c] = Ops<E>::mma_grp(L::nat(s_m + (16 * c + li) * LDX, k * KG, g), L::nat(s_k + me * LDX, k * KG, g), dv[c]);
+      const float f = s_d.left[me];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dv[c][e] *= f;
+#pragma unroll
+      for (int kb = 0; kb < C; kb += KG)
+        if (kb + KG > 16 * wave) dv[c] = Ops<E>::mma_grp(L::tr(s_o, LDY, kb, 16 * c, lane), pv[kb / KG], dv[c]);
+      const int col = c0 + 16 * c + 4 * g;
+      if (me < rows && col < p.dv) store4((E *)p.dv_ + (row0 + me) * p.dv + col, dv[c]);
+    }
+  }
+
+  // what the states' parts give to the decays' gradient, then the chunk's own parts
+  const float fo = s_d.out[me], fl = s_d.left[me];
+  float read = 0.f, write = 0.f;
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const f32x4 a = load4(s_q + me * LDX + 16 * i + 4 * g), b = load4(s_k + me * LDX + 16 * i + 4 * g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      dq[i][e] *= fo;
+      dk[i][e] *= fl;
+      read = fmaf(a[e], dq[i][e], read);
+      write = fmaf(b[e], dk[i][e], write);
+    }
+  }
+  read += __shfl_xor(read, 16);
+  read += __shfl_xor(read, 32);
+  write += __shfl_xor(write, 16);
+  write += __shfl_xor(write, 32);
+  float col = 0.f;  // the products of the wave's keys with later queries
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    f32x4 r = zero4();
+    if (i >= wave) {
+      const f32x4 th = *reinterpret_cast<const f32x4 *>(&s_d.hi[16 * i + 4 * g]);
+      const f32x4 tl = *reinterpret_cast<const f32x4 *>(&s_d.lo[16 * i + 4 * g]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool seen = i > wave || 4 * g + e >= li;
+        r[e] = i > wave || 4 * g + e > li ? sc[i][e] * w[i][e] : 0.f;  // sc has its decay
+        col += r[e];
+        w[i][e] = seen ? w[i][e] * __builtin_amdgcn_exp2f((th[e] - s_d.hi[me]) + (tl[e] - s_d.lo[me])) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r[e] += __shfl_xor(r[e], 1);
+      r[e] += __shfl_xor(r[e], 2);
+      r[e] += __shfl_xor(r[e], 4);
+      r[e] += __shfl_xor(r[e], 8);
+    }
+    if (li == 0) *reinterpret_cast<f32x4 *>(&s_row[wave][16 * i + 4 * g]) = r;
+    if (i <= wave) {
+      const f32x4 sh = *reinterpret_cast<const f32x4 *>(&s_d.hi[16 * i + 4 * g]);
+      const f32x4 sl = *reinterpret_cast<const f32x4 *>(&s_d.lo[16 * i + 4 * g]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        wt[i][e] = i < wave || 4 * g + e <= li
+                       ? wt[i][e] * __builtin_amdgcn_exp2f((s_d.hi[me] - sh[e]) + (s_d.lo[me] - sl[e])) : 0.f;
+    }
+  }
+  col += __shfl_xor(col, 16);
+  col += __shfl_xor(col, 32);
+  if (g == 0) {
+    s_read[me] = read - col;
+    s_write[me] = write;
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off);
+  if (lane == 0) s_dot[wave] = dot;
+#pragma unroll
+  for (int kb = 0; kb < C; kb += KG) {
+    if (kb <= 16 * wave) {  // keys up to the queries
+      const Op b = Ops<E>::b_from_d(&wt[kb / 16]);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) dq[i] = Ops<E>::mma_grp(L::tr(s_k, LDX, kb, 16 * i, lane), b, dq[i]);
+    }
+    if (kb + KG > 16 * wave) {  // queries from the keys on
+      const Op b = Ops<E>::b_from_d(&w[kb / 16]);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) dk[i] = Ops<E>::mma_grp(L::tr(s_q, LDX, kb, 16 * i, lane), b, dk[i]);
+    }
+  }
+  if (me < rows) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int c = 16 * i + 4 * g;
+      if (c < p.dk) {
+        store4((E *)p.dq + (row0 + me) * p.dk + c, dq[i]);
+        store4((E *)p.dk_ + (row0 + me) * p.dk + c, dk[i]);
+      }
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    // lane l: token C - 1 - l, so that sums from a token on are prefix sums
+    const int t = C - 1 - lane;
+    float ahead = 0.f, before = 0.f, x = 0.f;
+    if (t >= 0) {
+      ahead = s_read[t];
+      before = s_write[t];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) ahead += s_row[i][t];
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) x += s_dot[i];
+    const float sum = wave_inclusive_scan(ahead), behind = wave_inclusive_scan(before);
+    // writes in front of t: all of them less those from t on
+    const float all = lane_value(behind, 63);
+    const float dg = sum + (all - behind) + s_d.all * x;
+    if (p.dg_chunk) {
+      float s = t >= 0 && t < rows ? dg : 0.f;
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+      if (lane == 0) p.dg_chunk[(size_t)h * p.slots + slot] = s;
+    } else if (t >= 0 && t < rows) {
+      ((E *)p.dg)[row0 + t] = Elem<E>::from_f32(dg);
+    }
+  }
+}
+
+// The fixed decays' gradient: a head's chunks, in 64 bits and in an order of their own.
+__global__ __launch_bounds__(256) void kla_la_sum_kernel(const float *part, float *out, int slots) {
+  __shared__ double s[256];
+  double a = 0.0;
+  for (int i = threadIdx.x; i < slots; i += 256) a += part[(size_t)blockIdx.x * slots + i];
+  s[threadIdx.x] = a;
+  __syncthreads();
+  for (int w = 128; w >= 1; w >>= 1) {
+    if ((int)threadIdx.x < w) s[threadIdx.x] += s[threadIdx.x + w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) out[blockIdx.x] = (float)s[0];
+}
+
+// One token.  A workgroup owns 4 CG columns of one state, CG threads to a row and 256 / CG rows
+// at a time; each thread's rows are loaded together.
+struct LaStepParams {
+  const void *q, *k, *v, *g;
+  const float *gfix;
+  float *state;
+  void *o;
+  int H, dk, dv, slices;
+};
+
+template <typename E, int CG>
+__global__ __launch_bounds__(256) void kla_la_step_kernel(LaStepParams p) {
+  constexpr int RG = 256 / CG, RPT = 256 / RG < 16 ? 256 / RG : 16;  // rows at a time
+  __shared__ float s_k[256], s_q[256];
+  __shared__ f32x4 s_o[4][CG];
+  const size_t nh = blockIdx.x / p.slices;
+  const int slice = blockIdx.x % p.slices, tid = threadIdx.x;
+  const int cg = tid % CG, rg = tid / CG, col = (slice * CG + cg) * 4;
+  const bool mine = col < p.dv;
+  float *const S = p.state + nh * p.dk * p.dv + col;
+  f32x4 s[RPT];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int r = r0 + rg + RG * i;
+      s[i] = mine && r < p.dk ? *reinterpret_cast<const f32x4 *>(S + (size_t)r * p.dv) : zero4();
+    }
+  };
+  load(0);
+  if (tid < p.dk) {
+    s_k[tid] = Elem<E>::to_f32(((const E *)p.k)[nh * p.dk + tid]);
+    s_q[tid] = Elem<E>::to_f32(((const E *)p.q)[nh * p.dk + tid]);
+  }
+  const float g = p.gfix ? p.gfix[nh % p.H] : Elem<E>::to_f32(((const E *)p.g)[nh]);
+  const float a = __expf(g);
+  f32x4 v = zero4(), o = zero4();
+  if (mine) v = load4((const E *)p.v + nh * p.dv + col);
+  __syncthreads();
+  for (int r0 = 0; r0 < p.dk; r0 += RG * RPT) {
+    if (r0) load(r0);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int r = r0 + rg + RG * i;
+      if (r < p.dk) {
+        const float k = s_k[r], q = s_q[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[i][e] = fmaf(a, s[i][e], k * v[e]);
+          o[e] = fmaf(q, s[i][e], o[e]);
+        }
+        if (mine) *reinterpret_cast<f32x4 *>(S + (size_t)r * p.dv) = s[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int off = CG; off < 64; off <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], off);
+  if ((tid & 63) < CG) s_o[tid >> 6][cg] = o;
+  __syncthreads();
+  if (tid < CG && mine) {
+    o = s_o[0][cg];
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += s_o[w][cg][e];
+    store4((E *)p.o + nh * p.dv + col, o);
+  }
+}
+
+template <typename E, int DK, int MODE, bool REV>
+hipError_t launch_scan_t(const LaParams &p, hipStream_t st) {
+  const long long pairs = ((long long)p.N * p.H * p.segs + 7) / 8 * 8;
+  hipLaunchKernelGGL((kla_la_scan_kernel<E, DK, MODE, REV>), dim3((unsigned)(pairs * p.slices)), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+template <typename E, int MODE, bool REV>
+hipError_t launch_scan(const LaParams &p, hipStream_t st) {
+  if (p.dk <= 64) return launch_scan_t<E, 64, MODE, REV>(p, st);
+  if (p.dk <= 128) return launch_scan_t<E, 128, MODE, REV>(p, st);
+  return launch_scan_t<E, 256, MODE, REV>(p, st);
+}
+
+int la_chunk(int dtype) { return dtype == 0 ? La<bf16>::C : La<float>::C; }
+
+int la_slots(const LaArgs &a) {
+  const int C = la_chunk(a.dtype);
+  return a.cu_seqlens ? a.T / C + a.num_seqs : a.num_seqs * ((a.T + C - 1) / C);
+}
+
+// Segments of the scans.
+void la_segments(const LaArgs &a, int *segs, int *chunks) {
+  const int C = la_chunk(a.dtype), nch = (a.longest + C - 1) / C;
+  *segs = 1;
+  *chunks = std::max(nch, 1);
+}
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+// The workspace: the segments' states and decays; the backward's states and gradients of states
+// of all chunks, and the fixed decays' partial sums.
+struct LaSpace {
+  size_t seg_s, seg_g, states, dstates, dg, total;
+};
+LaSpace la_space(const LaArgs &a, bool bwd) {
+  int segs, chunks;
+  la_segments(a, &segs, &chunks);
+  const size_t pairs = (size_t)a.num_seqs * a.H * segs, state = (size_t)a.dk * a.dv;
+  LaSpace s{};
+  s.seg_g = segs > 1 ? up(pairs * state * sizeof(float)) : 0;
+  s.states = s.seg_g + (segs > 1 ? up(pairs * sizeof(double)) : 0);
+  s.total = s.dstates = s.dg = s.states;
+  if (bwd) {
+    const size_t n = (size_t)la_slots(a) * a.H, e = a.dtype == 0 ? 2 : 4;
+    s.dstates = s.states + up(n * state * e);
+    s.dg = s.dstates + up(n * state * e);
+    s.total = s.dg + up(n * sizeof(float));
+  }
+  return s;
+}
+
+LaParams la_params(const LaArgs &a) {
+  LaParams p{};
+  p.q = a.q;
+  p.x = a.k;
+  p.y = a.v;
+  p.g = a.g;
+  p.gfix = a.gfix;
+  p.cu = a.cu_seqlens;
+  p.N = a.num_seqs;
+  p.H = a.H;
+  p.T = a.T;
+  p.dk = a.dk;
+  p.dv = a.dv;
+  p.slices = (a.dv + LA_NV - 1) / LA_NV;
+  la_segments(a, &p.segs, &p.seg_chunks);
+  p.slots = la_slots(a);
+  return p;
+}
+
+template <typename E>
+hipError_t la_fwd_t(const LaArgs &a, hipStream_t st) {
+  LaParams p = la_params(a);
+  const LaSpace s = la_space(a, false);
+  p.s0 = a.initial_state;
+  p.o = a.o;
+  p.send = a.final_state;
+  p.seg_s = (float *)((char *)a.workspace + s.seg_s);
+  p.seg_g = (double *)((char *)a.workspace + s.seg_g);
+  if (p.segs > 1)
+    if (const hipError_t e = launch_scan<E, LA_ENDS, false>(p, st); e != hipSuccess) return e;
+  return launch_scan<E, LA_OUT, false>(p, st);
+}
+
+template <typename E, int DK>
+hipError_t launch_grad_t(const LaGradParams &p, hipStream_t st) {
+  hipLaunchKernelGGL((kla_la_grad_kernel<E, DK>), dim3((unsigned)((long long)p.slots * p.H)), dim3(La<E>::C * 4), 0, st, p);
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t la_bwd_t(const LaArgs &a, const LaGrads &b, hipStream_t st) {
+  const LaSpace s = la_space(a, true);
+  char *const ws = (char *)a.workspace;
+  if (a.num_seqs == 0) {  // nothing but the fixed decays' gradient, which is zero
+    if (a.gfix) hipLaunchKernelGGL(kla_la_sum_kernel, dim3((unsigned)a.H), dim3(256), 0, st, nullptr, (float *)b.dg, 0);
+    return hipGetLastError();
+  }
+  LaParams p = la_params(a);
+  p.seg_s = (float *)(ws + s.seg_s);
+  p.seg_g = (double *)(ws + s.seg_g);
+  p.s0 = a.initial_state;
+  p.states = ws + s.states;
+  hipError_t e;
+  if (p.segs > 1 && (e = launch_scan<E, LA_ENDS, false>(p, st)) != hipSuccess) return e;
+  if ((e = launch_scan<E, LA_STORE, false>(p, st)) != hipSuccess) return e;
+  p.x = a.q;
+  p.y = b.dout;
+  p.s0 = b.dfinal_state;
+  p.send = b.dinitial_state;
+  p.states = ws + s.dstates;
+  if (p.segs > 1 && (e = launch_scan<E, LA_ENDS, true>(p, st)) != hipSuccess) return e;
+  if ((e = launch_scan<E, LA_STORE, true>(p, st)) != hipSuccess) return e;
+  LaGradParams gp{};
+  gp.q = a.q;
+  gp.k = a.k;
+  gp.v = a.v;
+  gp.g = a.g;
+  gp.gfix = a.gfix;
+  gp.dout = b.dout;
+  gp.states = ws + s.states;
+  gp.dstates = ws + s.dstates;
+  gp.dq = b.dq;
+  gp.dk_ = b.dk;
+  gp.dv_ = b.dv;
+  gp.dg = b.dg;
+  gp.dg_chunk = a.gfix ? (float *)(ws + s.dg) : nullptr;
+  gp.cu = a.cu_seqlens;
+  gp.N = a.num_seqs;
+  gp.H = a.H;
+  gp.T = a.T;
+  gp.dk = a.dk;
+  gp.dv = a.dv;
+  gp.slots = p.slots;
+  if (gp.slots > 0) {
+    e = a.dk <= 64 ? launch_grad_t<E, 64>(gp, st) : a.dk <= 128 ? launch_grad_t<E, 128>(gp, st) : launch_grad_t<E, 256>(gp, st);
+    if (e != hipSuccess) return e;
+  }
+  if (a.gfix) {
+    hipLaunchKernelGGL(kla_la_sum_kernel, dim3((unsigned)a.H), dim3(256), 0, st, gp.dg_chunk, (float *)b.dg, gp.slots);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+template <typename E, int CG>
+hipError_t launch_step_t(LaStepParams p, long long nh, hipStream_t st) {
+  p.slices = (p.dv + 4 * CG - 1) / (4 * CG);
+  hipLaunchKernelGGL((kla_la_step_kernel<E, CG>), dim3((unsigned)(nh * p.slices)), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+template <typename E>
+hipError_t launch_step(const LaStepParams &p, long long nh, hipStream_t st) {
+  if (nh * ((p.dv + 127) / 128) < 512) return launch_step_t<E, 4>(p, nh, st);
+  return launch_step_t<E, 32>(p, nh, st);
+}
+
+}  // namespace
+
+bool la_supported(int dk, int dv) { return dk % 16 == 0 && dk <= 256 && dv % 16 == 0 && dv <= 256; }
+
+bool la_grid_fits(const LaArgs &a) {
+  int segs, chunks;
+  la_segments(a, &segs, &chunks);
+  const int C = la_chunk(a.dtype);
+  const double slots = a.cu_seqlens ? (double)a.T / C + a.num_seqs + 1 : (double)a.num_seqs * ((a.T + C - 1) / C);
+  return launch_fits(((double)a.num_seqs * a.H * segs + 8) * ((a.dv + LA_NV - 1) / LA_NV), 256) &&
+         launch_fits(slots * a.H, 256);
+}
+
+size_t la_workspace_bytes(const LaArgs &a, bool bwd) { return la_space(a, bwd).total; }
+
+hipError_t launch_la_fwd(const LaArgs &a, hipStream_t st) {
+  return a.dtype == 0 ? la_fwd_t<bf16>(a, st) : la_fwd_t<float>(a, st);
+}
+hipError_t launch_la_bwd(const LaArgs &a, const LaGrads &b, hipStream_t st) {
+  return a.dtype == 0 ? la_bwd_t<bf16>(a, b, st) : la_bwd_t<float>(a, b, st);
+}
+
+bool la_step_fits(long long nh, int dv) { return launch_fits((double)nh * ((dv + 15) / 16), 256); }
+
+hipError_t launch_la_step(const void *q, const void *k, const void *v, const void *g, const float *gfix, float *state,
+                          void *o, int N, int H, int dk, int dv, int dtype, hipStream_t st) {
+  const LaStepParams p{q, k, v, g, gfix, state, o, H, dk, dv, 1};
+  return dtype == 0 ? launch_step<bf16>(p, (long long)N * H, st) : launch_step<float>(p, (long long)N * H, st);
+}
+
+}  // namespace kla

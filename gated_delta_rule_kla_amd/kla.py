@@ -17,7 +17,8 @@ __all__ = ["chunk_fwd", "chunk_workspace_bytes", "chunk_fwd_workspace_bytes", "p
            "pgdn_chunk_workspace_bytes",
            "GAINS", "decode_step", "gdn_chunk_fwd", "gdn_decode_step", "chunk_bwd",
            "gdn_chunk_bwd", "chunk_bwd_workspace_bytes", "glr_chunk_fwd", "glr_chunk_bwd", "glr_decode_step",
-           "glr_chunk_workspace_bytes", "attn_fwd", "kv4_append", "kv4_read", "kv4_cache", "attn_kv4_decode_step",
+           "glr_chunk_workspace_bytes", "la_chunk_fwd", "la_chunk_bwd", "la_decode_step",
+           "la_chunk_workspace_bytes", "attn_fwd", "kv4_append", "kv4_read", "kv4_cache", "attn_kv4_decode_step",
            "attn_kv4_decode_workspace_bytes", "lib", "lib_path", "KlaError", "KLA_DT_BF16",
            "KLA_DT_F32"]
 
@@ -101,6 +102,15 @@ def lib() -> ctypes.CDLL:
         L.kla_glr_chunk_workspace_bytes.restype = sz
         L.kla_glr_decode_step.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp]
         L.kla_glr_decode_step.restype = i32
+        L.kla_la_chunk_fwd.argtypes = [vp] * 10 + [i32] * 7 + [vp, sz, vp]
+        L.kla_la_chunk_fwd.restype = i32
+        L.kla_la_chunk_bwd.argtypes = [vp] * 15 + [i32] * 7 + [vp, sz, vp]
+        L.kla_la_chunk_bwd.restype = i32
+        for f in (L.kla_la_chunk_workspace_bytes, L.kla_la_chunk_bwd_workspace_bytes):
+            f.argtypes = [vp, vp] + [i32] * 7
+            f.restype = sz
+        L.kla_la_decode_step.argtypes = [vp] * 7 + [i32] * 5 + [vp]
+        L.kla_la_decode_step.restype = i32
         L.kla_attn_fwd.argtypes = [vp, vp, vp, f32, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp]
         L.kla_attn_fwd.restype = i32
         for f in (L.kla_kv4_append, L.kla_kv4_read):
@@ -800,6 +810,152 @@ def _refuse_glr_step(x, g, state) -> None:
     _need(x, "x", x.dtype, shape, dev)
     _need(g, "g", x.dtype, shape, dev)
     _need(state, "state", torch.float32, shape, dev)
+
+
+def _decays(g, dtype, shape, dev):
+    """Pointers of g [*shape] in the inputs' dtype, or of per-head log-decays [H] in fp32."""
+    if isinstance(g, torch.Tensor) and g.dim() == 1:
+        _fit(g, "g", torch.float32, (shape[1],), dev)
+        return None, g.data_ptr()
+    _fit(g, "g", dtype, shape, dev)
+    return g.data_ptr(), None
+
+
+def la_chunk_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int, dtype: torch.dtype = torch.bfloat16,
+                             cu_seqlens_host: Optional[torch.Tensor] = None, backward: bool = False) -> int:
+    """Workspace bytes la_chunk_fwd, or la_chunk_bwd, needs (kla_la_chunk_workspace_bytes)."""
+    f = lib().kla_la_chunk_bwd_workspace_bytes if backward else lib().kla_la_chunk_workspace_bytes
+    if cu_seqlens_host is not None:
+        cu = cu_seqlens_host.to("cpu", torch.int32).contiguous()
+        # the device pointer is only tested for NULL here
+        return f(ctypes.c_void_p(16), cu.data_ptr(), cu.numel() - 1, B, H, T, dk, dv, _DTYPES[dtype])
+    return f(None, None, B, B, H, T, dk, dv, _DTYPES[dtype])
+
+
+def la_chunk_fwd(
+    q: torch.Tensor,
+    k: torch.Tensor,
+    v: torch.Tensor,
+    g: torch.Tensor,
+    initial_state: Optional[torch.Tensor] = None,
+    cu_seqlens: Optional[torch.Tensor] = None,
+    output_final_state: bool = True,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+    out: Optional[torch.Tensor] = None,
+    final_state: Optional[torch.Tensor] = None,
+    workspace: Optional[torch.Tensor] = None,
+) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay per head over whole sequences (kla_la_chunk_fwd):
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k: [B, H, T, dk]; v: [B, H, T, dv], bf16 or fp32; g: [B, H, T] in their dtype, or [H] fp32
+    for decays that are the same for all tokens of a head; initial_state: [N, H, dk, dv] fp32 or
+    None; cu_seqlens: int32 [N + 1] on the GPU (B must be 1) or None, with its host mirror to avoid
+    a copy back.  The mirror sizes the call, the offsets on the GPU decide: a captured call may be
+    replayed with others.  Returns (o, final_state); ``final_state`` may be passed as the same
+    tensor as ``initial_state``.
+    """
+    dev = _device_of("la_chunk_fwd", q)
+    dtype = q.dtype
+    B, H, T, dk = shape = _rank(q, "q", 4)
+    dv = _rank(v, "v", 4)[3]
+    _fit(q, "q", dtype, shape, dev)
+    _fit(k, "k", dtype, shape, dev)
+    _fit(v, "v", dtype, (B, H, T, dv), dev)
+    each, fixed = _decays(g, dtype, (B, H, T), dev)
+    N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
+    _optional(initial_state, "initial_state", torch.float32, (N, H, dk, dv), dev)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _fit(out, "out", dtype, (B, H, T, dv), dev)
+    if output_final_state and final_state is None:
+        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    _optional(final_state, "final_state", torch.float32, (N, H, dk, dv), dev)
+    host_ptr, dt = _ptr(host), _DTYPES[dtype]
+    ws = _scratch(workspace, lib().kla_la_chunk_workspace_bytes(_ptr(cu_seqlens), host_ptr, N, B, H, T, dk, dv, dt), dev)
+    _call("kla_la_chunk_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), each, fixed, _ptr(initial_state),
+          out.data_ptr(), _ptr(final_state), _ptr(cu_seqlens), host_ptr, N, B, H, T, dk, dv, dt, _ptr(ws),
+          0 if ws is None else ws.numel())
+    return out, final_state
+
+
+def la_chunk_bwd(
+    q: torch.Tensor,
+    k: torch.Tensor,
+    v: torch.Tensor,
+    g: torch.Tensor,
+    do: torch.Tensor,
+    initial_state: Optional[torch.Tensor] = None,
+    dfinal_state: Optional[torch.Tensor] = None,
+    cu_seqlens: Optional[torch.Tensor] = None,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+    need_dinitial: bool = True,
+    workspace: Optional[torch.Tensor] = None,
+):
+    """Gradients of la_chunk_fwd (kla_la_chunk_bwd) from its inputs and the upstream gradients
+    ``do`` [B, H, T, dv] and ``dfinal_state`` [N, H, dk, dv] fp32 or None.
+
+    Returns (dq, dk, dv, dg, dinitial_state): the first four shaped and typed as q, k, v and g
+    ([H] fp32 log-decays have the sum over all tokens), dinitial_state fp32 (None unless
+    ``need_dinitial``).
+    """
+    dev = _device_of("la_chunk_bwd", q)
+    dtype = q.dtype
+    B, H, T, dk = shape = _rank(q, "q", 4)
+    dv = _rank(v, "v", 4)[3]
+    _fit(q, "q", dtype, shape, dev)
+    _fit(k, "k", dtype, shape, dev)
+    _fit(v, "v", dtype, (B, H, T, dv), dev)
+    _fit(do, "do", dtype, (B, H, T, dv), dev)
+    each, fixed = _decays(g, dtype, (B, H, T), dev)
+    N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
+    _optional(initial_state, "initial_state", torch.float32, (N, H, dk, dv), dev)
+    _optional(dfinal_state, "dfinal_state", torch.float32, (N, H, dk, dv), dev)
+    dq, dk_, dv_, dg = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g)
+    ds0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if need_dinitial else None
+    host_ptr, dt = _ptr(host), _DTYPES[dtype]
+    ws = _scratch(workspace, lib().kla_la_chunk_bwd_workspace_bytes(_ptr(cu_seqlens), host_ptr, N, B, H, T, dk, dv, dt),
+                  dev)
+    _call("kla_la_chunk_bwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), each, fixed, _ptr(initial_state),
+          do.data_ptr(), _ptr(dfinal_state), dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), dg.data_ptr(), _ptr(ds0),
+          _ptr(cu_seqlens), host_ptr, N, B, H, T, dk, dv, dt, _ptr(ws), 0 if ws is None else ws.numel())
+    return dq, dk_, dv_, dg, ds0
+
+
+def la_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of linear attention (kla_la_decode_step): q, k [N, H, dk], v [N, H, dv], g [N, H]
+    in their dtype or [H] fp32; ``state`` [N, H, dk, dv] fp32 is updated in place.  Returns
+    o [N, H, dv]."""
+    if not (isinstance(q, torch.Tensor) and isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor)
+            and isinstance(g, torch.Tensor) and isinstance(state, torch.Tensor) and q.is_cuda and q.dtype in _DTYPES
+            and k.dtype is v.dtype is q.dtype and state.dtype is torch.float32 and q.dim() == 3 and v.dim() == 3
+            and q.shape == k.shape and state.shape == q.shape + v.shape[2:] and v.shape[:2] == q.shape[:2]
+            and q.device == k.device == v.device == g.device == state.device and q.is_contiguous()
+            and k.is_contiguous() and v.is_contiguous() and state.is_contiguous()):
+        _refuse_la_step(q, k, v, state)
+    dev, (N, H, dk), dv = q.device, q.shape, v.shape[2]
+    if N > _INT32 or H > _INT32 or dk > _INT32 or dv > _INT32:
+        _refuse_la_step(q, k, v, state)
+    each, fixed = _decays(g, q.dtype, (N, H), dev)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _fit(out, "out", q.dtype, v.shape, dev)
+    _call("kla_la_decode_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), each, fixed, state.data_ptr(),
+          out.data_ptr(), N, H, dk, dv, _DTYPES[q.dtype])
+    return out
+
+
+def _refuse_la_step(q, k, v, state) -> None:
+    dev = _device_of("la_decode_step", q)
+    N, H, dk = _rank(q, "q", 3)
+    dv = _rank(v, "v", 3)[2]
+    _need(q, "q", q.dtype, (N, H, dk), dev)
+    _need(k, "k", q.dtype, (N, H, dk), dev)
+    _need(v, "v", q.dtype, (N, H, dv), dev)
+    _need(state, "state", torch.float32, (N, H, dk, dv), dev)
 
 
 def attn_fwd(

@@ -67,7 +67,8 @@ typedef enum {
     KLA_ERR_HIP = -9,         /* the HIP runtime rejected a launch               */
     KLA_ERR_SCRATCH = -10,    /* kla_chunk_fwd_noalloc: more scratch than its fixed buffer */
     KLA_ERR_PARAM = -11       /* PGDN: gain not a kla_gain_t, or band not finite and >= 1;
-                                 attention: scale not finite, or beyond 2.3e38   */
+                                 attention: scale not finite, or beyond 2.3e38;
+                                 linear attention: both g and decay given        */
 } kla_status_t;
 
 /* The update coefficient ("gain") of the preconditioned variant (kla_pgdn_*). */
@@ -528,6 +529,88 @@ size_t kla_glr_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *c
  */
 kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, void *o,
                                  int N, int H, int d, kla_dtype_t dtype, void *stream);
+
+/*
+ * kla_la_chunk_fwd -- linear attention with a decay per head: the mixer whose state every token
+ * adds to without a look at what it holds.  Per sequence and head, with the state S in
+ * R^{dk x dv}:
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,     o_t = S_t^T q_t
+ *
+ *   q, k           [B, H, T, dk]  dtype
+ *   v, o           [B, H, T, dv]  dtype
+ *   g              [B, H, T]      dtype, the log-decay (g <= 0; -inf forgets the state), or NULL
+ *   decay          [H] fp32: a log-decay of each head's own, the same for all tokens, in place of
+ *                  g; or NULL.  Both: KLA_ERR_PARAM; neither: KLA_ERR_NULL
+ *   initial_state, final_state, cu_seqlens, cu_seqlens_host, num_seqs (N), B, H, T: as
+ *                  kla_chunk_fwd, without its limit on H.  The mirror only sizes the launch: with
+ *                  other offsets on the device (a captured call that is replayed with other
+ *                  lengths; not decreasing, within [0, T]) results are theirs, and rows that
+ *                  belong to no sequence are left as they were
+ *   workspace      kla_la_chunk_workspace_bytes(...) bytes for the same arguments (16-byte
+ *                  aligned, no initialisation needed; NULL when that is 0)
+ *
+ * Supported: dk and dv multiples of 16 up to 256, either dtype.  Tokens go in chunks (64 in BF16,
+ * 32 in F32).  With BF16 the scores q.k and the state that a chunk's outputs read are rounded to
+ * bf16 once (half a step of 2^-8, as o itself is), the state is summed in fp32 from products of
+ * 16 bits; F32 is fp32 throughout.  Where g > 0 makes a product of decays overflow fp32, outputs
+ * are not finite even if the recurrence would be; a value that is not finite reaches all outputs
+ * of its chunk, of its own and of later chunks, and no other sequence.  Sizes whose launch would
+ * have more than 2^32 threads are refused (KLA_ERR_SHAPE).  Results repeat bit for bit.  Status
+ * codes as kla_chunk_fwd.
+ */
+kla_status_t kla_la_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const float *decay,
+                              const float *initial_state, void *o, float *final_state,
+                              const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                              int num_seqs, int B, int H, int T, int dk, int dv,
+                              kla_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * kla_la_chunk_bwd -- gradients of kla_la_chunk_fwd.  With M_t the gradient that reaches S_t:
+ *
+ *     M_t  = q_t do_t^T + exp(g_{t+1}) M_{t+1}   (at the last token: q_t do_t^T + dL/dS_final)
+ *     dq_t = S_t do_t,   dk_t = M_t v_t,   dv_t = M_t^T k_t,   dg_t = exp(g_t) <M_t, S_{t-1}>,
+ *     dL/dS_initial = exp(g_1) M_1
+ *
+ *   q, k, v, g, decay, initial_state, cu_seqlens, ...: the forward call's
+ *   dout            [B, H, T, dv] dtype
+ *   dfinal_state    [N, H, dk, dv] fp32, or NULL (zero)
+ *   dq, dk_, dv_    shaped and typed as q, k, v (written)
+ *   dg              with g: [B, H, T] dtype; with decay: [H] fp32, the sum over all tokens, in a
+ *                   fixed order (written)
+ *   dinitial_state  [N, H, dk, dv] fp32 (written), or NULL (not computed)
+ *   workspace       kla_la_chunk_bwd_workspace_bytes(...) bytes
+ *
+ * Gradient buffers must not alias the inputs.  With BF16 each of the two states and of the two
+ * matrices of scores is rounded to bf16 once; dg's terms are products with such roundings, summed
+ * in fp32 (in 64 bits over a head).  Everything else as kla_la_chunk_fwd.
+ */
+kla_status_t kla_la_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const float *decay,
+                              const float *initial_state, const void *dout, const float *dfinal_state,
+                              void *dq, void *dk_, void *dv_, void *dg, float *dinitial_state,
+                              const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                              int num_seqs, int B, int H, int T, int dk, int dv,
+                              kla_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/* Device workspaces of kla_la_chunk_fwd and kla_la_chunk_bwd (host-only, no HIP call): where few
+ * sequences and heads make the library cut long sequences into segments, a state per segment;
+ * backward also two states per (chunk, head) in dtype and 4 bytes.  0 for arguments they would
+ * reject. */
+size_t kla_la_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs,
+                                    int B, int H, int T, int dk, int dv, kla_dtype_t dtype);
+size_t kla_la_chunk_bwd_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs,
+                                        int B, int H, int T, int dk, int dv, kla_dtype_t dtype);
+
+/*
+ * kla_la_decode_step -- one token of linear attention for N sequences x H heads: q, k [N, H, dk],
+ * v, o [N, H, dv], g [N, H] dtype or decay [H] fp32; state [N, H, dk, dv] fp32 updated IN PLACE.
+ * dk, dv as kla_la_chunk_fwd; fp32 throughout.
+ */
+kla_status_t kla_la_decode_step(const void *q, const void *k, const void *v, const void *g, const float *decay,
+                                float *state, void *o, int N, int H, int dk, int dv,
+                                kla_dtype_t dtype, void *stream);
 
 /*
  * kla_attn_fwd -- causal softmax attention over whole prompts: the quadratic mixer of stacks
