@@ -330,6 +330,35 @@ kla_status_t check_kv4_decode(int N, int Hq, int Hkv, int D, int num_pages, int 
 // Attention's scale, also as the kernels take it: times log2(e).
 bool good_scale(float scale) { return std::isfinite(scale * 1.44269504f); }
 
+// Sizes of a call of new tokens over the 4-bit cache; a's are set where they are fine.
+kla_status_t check_kv4_chunk(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B, int Hq,
+                             int Hkv, int T, int D, int num_pages, int page_size, int max_pages, int max_len,
+                             int dtype, kla::Kv4ChunkArgs *a) {
+  kla_status_t st = check_kv4(Hkv, D, num_pages, page_size, max_pages, num_seqs, dtype);
+  if (st != KLA_OK) return st;
+  if (B < 0 || T < 0 || T > kMaxTokens || Hq <= 0 || Hq > (1 << 20) || Hq % Hkv != 0 || max_len < 0 ||
+      max_len > kMaxTokens)
+    return KLA_ERR_SHAPE;
+  if ((double)B * Hq * T > (double)(1LL << 40)) return KLA_ERR_SHAPE;
+  int longest;
+  st = check_seqs(cu_seqlens, cu_seqlens_host, num_seqs, B, T, &longest);
+  if (st != KLA_OK) return st;
+  *a = kla::Kv4ChunkArgs{};
+  a->c.num_pages = num_pages;
+  a->c.page = page_size;
+  a->c.max_pages = max_pages;
+  a->c.Hkv = Hkv;
+  a->cu = cu_seqlens;
+  a->N = num_seqs;
+  a->B = B;
+  a->Hq = Hq;
+  a->T = T;
+  a->D = D;
+  a->max_len = max_len;
+  a->dtype = dtype;
+  return KLA_OK;
+}
+
 float band_log(float band) { return band == 1.f ? 0.f : std::log(band); }
 
 }  // namespace
@@ -740,6 +769,100 @@ kla_status_t kla_attn_kv4_decode_step(const void *q, const void *codes, const vo
   a.lens = seq_lens;
   a.scale = scale;
   return from_hip(kla::launch_attn_kv4_decode(a, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t kla_attn_kv4_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs,
+                                          int B, int Hq, int Hkv, int T, int D, int max_len, kla_dtype_t dtype_) {
+  kla::Kv4ChunkArgs a;
+  if (check_kv4_chunk(cu_seqlens, cu_seqlens_host, num_seqs, B, Hq, Hkv, T, D, 1, 16, 1, max_len, raw(dtype_), &a) !=
+          KLA_OK ||
+      !kla::kv4_chunk_grid_fits(a) || num_seqs == 0 || (long long)B * T == 0)
+    return 0;
+  return kla::kv4_chunk_workspace_bytes(a);
+}
+
+kla_status_t kla_attn_kv4_chunk_fwd(const void *q, const void *codes, const void *scales, const int32_t *block_table,
+                                    const int32_t *seq_lens, float scale, void *o, float *lse,
+                                    const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B,
+                                    int Hq, int Hkv, int T, int D, int num_pages, int page_size, int max_pages,
+                                    int max_len, kla_dtype_t dtype_, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+  kla::Kv4ChunkArgs a;
+  const kla_status_t st = check_kv4_chunk(cu_seqlens, cu_seqlens_host, num_seqs, B, Hq, Hkv, T, D, num_pages,
+                                          page_size, max_pages, max_len, raw(dtype_), &a);
+  if (st != KLA_OK) return st;
+  if (!kla::kv4_chunk_grid_fits(a)) return KLA_ERR_SHAPE;
+  if (!good_scale(scale)) return KLA_ERR_PARAM;
+  if (num_seqs == 0 || (long long)B * T == 0) return KLA_OK;
+  if (!q || !codes || !scales || !block_table || !seq_lens || !o) return KLA_ERR_NULL;
+  if (misaligned(q) || misaligned(codes) || misaligned(scales) || misaligned4(block_table) || misaligned4(seq_lens) ||
+      misaligned(o) || misaligned(lse) || misaligned(workspace))
+    return KLA_ERR_ALIGN;
+  const size_t need = kla::kv4_chunk_workspace_bytes(a);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KLA_ERR_WORKSPACE;
+  a.c.codes = const_cast<void *>(codes);
+  a.c.scales = const_cast<void *>(scales);
+  a.c.table = block_table;
+  a.q = q;
+  a.o = o;
+  a.lse = lse;
+  a.lens = seq_lens;
+  a.scale = scale;
+  return from_hip(kla::launch_attn_kv4_chunk(a, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+kla_status_t kla_attn_kv4_weigh(const void *q, const float *lse, const void *codes, const void *scales,
+                                const int32_t *block_table, const int32_t *seq_lens, float scale, float *weights,
+                                const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs, int B, int Hq,
+                                int Hkv, int T, int D, int num_pages, int page_size, int max_pages, int max_len,
+                                int max_tokens, kla_dtype_t dtype_, void *stream) {
+  kla::Kv4ChunkArgs a;
+  const kla_status_t st = check_kv4_chunk(cu_seqlens, cu_seqlens_host, num_seqs, B, Hq, Hkv, T, D, num_pages,
+                                          page_size, max_pages, max_len, raw(dtype_), &a);
+  if (st != KLA_OK) return st;
+  if ((long long)max_pages * page_size > max_tokens || !kla::kv4_weigh_grid_fits(a)) return KLA_ERR_SHAPE;
+  if (!good_scale(scale)) return KLA_ERR_PARAM;
+  if (num_seqs == 0 || (long long)B * T == 0) return KLA_OK;
+  if (!q || !lse || !codes || !scales || !block_table || !seq_lens || !weights) return KLA_ERR_NULL;
+  if (misaligned(q) || misaligned(lse) || misaligned(codes) || misaligned(scales) || misaligned4(block_table) ||
+      misaligned4(seq_lens) || misaligned(weights))
+    return KLA_ERR_ALIGN;
+  a.c.codes = const_cast<void *>(codes);
+  a.c.scales = const_cast<void *>(scales);
+  a.c.table = block_table;
+  a.q = q;
+  a.lse = const_cast<float *>(lse);
+  a.lens = seq_lens;
+  a.scale = scale;
+  return from_hip(kla::launch_attn_kv4_weigh(a, weights, max_tokens, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t kla_kv4_evict_workspace_bytes(int num_seqs, int Hkv, int D, int budget) {
+  if (check_kv4(Hkv, D, 1, 16, 1, num_seqs, KLA_DT_BF16) != KLA_OK || budget <= 0 || budget > kMaxTokens ||
+      !kla::kv4_evict_grid_fits(num_seqs, Hkv, budget))
+    return 0;
+  return kla::kv4_evict_workspace_bytes(num_seqs, Hkv, D, budget);
+}
+
+kla_status_t kla_kv4_evict(void *codes, void *scales, const int32_t *block_table, const int32_t *seq_lens,
+                           float *weights, int32_t *new_lens, int32_t *kept, int budget, int recent, int num_seqs,
+                           int Hkv, int D, int num_pages, int page_size, int max_pages, int max_tokens,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+  const kla_status_t st = check_kv4(Hkv, D, num_pages, page_size, max_pages, num_seqs, KLA_DT_BF16);
+  if (st != KLA_OK) return st;
+  if (max_tokens > kMaxTokens || (long long)max_pages * page_size > max_tokens) return KLA_ERR_SHAPE;
+  if (budget <= 0 || budget > kMaxTokens || recent < 0 || recent > budget) return KLA_ERR_PARAM;
+  if (!kla::kv4_evict_grid_fits(num_seqs, Hkv, budget)) return KLA_ERR_SHAPE;
+  if (num_seqs == 0) return KLA_OK;
+  if (!codes || !scales || !block_table || !seq_lens || !weights || !new_lens || !kept) return KLA_ERR_NULL;
+  if (misaligned(codes) || misaligned(scales) || misaligned4(block_table) || misaligned4(seq_lens) ||
+      misaligned(weights) || misaligned4(new_lens) || misaligned4(kept) || misaligned(workspace))
+    return KLA_ERR_ALIGN;
+  const size_t need = kla::kv4_evict_workspace_bytes(num_seqs, Hkv, D, budget);
+  if (workspace == nullptr || workspace_bytes < need) return KLA_ERR_WORKSPACE;
+  const kla::Kv4Cache c{codes, scales, block_table, num_pages, page_size, max_pages, Hkv};
+  return from_hip(kla::launch_kv4_evict(c, seq_lens, new_lens, kept, weights, num_seqs, D, max_tokens, budget, recent,
+                                        workspace, reinterpret_cast<hipStream_t>(stream)));
 }
 
 kla_status_t kla_attn_fwd(const void *q, const void *k, const void *v, float scale, void *o, float *lse,

@@ -201,6 +201,28 @@ size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs &a);
 bool kv4_decode_grid_fits(const Kv4DecodeArgs &a);
 hipError_t launch_attn_kv4_decode(const Kv4DecodeArgs &a, void *workspace, hipStream_t stream);
 
+// Attention of new tokens over the cache, and the weight they give to its tokens
+// (kla_kv4_chunk.hip).
+struct Kv4ChunkArgs {
+  Kv4Cache c;
+  const void *q;
+  void *o;
+  float *lse;                // attention: out, or nullptr; weights: in
+  const int32_t *lens, *cu;  // device; cu: or nullptr (dense)
+  float scale;
+  int N, B, Hq, T, D, max_len, dtype;
+};
+size_t kv4_chunk_workspace_bytes(const Kv4ChunkArgs &a);
+bool kv4_chunk_grid_fits(const Kv4ChunkArgs &a);
+hipError_t launch_attn_kv4_chunk(const Kv4ChunkArgs &a, void *workspace, hipStream_t stream);
+bool kv4_weigh_grid_fits(const Kv4ChunkArgs &a);
+hipError_t launch_attn_kv4_weigh(const Kv4ChunkArgs &a, float *weights, int W, hipStream_t stream);
+// The cache cut to a budget (kla_kv4_evict.hip).
+size_t kv4_evict_workspace_bytes(int N, int Hkv, int D, int budget);
+bool kv4_evict_grid_fits(int N, int Hkv, int budget);
+hipError_t launch_kv4_evict(const Kv4Cache &c, const int32_t *lens, int32_t *new_lens, int32_t *kept, float *weights,
+                            int N, int D, int W, int budget, int recent, void *workspace, hipStream_t stream);
+
 // Causal attention over whole prompts (kla_attn.hip).
 struct AttnArgs {
   const void *q, *k, *v;

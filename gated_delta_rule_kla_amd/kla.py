@@ -19,7 +19,8 @@ __all__ = ["chunk_fwd", "chunk_workspace_bytes", "chunk_fwd_workspace_bytes", "p
            "gdn_chunk_bwd", "chunk_bwd_workspace_bytes", "glr_chunk_fwd", "glr_chunk_bwd", "glr_decode_step",
            "glr_chunk_workspace_bytes", "la_chunk_fwd", "la_chunk_bwd", "la_decode_step",
            "la_chunk_workspace_bytes", "attn_fwd", "kv4_append", "kv4_read", "kv4_cache", "attn_kv4_decode_step",
-           "attn_kv4_decode_workspace_bytes", "lib", "lib_path", "KlaError", "KLA_DT_BF16",
+           "attn_kv4_decode_workspace_bytes", "attn_kv4_chunk_fwd", "attn_kv4_chunk_workspace_bytes",
+           "attn_kv4_weigh", "kv4_weights", "kv4_evict", "kv4_evict_workspace_bytes", "lib", "lib_path", "KlaError", "KLA_DT_BF16",
            "KLA_DT_F32"]
 
 KLA_DT_BF16 = 0
@@ -121,6 +122,16 @@ def lib() -> ctypes.CDLL:
         L.kla_attn_kv4_decode_step.restype = i32
         L.kla_attn_kv4_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
         L.kla_attn_kv4_decode_workspace_bytes.restype = sz
+        L.kla_attn_kv4_chunk_fwd.argtypes = [vp] * 5 + [f32] + [vp] * 4 + [i32] * 11 + [vp, sz, vp]
+        L.kla_attn_kv4_chunk_fwd.restype = i32
+        L.kla_attn_kv4_chunk_workspace_bytes.argtypes = [vp, vp] + [i32] * 8
+        L.kla_attn_kv4_chunk_workspace_bytes.restype = sz
+        L.kla_attn_kv4_weigh.argtypes = [vp] * 6 + [f32] + [vp] * 3 + [i32] * 12 + [vp]
+        L.kla_attn_kv4_weigh.restype = i32
+        L.kla_kv4_evict.argtypes = [vp] * 7 + [i32] * 9 + [vp, sz, vp]
+        L.kla_kv4_evict.restype = i32
+        L.kla_kv4_evict_workspace_bytes.argtypes = [i32] * 4
+        L.kla_kv4_evict_workspace_bytes.restype = sz
         L.kla_status_str.argtypes = [i32]
         L.kla_status_str.restype = ctypes.c_char_p
         L.kla_abi_version.argtypes = []
@@ -1149,3 +1160,151 @@ def attn_kv4_decode_step(
           seq_lens.data_ptr(), D ** -0.5 if scale is None else float(scale), out.data_ptr(), N, Hq, Hkv, D, P, page, M, max_len, dt, _ptr(ws),
           0 if ws is None else ws.numel())
     return out
+
+
+def _chunk_args(fn: str, q, codes, scales, block_table, seq_lens, cu_seqlens, cu_seqlens_host, max_len):
+    """Checked sizes of a call of new tokens over the cache."""
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dtype in _DTYPES and q.dim() == 4 and q.is_contiguous()):
+        _need(q, "q", q.dtype, _rank(q, "q", 4), _device_of(fn, q))
+    dev, (B, Hq, T, D) = q.device, q.shape
+    if max(q.shape) > _INT32:
+        _rank(q, "q", 4)
+    N, host = _seqlens(cu_seqlens, cu_seqlens_host, B, dev)
+    P, Hkv, page, Dc, M = _cache_args(codes, scales, block_table, N, dev)
+    if Dc != D:
+        raise ValueError(f"q has {D} channels, the cache {Dc}")
+    _fit(seq_lens, "seq_lens", torch.int32, (N,), dev)
+    max_len = min(M * page, _MAX_LEN) if max_len is None else min(int(max_len), _INT32)
+    return dev, N, host, (N, B, Hq, Hkv, T, D), (P, page, M, max_len)
+
+
+def attn_kv4_chunk_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, max_len: int,
+                                   dtype: torch.dtype = torch.bfloat16,
+                                   cu_seqlens_host: Optional[torch.Tensor] = None) -> int:
+    """Workspace bytes attn_kv4_chunk_fwd needs (kla_attn_kv4_chunk_workspace_bytes)."""
+    f, max_len = lib().kla_attn_kv4_chunk_workspace_bytes, min(int(max_len), _INT32)
+    if cu_seqlens_host is not None:
+        cu = cu_seqlens_host.to("cpu", torch.int32).contiguous()
+        # the device pointer is only tested for NULL here
+        return f(ctypes.c_void_p(16), cu.data_ptr(), cu.numel() - 1, B, Hq, Hkv, T, D, max_len, _DTYPES[dtype])
+    return f(None, None, B, B, Hq, Hkv, T, D, max_len, _DTYPES[dtype])
+
+
+def attn_kv4_chunk_fwd(
+    q: torch.Tensor,
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    block_table: torch.Tensor,
+    seq_lens: torch.Tensor,
+    cu_seqlens: Optional[torch.Tensor] = None,
+    scale: Optional[float] = None,
+    max_len: Optional[int] = None,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+    out: Optional[torch.Tensor] = None,
+    lse: Optional[torch.Tensor] = None,
+    workspace: Optional[torch.Tensor] = None,
+) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention of each sequence's newest tokens over a 4-bit cache
+    (kla_attn_kv4_chunk_fwd), which holds them already.
+
+    q: [B, Hq, T, D], bf16 or fp32; codes, scales, block_table: the cache; seq_lens: int32 [N]
+    cached tokens, the new ones among them; cu_seqlens: int32 [N + 1] packs the new tokens of N
+    sequences (B must be 1; None: N = B sequences of T); scale: D ** -0.5 when None; max_len: a bound
+    on seq_lens known to the host (the block table's room when None).  Returns (o, lse): lse
+    [B, Hq, T] fp32, the logarithm of each query's sum.
+    """
+    dev, N, host, sizes, cache = _chunk_args("attn_kv4_chunk_fwd", q, codes, scales, block_table, seq_lens, cu_seqlens,
+                                             cu_seqlens_host, max_len)
+    _, B, Hq, Hkv, T, D = sizes
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _fit(out, "out", q.dtype, q.shape, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+    else:
+        _fit(lse, "lse", torch.float32, (B, Hq, T), dev)
+    cu, host_ptr, dt = _ptr(cu_seqlens), _ptr(host), _DTYPES[q.dtype]
+    ws = _scratch(workspace, lib().kla_attn_kv4_chunk_workspace_bytes(cu, host_ptr, *sizes, cache[3], dt), dev)
+    _call("kla_attn_kv4_chunk_fwd", dev, q.data_ptr(), codes.data_ptr(), scales.data_ptr(), block_table.data_ptr(),
+          seq_lens.data_ptr(), D ** -0.5 if scale is None else float(scale), out.data_ptr(), lse.data_ptr(), cu, host_ptr,
+          *sizes, *cache, dt, _ptr(ws), 0 if ws is None else ws.numel())
+    return out, lse
+
+
+def kv4_weights(block_table: torch.Tensor, Hkv: int, page_size: int) -> torch.Tensor:
+    """No attention weight yet for any token of a cache: zeros [N, Hkv, max_pages * page_size] fp32."""
+    N, M = _rank(block_table, "block_table", 2)
+    return torch.zeros(N, Hkv, M * page_size, dtype=torch.float32, device=block_table.device)
+
+
+def attn_kv4_weigh(
+    q: torch.Tensor,
+    lse: torch.Tensor,
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    block_table: torch.Tensor,
+    seq_lens: torch.Tensor,
+    weights: torch.Tensor,
+    cu_seqlens: Optional[torch.Tensor] = None,
+    scale: Optional[float] = None,
+    max_len: Optional[int] = None,
+    cu_seqlens_host: Optional[torch.Tensor] = None,
+) -> None:
+    """Add the attention weight that each sequence's newest tokens give to every cached token
+    (kla_attn_kv4_weigh) to ``weights`` [N, Hkv, max_tokens] fp32, in place (kv4_weights makes
+    them).  q, lse and the rest as attn_kv4_chunk_fwd's, lse as it returned it."""
+    dev, N, host, sizes, cache = _chunk_args("attn_kv4_weigh", q, codes, scales, block_table, seq_lens, cu_seqlens,
+                                             cu_seqlens_host, max_len)
+    _, B, Hq, Hkv, T, D = sizes
+    _fit(lse, "lse", torch.float32, (B, Hq, T), dev)
+    W = _rank(weights, "weights", 3)[2]
+    _fit(weights, "weights", torch.float32, (N, Hkv, W), dev)
+    if W < cache[1] * cache[2]:
+        raise ValueError(f"weights has room for {W} tokens, the block table for {cache[1] * cache[2]}")
+    _call("kla_attn_kv4_weigh", dev, q.data_ptr(), lse.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+          block_table.data_ptr(), seq_lens.data_ptr(), D ** -0.5 if scale is None else float(scale), weights.data_ptr(),
+          _ptr(cu_seqlens), _ptr(host), *sizes, *cache, W, _DTYPES[q.dtype])
+
+
+def kv4_evict_workspace_bytes(N: int, Hkv: int, D: int, budget: int) -> int:
+    """Workspace bytes kv4_evict needs (kla_kv4_evict_workspace_bytes)."""
+    return lib().kla_kv4_evict_workspace_bytes(N, Hkv, D, min(int(budget), _INT32))
+
+
+def kv4_evict(
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    block_table: torch.Tensor,
+    seq_lens: torch.Tensor,
+    weights: torch.Tensor,
+    budget: int,
+    recent: int = 0,
+    workspace: Optional[torch.Tensor] = None,
+) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Cut every sequence of a 4-bit cache that holds more than ``budget`` tokens to that many
+    (kla_kv4_evict), in place, ``weights`` [N, Hkv, max_tokens] too: per key head the newest
+    ``recent`` tokens stay and those of the largest weight, in their order.
+
+    Returns (new_lens, kept): int32 [N] cached tokens and int32 [N, Hkv, budget] the former
+    position of each token that stays (-1 behind a shorter sequence's).
+    """
+    if not isinstance(codes, torch.Tensor) or codes.device.type != "cuda":
+        raise ValueError("kla.kv4_evict needs GPU tensors")
+    dev, N = codes.device, _rank(seq_lens, "seq_lens", 1)[0]
+    P, Hkv, page, D, M = _cache_args(codes, scales, block_table, N, dev)
+    _fit(seq_lens, "seq_lens", torch.int32, (N,), dev)
+    W = _rank(weights, "weights", 3)[2]
+    _fit(weights, "weights", torch.float32, (N, Hkv, W), dev)
+    if W < M * page:
+        raise ValueError(f"weights has room for {W} tokens, the block table for {M * page}")
+    budget, recent = int(budget), int(recent)
+    if not 1 <= budget <= _MAX_LEN or not 0 <= recent <= budget:
+        raise ValueError(f"budget {budget} and recent {recent}: expected 1 <= budget and 0 <= recent <= budget")
+    new_lens = torch.empty_like(seq_lens)
+    kept = torch.empty((N, Hkv, budget), dtype=torch.int32, device=dev)
+    ws = _scratch(workspace, lib().kla_kv4_evict_workspace_bytes(N, Hkv, D, budget), dev)
+    _call("kla_kv4_evict", dev, codes.data_ptr(), scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+          weights.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), budget, recent, N, Hkv, D, P, page, M, W, _ptr(ws),
+          0 if ws is None else ws.numel())
+    return new_lens, kept

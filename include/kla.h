@@ -68,7 +68,8 @@ typedef enum {
     KLA_ERR_SCRATCH = -10,    /* kla_chunk_fwd_noalloc: more scratch than its fixed buffer */
     KLA_ERR_PARAM = -11       /* PGDN: gain not a kla_gain_t, or band not finite and >= 1;
                                  attention: scale not finite, or beyond 2.3e38;
-                                 linear attention: both g and decay given        */
+                                 linear attention: both g and decay given;
+                                 eviction: budget < 1 or recent not in [0, budget] */
 } kla_status_t;
 
 /* The update coefficient ("gain") of the preconditioned variant (kla_pgdn_*). */
@@ -731,6 +732,103 @@ kla_status_t kla_attn_kv4_decode_step(const void *q, const void *codes, const vo
  * for arguments it would reject. */
 size_t kla_attn_kv4_decode_workspace_bytes(int N, int Hq, int Hkv, int D, int max_len,
                                            kla_dtype_t dtype);
+
+/*
+ * kla_attn_kv4_chunk_fwd -- causal softmax attention of each sequence's newest tokens over the
+ * 4-bit cache, which holds them already (append them first): a chunk of a prompt, the tokens of a draft that
+ * is verified, or one token.  With new = a sequence's queries, len = seq_lens[n], off = len - new:
+ *
+ *     o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j),   j <= i + off
+ *     lse_i = ln sum_j p_ij
+ *
+ * query head h reading key head h / (Hq / Hkv).  A query that sees no key has o = 0, lse = -inf.
+ *
+ *   q, o        [B, Hq, T, D] dtype; Hq a multiple of Hkv
+ *   lse         [B, Hq, T] fp32, or NULL (not written)
+ *   seq_lens    device int32 [N]: cached tokens of each sequence, the new ones among them
+ *   cu_seqlens, cu_seqlens_host, num_seqs (N), B, T: the new tokens' sequences, as
+ *               kla_chunk_fwd's.  The mirror sizes the launch, the device's offsets decide;
+ *               queries of no sequence keep what o and lse hold
+ *   max_len     host bound on seq_lens, which sizes the launch and the workspace; of a longer
+ *               sequence the keys up to max_len are read, and none beyond its block table
+ *   scale, codes, scales, block_table: as kla_attn_kv4_decode_step
+ *   workspace   kla_attn_kv4_chunk_workspace_bytes(...) bytes, as kla_chunk_fwd's
+ *
+ * Tokens on a page outside [0, num_pages) are left out.  Precision as kla_attn_kv4_decode_step.
+ * Keys and values that a query does not see do not reach it, also where the cache holds NaN:
+ * queries whose results are not finite are computed again key by key, which is slow.  Results
+ * repeat bit for bit.  Supported as kla_kv4_append; T * Hq / Hkv below 2^31 - 2^16.
+ */
+kla_status_t kla_attn_kv4_chunk_fwd(const void *q, const void *codes, const void *scales,
+                                    const int32_t *block_table, const int32_t *seq_lens,
+                                    float scale, void *o, float *lse,
+                                    const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                                    int num_seqs, int B, int Hq, int Hkv, int T, int D,
+                                    int num_pages, int page_size, int max_pages, int max_len,
+                                    kla_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* Device workspace of kla_attn_kv4_chunk_fwd (host-only, no HIP call): D + 2 floats per (query,
+ * query head, run of keys) where the keys are read in several runs, else 0; 0 for arguments it
+ * would reject. */
+size_t kla_attn_kv4_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                                          int num_seqs, int B, int Hq, int Hkv, int T, int D, int max_len,
+                                          kla_dtype_t dtype);
+
+/*
+ * kla_attn_kv4_weigh -- adds to every cached token the attention weight that the newest tokens
+ * give to it: for each sequence, key head and cached token j
+ *
+ *     weights_j += sum of exp(scale q_i . k_j - lse_i) over the queries i that see j, of all query
+ *                  heads that read the key head
+ *
+ * with the queries, lse and causal rule of kla_attn_kv4_chunk_fwd (call it first, or
+ * kla_attn_fwd for a prompt's first tokens; their lse differ where the keys were not rounded).
+ *
+ *   weights     [N, Hkv, max_tokens] fp32, updated IN PLACE; max_tokens at least
+ *               max_pages * page_size
+ *   lse         [B, Hq, T] fp32; a query whose lse is not finite gives nothing
+ *   others as kla_attn_kv4_chunk_fwd; tokens beyond max_len get nothing
+ *
+ * fp32 throughout (with F32 queries are three bf16 terms as in kla_attn_fwd); a token's sum is
+ * made in one order, so results repeat bit for bit.  No workspace.
+ */
+kla_status_t kla_attn_kv4_weigh(const void *q, const float *lse, const void *codes, const void *scales,
+                                const int32_t *block_table, const int32_t *seq_lens, float scale,
+                                float *weights, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                                int num_seqs, int B, int Hq, int Hkv, int T, int D,
+                                int num_pages, int page_size, int max_pages, int max_len, int max_tokens,
+                                kla_dtype_t dtype, void *stream);
+
+/*
+ * kla_kv4_evict -- cuts the 4-bit cache of every sequence that holds more than `budget` tokens to
+ * that many, for each key head by itself: the newest `recent` tokens stay, and of the others the
+ * budget - recent of the largest weight (of equal weights the earlier tokens; NaN counts as the
+ * largest).  They move to the positions 0 .. budget - 1 of the same pages, in their order, with
+ * their weights; the weights behind them up to the old length become zero, codes and scales there
+ * stay as they are.  Shorter sequences are not touched.  Attention over what is left needs no
+ * positions; a program that does finds them in `kept`.
+ *
+ *   seq_lens    device int32 [N]: cached tokens (none beyond the block table counts)
+ *   weights     [N, Hkv, max_tokens] fp32, as kla_attn_kv4_weigh's
+ *   new_lens    device int32 [N] (written): min(seq_lens, budget); not seq_lens' memory
+ *   kept        device int32 [N, Hkv, budget] (written): the former position of each token that
+ *               stays, -1 behind a shorter sequence's
+ *   budget      at least 1;  recent  in [0, budget]  (else KLA_ERR_PARAM)
+ *   workspace   kla_kv4_evict_workspace_bytes(...) bytes
+ *   others as kla_kv4_append
+ *
+ * A page in use by two sequences must not be cut.  A token of a missing page moves as zero, one
+ * that would move to a missing page is lost.  Results repeat bit for bit.
+ */
+kla_status_t kla_kv4_evict(void *codes, void *scales, const int32_t *block_table, const int32_t *seq_lens,
+                           float *weights, int32_t *new_lens, int32_t *kept, int budget, int recent,
+                           int num_seqs, int Hkv, int D, int num_pages, int page_size, int max_pages,
+                           int max_tokens, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device workspace of kla_kv4_evict (host-only, no HIP call): D + 32 bytes per sequence, key head
+ * and token of the budget; 0 for arguments it would reject. */
+size_t kla_kv4_evict_workspace_bytes(int num_seqs, int Hkv, int D, int budget);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *kla_status_str(kla_status_t s);
