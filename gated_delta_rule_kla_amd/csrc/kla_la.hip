@@ -12,7 +12,7 @@
 // exact behind a token that forgets everything (g = -inf counts as 2^-65536) as elsewhere.
 // Operands of the products are in the element type: the scores and the state (where outputs are
 // read from it) are rounded to it once, as the outputs are; the state itself is fp32, and the
-// scaled v_s that enter it are two bf16 terms (16 bits), since a final state is fp32 as well.
+// scaled v_s that enter it are three bf16 terms (24 bits), since a final state is fp32 as well.
 //
 // Backward, with M the gradient of the state at a chunk's end (dL/dS_final at the last):
 //
@@ -44,7 +44,7 @@ constexpr float LA_FORGET = -65536.f;  // log2 of the smallest decay
 // (or column), four of them (KG values) make a product.
 template <typename E> struct La;
 template <> struct La<bf16> {
-  static constexpr int C = 64, KG = 32, VL = 8, TERMS = 2;
+  static constexpr int C = 64, KG = 32, VL = 8, TERMS = 3;
   typedef bf16x8 Op;
   static __device__ __forceinline__ Op nat(const bf16 *row, int kb, int g) {
     return *reinterpret_cast<const bf16x8 *>(row + kb + 8 * g);
@@ -113,20 +113,30 @@ struct Decays {
   double tot;
 };
 
-// by one wave; g: the lane's log-decay (0 past the chunk's tokens)
+// by one wave; g[i]: the log-decay of token 64 i + lane (0 past the chunk's tokens)
 template <int C>
-__device__ __forceinline__ void scan_decays(Decays<C> *d, float g) {
+__device__ __forceinline__ void scan_decays(Decays<C> *d, const float *g) {
+  constexpr int N = (C + 63) / 64;
   const int lane = threadIdx.x & 63;
-  double x = (double)g * 1.4426950408889634;
-  x = x < LA_FORGET ? LA_FORGET : x;  // a NaN stays
-  if (lane >= C) x = 0.0;
-  const double c = scan_double(x), tot = lane_double(c, 63);
-  if (lane < C) {
-    const float hi = (float)c;
-    d->hi[lane] = hi;
-    d->lo[lane] = (float)(c - (double)hi);
-    d->out[lane] = __builtin_amdgcn_exp2f((float)c);
-    d->left[lane] = __builtin_amdgcn_exp2f((float)(tot - c));
+  double c[N], tot = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    double x = (double)g[i] * 1.4426950408889634;
+    x = x < LA_FORGET ? LA_FORGET : x;  // a NaN stays
+    if (64 * i + lane >= C) x = 0.0;
+    c[i] = scan_double(x) + tot;
+    tot = lane_double(c[i], 63);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int t = 64 * i + lane;
+    if (t < C) {
+      const float hi = (float)c[i];
+      d->hi[t] = hi;
+      d->lo[t] = (float)(c[i] - (double)hi);
+      d->out[t] = __builtin_amdgcn_exp2f((float)c[i]);
+      d->left[t] = __builtin_amdgcn_exp2f((float)(tot - c[i]));
+    }
   }
   if (lane == 0) {
     d->all = __builtin_amdgcn_exp2f((float)tot);
@@ -134,22 +144,31 @@ __device__ __forceinline__ void scan_decays(Decays<C> *d, float g) {
   }
 }
 
+// One direction of a scan: the factors of the state's updates (k, v; reverse: q, dout), the state
+// at the first processed chunk and behind the last.
+struct LaDir {
+  const void *x, *y;
+  const float *s0;  // or nullptr
+  float *send;      // or nullptr
+  void *states;     // [H, slots, dv, dk] element type
+  float *seg_s;     // [N H segs, dk, dv] states behind all segments but the last; in the last's
+                    // place the initial state (final_state may be the same memory)
+  double *seg_g;    // [N H segs] log2 of their decays
+};
+
 struct LaParams {
-  const void *q, *x, *y, *g;  // x, y: the factors of the state's updates (k, v; reverse: q, dout)
+  LaDir dir[2];               // forward, reverse
+  const void *q, *g;
   const float *gfix;          // [H] log-decays in place of g, or nullptr
-  const float *s0;            // state at the first processed chunk, or nullptr
-  void *o, *states;
-  float *send;                // state behind the last, or nullptr
+  void *o;
   const int32_t *cu;          // device offsets, or nullptr
   int N, H, T, dk, dv;
   int slices, segs, seg_chunks;
-  float *seg_s;               // [N H segs, dk, dv] states behind all segments but the last; in the last's
-                              // place the initial state (final_state may be the same memory)
-  double *seg_g;              // [N H segs] log2 of their decays
-  int slots;                  // chunk slots of a head (states)
+  unsigned half;              // workgroups of a direction
+  int slots, group;           // state slots of a head, chunks to a state
 };
 
-// Sequence n: its first row among a head's, its length, and its first chunk's slot.
+// Sequence n: its first row among a head's, its length, and its first slot of C tokens.
 __device__ __forceinline__ void la_span(const int32_t *cu, int n, int T, int C, int *t0, int *len, int *slot0) {
   if (!cu) {
     *t0 = 0, *len = T, *slot0 = n * ((T + C - 1) / C);
@@ -159,20 +178,23 @@ __device__ __forceinline__ void la_span(const int32_t *cu, int n, int T, int C, 
   *t0 = a, *len = z - a, *slot0 = a / C + n;
 }
 
-// The scan over a sequence's chunks.  A workgroup (four waves) holds LA_NV columns of the state,
-// each wave a quarter of its rows, in fp32, and a copy in the element type in LDS, from which all
-// waves read.  Of the outputs a wave computes 16 rows (bf16: of all columns; fp32, 32 tokens to a
-// chunk: of half of them).  x, y and q arrive in registers a chunk ahead, and go to LDS a chunk
-// ahead of their use, with y's scaled copy for the state; one barrier per chunk.
+// The scan over a sequence's chunks.  A workgroup holds LA_NV columns of the state.  Four waves
+// own the state, a quarter of its rows each, in fp32: they bring x and y to LDS a chunk ahead of
+// their use (from registers that hold the chunk after that), with y's scaled copy, update the
+// state, and leave a copy of it in the element type in LDS.  Beside them four waves compute the
+// outputs from those copies, 16 rows each (fp32, 32 tokens to a chunk: half of the columns);
+// the first, which has the fewest scores, also sums the decays of the chunk after next.  One
+// barrier per chunk.
 //
 // OUT: outputs and the final state.  ENDS: a segment's end state only, where few sequences leave
-// CUs idle and are cut: all segments but the last are scanned once for that, and OUT starts each
-// from those before it.  STORE: the state at each chunk's start (REV: the state's gradient
-// at its end), for the gradients.
+// CUs idle and are cut: all segments but the last are scanned once for that, and the other modes
+// start each from those before it.  STORE: the state at the start of every `group` chunks, and of
+// the reverse direction the state's gradient at their end, for the gradients.
 enum { LA_OUT, LA_ENDS, LA_STORE };
+constexpr int la_threads(int mode) { return mode == LA_OUT ? 512 : 320; }
 
-template <typename E, int DK, int MODE, bool REV>
-__global__ __launch_bounds__(256) void kla_la_scan_kernel(LaParams p) {
+template <typename E, int DK, int MODE>
+__global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams p) {
   using L = La<E>;
   using Op = typename L::Op;
   constexpr int C = L::C, KG = L::KG, VL = L::VL, NV = LA_NV;
@@ -183,39 +205,140 @@ __global__ __launch_bounds__(256) void kla_la_scan_kernel(LaParams p) {
   constexpr int KS = DK / KG;
   static_assert(XP * 256 * VL == C * DK && YP * 256 * VL == C * NV && CT * 4 == NC * NS, "tiles");
   __shared__ __attribute__((aligned(16))) E s_x[2][C * LDX];
-  __shared__ __attribute__((aligned(16))) E s_y[MODE == LA_OUT ? 2 : 1][C * LDY];
+  __shared__ __attribute__((aligned(16))) E s_y[MODE == LA_OUT ? 2 : 1][MODE == LA_OUT ? C * LDY : 8];
   __shared__ __attribute__((aligned(16))) E s_w[2][L::TERMS][C * LDY];  // y scaled
-  __shared__ __attribute__((aligned(16))) E s_s[MODE == LA_ENDS ? 1 : 2][MODE == LA_ENDS ? 16 : NV * LDX];  // S^T
+  __shared__ __attribute__((aligned(16))) E s_s[MODE == LA_OUT ? 2 : 1][MODE == LA_OUT ? NV * LDX : 8];  // S^T
   __shared__ Decays<C> s_d[3];
 
+  const bool rev = MODE != LA_OUT && blockIdx.x >= p.half;
+  const LaDir &dir = p.dir[rev];
   // workgroup ids go round the eight XCDs: the slices of a sequence and head, which read the
   // same rows, stay on one
-  const unsigned rest = blockIdx.x >> 3;
+  const unsigned id = blockIdx.x - (rev ? p.half : 0), rest = id >> 3;
   const int slice = rest % p.slices;
-  const long long pair = (long long)(rest / p.slices) * 8 + (blockIdx.x & 7);
+  const long long pair = (long long)(rest / p.slices) * 8 + (id & 7);
   if (pair >= (long long)p.N * p.H * p.segs) return;
   const int seg = pair % p.segs;
   const long long nh = pair / p.segs;
   const int n = nh / p.H, h = nh % p.H;
   int t0, len, slot0;
-  la_span(p.cu, n, p.T, C, &t0, &len, &slot0);
+  la_span(p.cu, n, p.T, C * p.group, &t0, &len, &slot0);
   const int nch = (len + C - 1) / C;
   // the chunks in processed order
   const int c0 = seg * p.seg_chunks, c1 = seg == p.segs - 1 ? nch : min(nch, c0 + p.seg_chunks);
   if (seg > 0 && c0 >= nch) return;
   if (MODE == LA_ENDS && c1 >= nch) return;
   const size_t row0 = ((size_t)(p.cu ? 0 : n) * p.H + h) * p.T + t0;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, li = lane & 15;
   const int col0 = slice * NV;
-  const int strip = wave % NS, ct0 = wave / NS * CT;
+  auto first_token = [&](int j) { return (rev ? nch - 1 - j : j) * C; };
 
-  auto first_token = [&](int j) { return (REV ? nch - 1 - j : j) * C; };
+  if (wave >= 4) {  // decays and outputs
+    const int strip = (wave - 4) % NS, ct0 = (wave - 4) / NS * CT;
+    auto load_g = [&](int j) {  // the lane's log-decay
+      const int t = first_token(j) + lane;
+      if (lane >= C || t >= len) return 0.f;
+      return p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + t]);
+    };
+    Op q[MODE == LA_OUT ? KS : 1];
+    auto load_q = [&](int j) {
+      if constexpr (MODE == LA_OUT) {
+        const int t = first_token(j), rows = min(C, len - t);
+        const __amdgpu_buffer_rsrc_t rq = buffer_rsrc((const E *)p.q + (row0 + t) * p.dk, rows * p.dk * (int)sizeof(E));
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int c = k * KG + VL * g;
+          q[k] = L::cvt(buffer_ld16(rq, c < p.dk ? ((16 * strip + li) * p.dk + c) * (int)sizeof(E) : 0x40000000));
+        }
+      }
+    };
+    float gn[2] = {0.f, 0.f};
+    if (c0 < c1) {
+      load_q(c0);
+      if (wave == 4) {
+        const float g0 = load_g(c0), g1 = c0 + 1 < c1 ? load_g(c0 + 1) : 0.f;
+        if (c0 + 2 < c1) gn[0] = load_g(c0 + 2);
+        if (c0 + 3 < c1) gn[1] = load_g(c0 + 3);
+        scan_decays<C>(&s_d[c0 % 3], &g0);
+        if (c0 + 1 < c1) scan_decays<C>(&s_d[(c0 + 1) % 3], &g1);
+      }
+      lds_barrier();
+    }
+    for (int j = c0; j < c1; ++j) {
+      lds_barrier();
+      if (wave == 4 && j + 2 < c1) {
+        scan_decays<C>(&s_d[(j + 2) % 3], &gn[0]);
+        gn[0] = gn[1];
+        if (j + 4 < c1) gn[1] = load_g(j + 4);
+      }
+      if constexpr (MODE == LA_OUT) {
+        const E *const X = s_x[j & 1], *const Y = s_y[j & 1], *const S = s_s[j & 1];
+        const Decays<C> &d = s_d[j % 3];
+        // P^T: keys 16 kt + 4 g + e against the strip's query li
+        f32x4 pt[NS];
+        const float th = d.hi[16 * strip + li], tl = d.lo[16 * strip + li];
+#pragma unroll
+        for (int kt = 0; kt < NS; ++kt) {
+          pt[kt] = zero4();
+          if (kt <= strip) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+              pt[kt] = Ops<E>::mma_grp(L::nat(X + (16 * kt + li) * LDX, k * KG, g), q[k], pt[kt]);
+          }
+        }
+        f32x4 o[CT];  // o^T: columns 4 g + e of query li
+        const float f = d.out[16 * strip + li];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          o[c] = zero4();
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            o[c] = Ops<E>::mma_grp(L::nat(S + (16 * (ct0 + c) + li) * LDX, k * KG, g), q[k], o[c]);
+        }
+        if (j + 1 < c1) load_q(j + 1);
+#pragma unroll
+        for (int kt = 0; kt < NS; ++kt)
+          if (kt <= strip) {
+            const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * kt + 4 * g]);
+            const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * kt + 4 * g]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              pt[kt][e] = kt < strip || 4 * g + e <= li
+                              ? pt[kt][e] * __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) : 0.f;
+          }
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[c][e] *= f;
+#pragma unroll
+        for (int kb = 0; kb < C; kb += KG)
+          if (kb / 16 <= strip) {
+            const Op w = Ops<E>::b_from_d(&pt[kb / 16]);
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+              o[c] = Ops<E>::mma_grp(L::tr(Y, LDY, kb, 16 * (ct0 + c), lane), w, o[c]);
+          }
+        const int t = first_token(j) + 16 * strip + li;
+        if (t < len) {
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            const int col = col0 + 16 * (ct0 + c) + 4 * g;
+            if (col < p.dv) store4((E *)p.o + (row0 + t) * p.dv + col, o[c]);
+          }
+        }
+      }
+    }
+    return;
+  }
+
+  // the state
+  const int tid = threadIdx.x;
   uint4 xr[XP], yr[YP];
   auto load = [&](int j) {
     const int t = first_token(j), rows = min(C, len - t);
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc((const E *)p.x + (row0 + t) * p.dk, rows * p.dk * (int)sizeof(E));
-    const __amdgpu_buffer_rsrc_t ry = buffer_rsrc((const E *)p.y + (row0 + t) * p.dv, rows * p.dv * (int)sizeof(E));
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc((const E *)dir.x + (row0 + t) * p.dk, rows * p.dk * (int)sizeof(E));
+    const __amdgpu_buffer_rsrc_t ry = buffer_rsrc((const E *)dir.y + (row0 + t) * p.dv, rows * p.dv * (int)sizeof(E));
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
       const int pc = tid + 256 * i, r = pc / (DK / VL), c = pc % (DK / VL) * VL;
@@ -230,6 +353,7 @@ __global__ __launch_bounds__(256) void kla_la_scan_kernel(LaParams p) {
   auto put = [&](int j) {  // chunk j's rows from registers
     E *const dx = s_x[j & 1];
     const Decays<C> &d = s_d[j % 3];
+    const float *const fs = rev ? d.out : d.left;
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
       const int pc = tid + 256 * i;
@@ -238,7 +362,7 @@ __global__ __launch_bounds__(256) void kla_la_scan_kernel(LaParams p) {
 #pragma unroll
     for (int i = 0; i < YP; ++i) {
       const int pc = tid + 256 * i, r = pc / (NV / VL), at = r * LDY + pc % (NV / VL) * VL;
-      const float f = REV ? d.out[r] : d.left[r];
+      const float f = fs[r];
       E e[VL], w[L::TERMS][VL];
       __builtin_memcpy(e, &yr[i], 16);
 #pragma unroll
@@ -256,23 +380,6 @@ __global__ __launch_bounds__(256) void kla_la_scan_kernel(LaParams p) {
         uint4 v;
         __builtin_memcpy(&v, w[k], 16);
         *reinterpret_cast<uint4 *>(s_w[j & 1][k] + at) = v;
-      }
-    }
-  };
-  auto load_g = [&](int j) {  // the lane's log-decay
-    const int t = first_token(j) + lane;
-    if (lane >= C || t >= len) return 0.f;
-    return p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + t]);
-  };
-  Op q[MODE == LA_OUT ? KS : 1];
-  auto load_q = [&](int j) {
-    if constexpr (MODE == LA_OUT) {
-      const int t = first_token(j), rows = min(C, len - t);
-      const __amdgpu_buffer_rsrc_t rq = buffer_rsrc((const E *)p.q + (row0 + t) * p.dk, rows * p.dk * (int)sizeof(E));
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int c = k * KG + VL * g;
-        q[k] = L::cvt(buffer_ld16(rq, c < p.dk ? ((16 * strip + li) * p.dk + c) * (int)sizeof(E) : 0x40000000));
       }
     }
   };
@@ -295,116 +402,59 @@ __global__ __launch_bounds__(256) void kla_la_scan_kernel(LaParams p) {
         }
   };
   const size_t ssize = (size_t)p.dk * p.dv;
-  if (c0 < c1) {
-    load(c0);
-    load_q(c0);
-    if (wave == 0) scan_decays<C>(&s_d[c0 % 3], load_g(c0));
-    if (wave == 1 && c0 + 1 < c1) scan_decays<C>(&s_d[(c0 + 1) % 3], load_g(c0 + 1));
-  }
+  if (c0 < c1) load(c0);
   if (seg == 0) {
-    const bool copied = MODE == LA_OUT && p.segs > 1 && c1 < nch;
-    const float *s0 = p.s0 ? (copied ? p.seg_s + (nh * p.segs + p.segs - 1) * ssize : p.s0 + nh * ssize) : nullptr;
+    const bool copied = MODE != LA_ENDS && p.segs > 1 && c1 < nch;
+    const float *s0 = dir.s0 ? (copied ? dir.seg_s + (nh * p.segs + p.segs - 1) * ssize : dir.s0 + nh * ssize) : nullptr;
     if (s0) each([&](float, size_t at) { return s0[at]; });
     if (MODE == LA_ENDS && s0) {
-      float *const copy = p.seg_s + (nh * p.segs + p.segs - 1) * ssize;
+      float *const copy = dir.seg_s + (nh * p.segs + p.segs - 1) * ssize;
       each([&](float a, size_t at) { return copy[at] = a; });
     }
   } else if (MODE != LA_ENDS) {
     for (int i = 0; i < seg; ++i) {  // the segments before this one, in order
-      const float f = __builtin_amdgcn_exp2f((float)p.seg_g[nh * p.segs + i]);
-      const float *const d = p.seg_s + (nh * p.segs + i) * ssize;
+      const float f = __builtin_amdgcn_exp2f((float)dir.seg_g[nh * p.segs + i]);
+      const float *const d = dir.seg_s + (nh * p.segs + i) * ssize;
       each([&](float a, size_t at) { return (i ? f * a : 0.f) + d[at]; });
     }
   }
   auto publish = [&](int j) {  // the state in front of chunk j
-    if constexpr (MODE != LA_ENDS) {
+    if constexpr (MODE == LA_OUT) {
       E *const d = s_s[j & 1];
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int c = 0; c < NC; ++c) store4(d + (16 * c + li) * LDX + 16 * (wave * RT + i) + 4 * g, acc[i][c]);
     }
+    if constexpr (MODE == LA_STORE) {
+      const int chunk = first_token(j) / C;
+      if (rev ? (chunk + 1) % p.group == 0 || chunk == nch - 1 : chunk % p.group == 0) {
+        E *const to = (E *)dir.states + ((size_t)h * p.slots + slot0 + chunk / p.group) * ssize;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int r = 16 * (wave * RT + i) + 4 * g, col = col0 + 16 * c + li;
+            if (r < p.dk && col < p.dv) store4(to + (size_t)col * p.dk + r, acc[i][c]);
+          }
+      }
+    }
   };
   double total = 0.0;
-  float gn = 0.f;
   if (c0 < c1) {
     lds_barrier();
     put(c0);
     publish(c0);
     if (c0 + 1 < c1) load(c0 + 1);
-    if (c0 + 2 < c1) gn = load_g(c0 + 2);
   }
 
   for (int j = c0; j < c1; ++j) {
     lds_barrier();
     if (j + 1 < c1) put(j + 1);
-    if (j + 2 < c1) {
-      load(j + 2);
-      if (wave == (j & 3)) scan_decays<C>(&s_d[(j + 2) % 3], gn);
-    }
-    if (j + 3 < c1) gn = load_g(j + 3);
+    if (j + 2 < c1) load(j + 2);
     const E *const X = s_x[j & 1];
     const Decays<C> &d = s_d[j % 3];
     if (MODE == LA_ENDS) total += d.tot;
-
-    if constexpr (MODE == LA_STORE) {
-      // S^T as it stands in LDS, rows of dk elements
-      E *const to = (E *)p.states + ((size_t)h * p.slots + slot0 + first_token(j) / C) * ssize + (size_t)col0 * p.dk;
-      const int per = p.dk / VL, pieces = min(NV, p.dv - col0) * per;
-      for (int i = tid; i < pieces; i += 256) {
-        const int r = i / per, c = i % per * VL;
-        stg16(to + (size_t)r * p.dk + c, *reinterpret_cast<const uint4 *>(s_s[j & 1] + r * LDX + c));
-      }
-    }
-    if constexpr (MODE == LA_OUT) {
-      const E *const Y = s_y[j & 1], *const S = s_s[j & 1];
-      // P^T: keys 16 kt + 4 g + e against the strip's query li
-      f32x4 pt[NS];
-      const float th = d.hi[16 * strip + li], tl = d.lo[16 * strip + li];
-#pragma unroll
-      for (int kt = 0; kt < NS; ++kt) {
-        pt[kt] = zero4();
-        if (kt <= strip) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-            pt[kt] = Ops<E>::mma_grp(L::nat(X + (16 * kt + li) * LDX, k * KG, g), q[k], pt[kt]);
-          const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * kt + 4 * g]);
-          const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * kt + 4 * g]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            pt[kt][e] = kt < strip || 4 * g + e <= li
-                            ? pt[kt][e] * __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) : 0.f;
-        }
-      }
-      f32x4 o[CT];  // o^T: columns 4 g + e of query li
-#pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        o[c] = zero4();
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-          o[c] = Ops<E>::mma_grp(L::nat(S + (16 * (ct0 + c) + li) * LDX, k * KG, g), q[k], o[c]);
-        const float f = d.out[16 * strip + li];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[c][e] *= f;
-      }
-      if (j + 1 < c1) load_q(j + 1);
-#pragma unroll
-      for (int kb = 0; kb < C; kb += KG)
-        if (kb / 16 <= strip) {
-          const Op w = Ops<E>::b_from_d(&pt[kb / 16]);
-#pragma unroll
-          for (int c = 0; c < CT; ++c)
-            o[c] = Ops<E>::mma_grp(L::tr(Y, LDY, kb, 16 * (ct0 + c), lane), w, o[c]);
-        }
-      const int t = first_token(j) + 16 * strip + li;
-      if (t < len) {
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const int col = col0 + 16 * (ct0 + c) + 4 * g;
-          if (col < p.dv) store4((E *)p.o + (row0 + t) * p.dv + col, o[c]);
-        }
-      }
-    }
     const float f = d.all;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -423,19 +473,19 @@ __global__ __launch_bounds__(256) void kla_la_scan_kernel(LaParams p) {
       for (int i = 0; i < RT; ++i) {
         const Op a = L::tr(X, LDX, kb, 16 * (wave * RT + i), lane);
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int k = 0; k < L::TERMS; ++k)
 #pragma unroll
-          for (int k = 0; k < L::TERMS; ++k) acc[i][c] = Ops<E>::mma_grp(a, w[k][c], acc[i][c]);
+          for (int c = 0; c < NC; ++c) acc[i][c] = Ops<E>::mma_grp(a, w[k][c], acc[i][c]);
       }
     }
     if (j + 1 < c1) publish(j + 1);
   }
   if constexpr (MODE == LA_ENDS) {
-    float *const to = p.seg_s + (nh * p.segs + seg) * ssize;
+    float *const to = dir.seg_s + (nh * p.segs + seg) * ssize;
     each([&](float a, size_t at) { return to[at] = a; });
-    if (tid == 0 && slice == 0) p.seg_g[nh * p.segs + seg] = total;
-  } else if (p.send && c1 >= nch) {
-    float *const to = p.send + nh * ssize;
+    if (tid == 0 && slice == 0) dir.seg_g[nh * p.segs + seg] = total;
+  } else if (dir.send && c1 >= nch) {
+    float *const to = dir.send + nh * ssize;
     each([&](float a, size_t at) { return to[at] = a; });
   }
 }
@@ -455,11 +505,11 @@ struct LaGradParams {
   int N, B, H, T, dk, dv, slots;
 };
 
-template <typename E, int DK>
-__global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams p) {
+template <typename E, int DK, int C>
+__global__ __launch_bounds__(C * 4) void kla_la_grad_kernel(LaGradParams p) {
   using L = La<E>;
   using Op = typename L::Op;
-  constexpr int C = L::C, KG = L::KG, VL = L::VL, NV = LA_NV, NS = C / 16, NT = 64 * NS;
+  constexpr int KG = L::KG, VL = L::VL, NV = LA_NV, NS = C / 16, NT = 64 * NS;
   constexpr int PAD = LdsPad<E>::V, LDX = DK + PAD, LDY = NV + PAD;
   constexpr int KS = DK / KG, RB = DK / 16, NC = NV / 16;
   __shared__ __attribute__((aligned(16))) E s_q[C * LDX], s_k[C * LDX], s_v[C * LDY], s_o[C * LDY], s_s[NV * LDX], s_m[NV * LDX];
@@ -502,8 +552,13 @@ __global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams 
       b[i] = buffer_ld16(rk, at);
     }
     if (wave == 0) {
-      float gl = 0.f;
-      if (lane < rows) gl = p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + lane]);
+      constexpr int NG = (C + 63) / 64;
+      float gl[NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const int t = 64 * i + lane;
+        gl[i] = t >= rows ? 0.f : p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + t]);
+      }
       scan_decays<C>(&s_d, gl);
     }
 #pragma unroll
@@ -525,50 +580,55 @@ __global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams 
   float dot = 0.f;
   const int me = 16 * wave + li;
 
-  for (int c0 = 0; c0 < p.dv; c0 += NV) {
+  // a slice's rows and states: in registers while the one before it is in use
+  constexpr int YP = C * NV / VL / NT, XT = NV * DK / VL, XP = (XT + NT - 1) / NT;
+  uint4 rv[YP], ro[YP], rs[XP], rm[XP];
+  auto load = [&](int c0) {
     const int cols = min(NV, p.dv - c0);
-    {
-      const __amdgpu_buffer_rsrc_t rv = buffer_rsrc((const E *)p.v + row0 * p.dv, rows * p.dv * (int)sizeof(E));
-      const __amdgpu_buffer_rsrc_t ro = buffer_rsrc((const E *)p.dout + row0 * p.dv, rows * p.dv * (int)sizeof(E));
-      const size_t at0 = ((size_t)h * p.slots + slot) * p.dk * p.dv + (size_t)c0 * p.dk;
-      const __amdgpu_buffer_rsrc_t rs = buffer_rsrc((const E *)p.states + at0, cols * p.dk * (int)sizeof(E));
-      const __amdgpu_buffer_rsrc_t rm = buffer_rsrc((const E *)p.dstates + at0, cols * p.dk * (int)sizeof(E));
-      constexpr int YP = C * NV / VL / NT, XP = NV * DK / VL / NT;
-      uint4 v[YP], o[YP], s[XP], m[XP];
+    const __amdgpu_buffer_rsrc_t bv = buffer_rsrc((const E *)p.v + row0 * p.dv, rows * p.dv * (int)sizeof(E));
+    const __amdgpu_buffer_rsrc_t bo = buffer_rsrc((const E *)p.dout + row0 * p.dv, rows * p.dv * (int)sizeof(E));
+    const size_t at0 = ((size_t)h * p.slots + slot) * p.dk * p.dv + (size_t)c0 * p.dk;
+    const __amdgpu_buffer_rsrc_t bs = buffer_rsrc((const E *)p.states + at0, cols * p.dk * (int)sizeof(E));
+    const __amdgpu_buffer_rsrc_t bm = buffer_rsrc((const E *)p.dstates + at0, cols * p.dk * (int)sizeof(E));
 #pragma unroll
-      for (int i = 0; i < YP; ++i) {
-        const int pc = tid + NT * i, r = pc / (NV / VL), c = c0 + pc % (NV / VL) * VL;
-        const int at = c < p.dv ? (r * p.dv + c) * (int)sizeof(E) : 0x40000000;
-        v[i] = buffer_ld16(rv, at);
-        o[i] = buffer_ld16(ro, at);
-      }
-#pragma unroll
-      for (int i = 0; i < XP; ++i) {
-        const int pc = tid + NT * i, r = pc / (DK / VL), c = pc % (DK / VL) * VL;
-        const int at = c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000;
-        s[i] = buffer_ld16(rs, at);
-        m[i] = buffer_ld16(rm, at);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < YP; ++i) {
-        const int pc = tid + NT * i, at = pc / (NV / VL) * LDY + pc % (NV / VL) * VL;
-        *reinterpret_cast<uint4 *>(s_v + at) = v[i];
-        *reinterpret_cast<uint4 *>(s_o + at) = o[i];
-      }
-#pragma unroll
-      for (int i = 0; i < XP; ++i) {
-        const int pc = tid + NT * i, at = pc / (DK / VL) * LDX + pc % (DK / VL) * VL;
-        *reinterpret_cast<uint4 *>(s_s + at) = s[i];
-        *reinterpret_cast<uint4 *>(s_m + at) = m[i];
-        E a[VL], b[VL];
-        __builtin_memcpy(a, &s[i], 16);
-        __builtin_memcpy(b, &m[i], 16);
-#pragma unroll
-        for (int e = 0; e < VL; ++e) dot = fmaf(Elem<E>::to_f32(a[e]), Elem<E>::to_f32(b[e]), dot);
-      }
-      __syncthreads();
+    for (int i = 0; i < YP; ++i) {
+      const int pc = tid + NT * i, r = pc / (NV / VL), c = c0 + pc % (NV / VL) * VL;
+      const int at = c < p.dv ? (r * p.dv + c) * (int)sizeof(E) : 0x40000000;
+      rv[i] = buffer_ld16(bv, at);
+      ro[i] = buffer_ld16(bo, at);
     }
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      const int pc = tid + NT * i, r = pc / (DK / VL), c = pc % (DK / VL) * VL;
+      const int at = pc < XT && c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000;
+      rs[i] = buffer_ld16(bs, at);
+      rm[i] = buffer_ld16(bm, at);
+    }
+  };
+  load(0);
+  for (int c0 = 0; c0 < p.dv; c0 += NV) {
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < YP; ++i) {
+      const int pc = tid + NT * i, at = pc / (NV / VL) * LDY + pc % (NV / VL) * VL;
+      *reinterpret_cast<uint4 *>(s_v + at) = rv[i];
+      *reinterpret_cast<uint4 *>(s_o + at) = ro[i];
+    }
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      const int pc = tid + NT * i, at = pc / (DK / VL) * LDX + pc % (DK / VL) * VL;
+      if (XT % NT == 0 || pc < XT) {
+        *reinterpret_cast<uint4 *>(s_s + at) = rs[i];
+        *reinterpret_cast<uint4 *>(s_m + at) = rm[i];
+      }
+      E a[VL], b[VL];
+      __builtin_memcpy(a, &rs[i], 16);
+      __builtin_memcpy(b, &rm[i], 16);
+#pragma unroll
+      for (int e = 0; e < VL; ++e) dot = fmaf(Elem<E>::to_f32(a[e]), Elem<E>::to_f32(b[e]), dot);
+    }
+    if (c0 + NV < p.dv) load(c0 + NV);
+    lds_barrier();
     if (c0 == 0) {  // the scores of the wave's keys, once
 #pragma unroll
       for (int i = 0; i < NS; ++i)
@@ -709,28 +769,42 @@ __global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams 
   }
   __syncthreads();
   if (wave == 0) {
-    // lane l: token C - 1 - l, so that sums from a token on are prefix sums
-    const int t = C - 1 - lane;
-    float ahead = 0.f, before = 0.f, x = 0.f;
-    if (t >= 0) {
-      ahead = s_read[t];
-      before = s_write[t];
-#pragma unroll
-      for (int i = 0; i < NS; ++i) ahead += s_row[i][t];
-    }
+    // 64 tokens at a time from the end, lane l token 63 - l of them, so that sums from a token
+    // on are prefix sums
+    constexpr int NG = (C + 63) / 64;
+    float dg[NG], behind[NG], x = 0.f, sum = 0.f, all = 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) x += s_dot[i];
-    const float sum = wave_inclusive_scan(ahead), behind = wave_inclusive_scan(before);
-    // writes in front of t: all of them less those from t on
-    const float all = lane_value(behind, 63);
-    const float dg = sum + (all - behind) + s_d.all * x;
-    if (p.dg_chunk) {
-      float s = t >= 0 && t < rows ? dg : 0.f;
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
-      if (lane == 0) p.dg_chunk[(size_t)h * p.slots + slot] = s;
-    } else if (t >= 0 && t < rows) {
-      ((E *)p.dg)[row0 + t] = Elem<E>::from_f32(dg);
+    for (int u = NG - 1; u >= 0; --u) {
+      const int t = min(C, 64 * u + 64) - 1 - lane;
+      float ahead = 0.f, before = 0.f;
+      if (t >= 64 * u) {
+        ahead = s_read[t];
+        before = s_write[t];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) ahead += s_row[i][t];
+      }
+      dg[u] = wave_inclusive_scan(ahead) + sum;
+      behind[u] = wave_inclusive_scan(before) + all;
+      sum = lane_value(dg[u], 63);
+      all = lane_value(behind[u], 63);
+    }
+    float part = 0.f;
+#pragma unroll
+    for (int u = 0; u < NG; ++u) {
+      const int t = min(C, 64 * u + 64) - 1 - lane;
+      // writes in front of t: all of them less those from t on
+      const float d = dg[u] + (all - behind[u]) + s_d.all * x;
+      if (t >= 64 * u && t < rows) {
+        if (p.dg_chunk) part += d;
+        else ((E *)p.dg)[row0 + t] = Elem<E>::from_f32(d);
+      }
+    }
+    if (p.dg_chunk) {
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) part += __shfl_xor(part, off);
+      if (lane == 0) p.dg_chunk[(size_t)h * p.slots + slot] = part;
     }
   }
 }
@@ -819,64 +893,84 @@ __global__ __launch_bounds__(256) void kla_la_step_kernel(LaStepParams p) {
   }
 }
 
-template <typename E, int DK, int MODE, bool REV>
+template <typename E, int DK, int MODE>
 hipError_t launch_scan_t(const LaParams &p, hipStream_t st) {
-  const long long pairs = ((long long)p.N * p.H * p.segs + 7) / 8 * 8;
-  hipLaunchKernelGGL((kla_la_scan_kernel<E, DK, MODE, REV>), dim3((unsigned)(pairs * p.slices)), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((kla_la_scan_kernel<E, DK, MODE>), dim3(MODE == LA_OUT ? p.half : 2 * p.half), dim3(la_threads(MODE)), 0,
+                     st, p);
   return hipGetLastError();
 }
-template <typename E, int MODE, bool REV>
+template <typename E, int MODE>
 hipError_t launch_scan(const LaParams &p, hipStream_t st) {
-  if (p.dk <= 64) return launch_scan_t<E, 64, MODE, REV>(p, st);
-  if (p.dk <= 128) return launch_scan_t<E, 128, MODE, REV>(p, st);
-  return launch_scan_t<E, 256, MODE, REV>(p, st);
+  if (p.dk <= 64) return launch_scan_t<E, 64, MODE>(p, st);
+  if (p.dk <= 128) return launch_scan_t<E, 128, MODE>(p, st);
+  return launch_scan_t<E, 256, MODE>(p, st);
 }
 
 int la_chunk(int dtype) { return dtype == 0 ? La<bf16>::C : La<float>::C; }
 
+// Chunks to a state of the backward: two where the gradients' workgroup can hold them.
+int la_group(const LaArgs &a) { return a.dtype == 0 && a.dk <= 128 ? 2 : 1; }
+
 int la_slots(const LaArgs &a) {
-  const int C = la_chunk(a.dtype);
+  const int C = la_chunk(a.dtype) * la_group(a);
   return a.cu_seqlens ? a.T / C + a.num_seqs : a.num_seqs * ((a.T + C - 1) / C);
 }
 
-// Segments of the scans.
+long long la_workgroups(const LaArgs &a, int segs) {
+  return ((long long)a.num_seqs * a.H * segs + 7) / 8 * 8 * ((a.dv + LA_NV - 1) / LA_NV);
+}
+
+// Segments of the scans, where their workgroups leave CUs idle: as many as make two rounds of
+// workgroups, each of 8 chunks at least.
 void la_segments(const LaArgs &a, int *segs, int *chunks) {
   const int C = la_chunk(a.dtype), nch = (a.longest + C - 1) / C;
+  const long long wgs = (long long)a.num_seqs * a.H * ((a.dv + LA_NV - 1) / LA_NV);
   *segs = 1;
   *chunks = std::max(nch, 1);
+  if (wgs > 128 || wgs == 0 || nch < 32) return;
+  const int want = (int)std::min<long long>({512 / wgs, nch / 8, 32});
+  *chunks = (nch + want - 1) / want;
+  *segs = (nch + *chunks - 1) / *chunks;
 }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// The workspace: the segments' states and decays; the backward's states and gradients of states
-// of all chunks, and the fixed decays' partial sums.
+// The workspace: the segments' states and decays (backward: of both directions); the backward's
+// states and gradients of states of all chunks, and the fixed decays' partial sums.
 struct LaSpace {
-  size_t seg_s, seg_g, states, dstates, dg, total;
+  size_t seg_s[2], seg_g[2], states[2], dg, total;
 };
 LaSpace la_space(const LaArgs &a, bool bwd) {
   int segs, chunks;
   la_segments(a, &segs, &chunks);
   const size_t pairs = (size_t)a.num_seqs * a.H * segs, state = (size_t)a.dk * a.dv;
   LaSpace s{};
-  s.seg_g = segs > 1 ? up(pairs * state * sizeof(float)) : 0;
-  s.states = s.seg_g + (segs > 1 ? up(pairs * sizeof(double)) : 0);
-  s.total = s.dstates = s.dg = s.states;
-  if (bwd) {
-    const size_t n = (size_t)la_slots(a) * a.H, e = a.dtype == 0 ? 2 : 4;
-    s.dstates = s.states + up(n * state * e);
-    s.dg = s.dstates + up(n * state * e);
-    s.total = s.dg + up(n * sizeof(float));
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t was = at;
+    at += up(n);
+    return was;
+  };
+  for (int i = 0; i <= (int)bwd; ++i) {
+    s.seg_s[i] = take(segs > 1 ? pairs * state * sizeof(float) : 0);
+    s.seg_g[i] = take(segs > 1 ? pairs * sizeof(double) : 0);
   }
+  if (bwd) {
+    const size_t n = (size_t)la_slots(a) * a.H;
+    for (int i = 0; i < 2; ++i) s.states[i] = take(n * state * (a.dtype == 0 ? 2 : 4));
+    s.dg = take(n * sizeof(float));
+  }
+  s.total = at;
   return s;
 }
 
-LaParams la_params(const LaArgs &a) {
+LaParams la_params(const LaArgs &a, const LaSpace &s) {
   LaParams p{};
+  char *const ws = (char *)a.workspace;
   p.q = a.q;
-  p.x = a.k;
-  p.y = a.v;
   p.g = a.g;
   p.gfix = a.gfix;
+  p.o = a.o;
   p.cu = a.cu_seqlens;
   p.N = a.num_seqs;
   p.H = a.H;
@@ -885,28 +979,51 @@ LaParams la_params(const LaArgs &a) {
   p.dv = a.dv;
   p.slices = (a.dv + LA_NV - 1) / LA_NV;
   la_segments(a, &p.segs, &p.seg_chunks);
-  p.slots = la_slots(a);
+  p.half = (unsigned)la_workgroups(a, p.segs);
+  p.group = 1;
+  for (int i = 0; i < 2; ++i) {
+    p.dir[i].seg_s = (float *)(ws + s.seg_s[i]);
+    p.dir[i].seg_g = (double *)(ws + s.seg_g[i]);
+    p.dir[i].states = ws + s.states[i];
+  }
+  p.dir[0].x = a.k;
+  p.dir[0].y = a.v;
+  p.dir[0].s0 = a.initial_state;
   return p;
+}
+
+// The segments' end states, of the forward direction or of both.
+template <typename E>
+hipError_t launch_ends(const LaParams &p, bool both, hipStream_t st) {
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(both ? 2 * p.half : p.half), dim3(la_threads(LA_ENDS)), 0, st, p);
+    return hipGetLastError();
+  };
+  if (p.dk <= 64) return go(kla_la_scan_kernel<E, 64, LA_ENDS>);
+  if (p.dk <= 128) return go(kla_la_scan_kernel<E, 128, LA_ENDS>);
+  return go(kla_la_scan_kernel<E, 256, LA_ENDS>);
 }
 
 template <typename E>
 hipError_t la_fwd_t(const LaArgs &a, hipStream_t st) {
-  LaParams p = la_params(a);
-  const LaSpace s = la_space(a, false);
-  p.s0 = a.initial_state;
-  p.o = a.o;
-  p.send = a.final_state;
-  p.seg_s = (float *)((char *)a.workspace + s.seg_s);
-  p.seg_g = (double *)((char *)a.workspace + s.seg_g);
+  LaParams p = la_params(a, la_space(a, false));
+  p.dir[0].send = a.final_state;
   if (p.segs > 1)
-    if (const hipError_t e = launch_scan<E, LA_ENDS, false>(p, st); e != hipSuccess) return e;
-  return launch_scan<E, LA_OUT, false>(p, st);
+    if (const hipError_t e = launch_ends<E>(p, false, st); e != hipSuccess) return e;
+  return launch_scan<E, LA_OUT>(p, st);
 }
 
-template <typename E, int DK>
+template <typename E, int DK, int C>
 hipError_t launch_grad_t(const LaGradParams &p, hipStream_t st) {
-  hipLaunchKernelGGL((kla_la_grad_kernel<E, DK>), dim3((unsigned)((long long)p.slots * p.H)), dim3(La<E>::C * 4), 0, st, p);
+  hipLaunchKernelGGL((kla_la_grad_kernel<E, DK, C>), dim3((unsigned)((long long)p.slots * p.H)), dim3(C * 4), 0, st, p);
   return hipGetLastError();
+}
+template <typename E>
+hipError_t launch_grad(const LaGradParams &p, hipStream_t st) {
+  constexpr bool B = sizeof(E) == 2;  // chunks: la_group
+  if (p.dk <= 64) return launch_grad_t<E, 64, B ? 128 : 32>(p, st);
+  if (p.dk <= 128) return launch_grad_t<E, 128, B ? 128 : 32>(p, st);
+  return launch_grad_t<E, 256, B ? 64 : 32>(p, st);
 }
 
 template <typename E>
@@ -917,21 +1034,16 @@ hipError_t la_bwd_t(const LaArgs &a, const LaGrads &b, hipStream_t st) {
     if (a.gfix) hipLaunchKernelGGL(kla_la_sum_kernel, dim3((unsigned)a.H), dim3(256), 0, st, nullptr, (float *)b.dg, 0);
     return hipGetLastError();
   }
-  LaParams p = la_params(a);
-  p.seg_s = (float *)(ws + s.seg_s);
-  p.seg_g = (double *)(ws + s.seg_g);
-  p.s0 = a.initial_state;
-  p.states = ws + s.states;
+  LaParams p = la_params(a, s);
+  p.group = la_group(a);
+  p.slots = la_slots(a);
+  p.dir[1].x = a.q;
+  p.dir[1].y = b.dout;
+  p.dir[1].s0 = b.dfinal_state;
+  p.dir[1].send = b.dinitial_state;
   hipError_t e;
-  if (p.segs > 1 && (e = launch_scan<E, LA_ENDS, false>(p, st)) != hipSuccess) return e;
-  if ((e = launch_scan<E, LA_STORE, false>(p, st)) != hipSuccess) return e;
-  p.x = a.q;
-  p.y = b.dout;
-  p.s0 = b.dfinal_state;
-  p.send = b.dinitial_state;
-  p.states = ws + s.dstates;
-  if (p.segs > 1 && (e = launch_scan<E, LA_ENDS, true>(p, st)) != hipSuccess) return e;
-  if ((e = launch_scan<E, LA_STORE, true>(p, st)) != hipSuccess) return e;
+  if (p.segs > 1 && (e = launch_ends<E>(p, true, st)) != hipSuccess) return e;
+  if ((e = launch_scan<E, LA_STORE>(p, st)) != hipSuccess) return e;
   LaGradParams gp{};
   gp.q = a.q;
   gp.k = a.k;
@@ -939,8 +1051,8 @@ hipError_t la_bwd_t(const LaArgs &a, const LaGrads &b, hipStream_t st) {
   gp.g = a.g;
   gp.gfix = a.gfix;
   gp.dout = b.dout;
-  gp.states = ws + s.states;
-  gp.dstates = ws + s.dstates;
+  gp.states = p.dir[0].states;
+  gp.dstates = p.dir[1].states;
   gp.dq = b.dq;
   gp.dk_ = b.dk;
   gp.dv_ = b.dv;
@@ -953,10 +1065,7 @@ hipError_t la_bwd_t(const LaArgs &a, const LaGrads &b, hipStream_t st) {
   gp.dk = a.dk;
   gp.dv = a.dv;
   gp.slots = p.slots;
-  if (gp.slots > 0) {
-    e = a.dk <= 64 ? launch_grad_t<E, 64>(gp, st) : a.dk <= 128 ? launch_grad_t<E, 128>(gp, st) : launch_grad_t<E, 256>(gp, st);
-    if (e != hipSuccess) return e;
-  }
+  if (gp.slots > 0 && (e = launch_grad<E>(gp, st)) != hipSuccess) return e;
   if (a.gfix) {
     hipLaunchKernelGGL(kla_la_sum_kernel, dim3((unsigned)a.H), dim3(256), 0, st, gp.dg_chunk, (float *)b.dg, gp.slots);
     return hipGetLastError();
@@ -985,7 +1094,7 @@ bool la_grid_fits(const LaArgs &a) {
   la_segments(a, &segs, &chunks);
   const int C = la_chunk(a.dtype);
   const double slots = a.cu_seqlens ? (double)a.T / C + a.num_seqs + 1 : (double)a.num_seqs * ((a.T + C - 1) / C);
-  return launch_fits(((double)a.num_seqs * a.H * segs + 8) * ((a.dv + LA_NV - 1) / LA_NV), 256) &&
+  return launch_fits(2.0 * ((double)a.num_seqs * a.H * segs + 8) * ((a.dv + LA_NV - 1) / LA_NV), 512) &&
          launch_fits(slots * a.H, 256);
 }
 

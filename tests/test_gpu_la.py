@@ -242,3 +242,46 @@ def test_the_same_bits_again():
     for _ in range(3):
         again = [*kla.la_chunk_fwd(*x[:4], x[5], cu, cu_seqlens_host=host), *kla.la_chunk_bwd(*x[:5], x[5], x[6], cu, cu_seqlens_host=host)]
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fixed", [False, True])
+def test_few_long_sequences(dtype, fixed):
+    """Sequences in segments that are scanned side by side, beside shorter ones and an empty one."""
+    lens = [2500, 0, 3, 1100, 700]
+    cu, host = packed(lens)
+    check(*make(1, 1, sum(lens), 64, 48, len(lens), dtype, fixed, rate=0.02, seed=11), cu, host)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_segments_over_the_initial_state(dtype):
+    q, k, v, g, _, s0, _ = make(1, 2, 4100, 32, 32, 1, dtype, rate=0.001, seed=12)
+    o, S = kla.la_chunk_fwd(q, k, v, g, s0)
+    for _ in range(3):
+        keep = s0.clone()
+        o2, S2 = kla.la_chunk_fwd(q, k, v, g, keep, final_state=keep)
+        assert torch.equal(S, S2) and torch.equal(o, o2)
+    wo, ws, eo, es = la_forward(f64(q), f64(k), f64(v), f64(g), f64(s0), None, U[dtype])
+    near(o, wo, eo, dtype)
+    near(S, ws, es, F32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_segments_of_other_lengths_on_the_device(dtype):
+    """A call cut for even sequences, replayed with one that is longer than any of them."""
+    T = 4000
+    host = torch.tensor([0, 2000, T], dtype=torch.int32)
+    q, k, v, g, do, s0, df = make(1, 1, T, 32, 32, 2, dtype, rate=0.02, seed=13)
+    for real in ([0, 100, 3900], [0, 3990, 4000]):
+        cu = torch.tensor(real, dtype=torch.int32, device=DEV)
+        o, S = kla.la_chunk_fwd(q, k, v, g, s0, cu, cu_seqlens_host=host)
+        grads = kla.la_chunk_bwd(q, k, v, g, do, s0, df, cu, cu_seqlens_host=host)
+        n = real[-1]
+        cut = [f64(x[:, :, :n]) for x in (q, k, v, g)]
+        wo, ws, eo, es = la_forward(*cut, f64(s0), real, U[dtype])
+        near(o[:, :, :n], wo, eo, dtype)
+        near(S, ws, es, F32)
+        want, err = la_backward(*cut, f64(do[:, :, :n]), f64(s0), f64(df), real, U[dtype])
+        for i in range(4):
+            near(grads[i][:, :, :n], want[i], err[i], dtype)
+        near(grads[4], want[4], err[4], F32)
