@@ -38,6 +38,7 @@ namespace kla {
 namespace {
 
 constexpr int LA_NV = 32;         // state columns of a scan workgroup
+constexpr int LA_AHEAD = 3;       // chunks that a scan's loads run ahead
 constexpr float LA_FORGET = -65536.f;  // log2 of the smallest decay
 
 // Chunks and operands by element type.  A 16-byte operand holds VL contraction values of a row
@@ -95,20 +96,23 @@ __device__ __forceinline__ double lane_double(double v, int src) {
   const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(u >> 32), src);
   return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
 }
-__device__ __forceinline__ double scan_double(double v) {
+// *rest: what the sum over the lane's row of 16 still adds behind it
+__device__ __forceinline__ double scan_double(double v, double *rest) {
   v += dpp_shr<0x111>(v);
   v += dpp_shr<0x112>(v);
   v += dpp_shr<0x114>(v);
   v += dpp_shr<0x118>(v);
-  const double r0 = lane_double(v, 15), r1 = lane_double(v, 31), r2 = lane_double(v, 47);
+  const double r0 = lane_double(v, 15), r1 = lane_double(v, 31), r2 = lane_double(v, 47), r3 = lane_double(v, 63);
   const int row = (threadIdx.x & 63) >> 4;
+  *rest = (row == 0 ? r0 : row == 1 ? r1 : row == 2 ? r2 : r3) - v;
   return v + ((row >= 1 ? r0 : 0.0) + (row >= 2 ? r1 : 0.0) + (row >= 3 ? r2 : 0.0));
 }
 
-// A chunk's decays: c_t in base two as hi + lo, exp(c_t), exp(tot - c_t), exp(tot), tot.
+// A chunk's decays: c_t in base two as hi + lo, exp(c_t), exp(tot - c_t), the decay from a token
+// to the last of its 16, exp(tot), tot.
 template <int C>
 struct Decays {
-  float hi[C], lo[C], out[C], left[C];
+  float hi[C], lo[C], out[C], left[C], near[C];
   float all;
   double tot;
 };
@@ -118,13 +122,13 @@ template <int C>
 __device__ __forceinline__ void scan_decays(Decays<C> *d, const float *g) {
   constexpr int N = (C + 63) / 64;
   const int lane = threadIdx.x & 63;
-  double c[N], tot = 0.0;
+  double c[N], rest[N], tot = 0.0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     double x = (double)g[i] * 1.4426950408889634;
     x = x < LA_FORGET ? LA_FORGET : x;  // a NaN stays
     if (64 * i + lane >= C) x = 0.0;
-    c[i] = scan_double(x) + tot;
+    c[i] = scan_double(x, &rest[i]) + tot;
     tot = lane_double(c[i], 63);
   }
 #pragma unroll
@@ -136,6 +140,7 @@ __device__ __forceinline__ void scan_decays(Decays<C> *d, const float *g) {
       d->lo[t] = (float)(c[i] - (double)hi);
       d->out[t] = __builtin_amdgcn_exp2f((float)c[i]);
       d->left[t] = __builtin_amdgcn_exp2f((float)(tot - c[i]));
+      d->near[t] = __builtin_amdgcn_exp2f((float)rest[i]);
     }
   }
   if (lane == 0) {
@@ -180,7 +185,7 @@ __device__ __forceinline__ void la_span(const int32_t *cu, int n, int T, int C, 
 
 // The scan over a sequence's chunks.  A workgroup holds LA_NV columns of the state.  Four waves
 // own the state, a quarter of its rows each, in fp32: they bring x and y to LDS a chunk ahead of
-// their use (from registers that hold the chunk after that), with y's scaled copy, update the
+// their use (from registers that hold the chunks after that), with y's scaled copy, update the
 // state, and leave a copy of it in the element type in LDS.  Beside them four waves compute the
 // outputs from those copies, 16 rows each (fp32, 32 tokens to a chunk: half of the columns);
 // the first, which has the fewest scores, also sums the decays of the chunk after next.  One
@@ -233,19 +238,32 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
   const int g = lane >> 4, li = lane & 15;
   const int col0 = slice * NV;
   auto first_token = [&](int j) { return (rev ? nch - 1 - j : j) * C; };
+  // loads ahead go past the last chunk as loads of it: under a condition the compiler would wait
+  // for them where they are issued
+  auto within = [&](int j) { return min(j, c1 - 1); };
 
   if (wave >= 4) {  // decays and outputs
     const int strip = (wave - 4) % NS, ct0 = (wave - 4) / NS * CT;
-    auto load_g = [&](int j) {  // the lane's log-decay
-      const int t = first_token(j) + lane;
-      if (lane >= C || t >= len) return 0.f;
-      return p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + t]);
+    if (c0 >= c1) return;
+    const float fixed = p.gfix ? p.gfix[h] : 0.f;
+    const E *const gp = p.gfix ? (const E *)p.q : (const E *)p.g + row0;
+    auto load_g = [&](int j) {  // the lane's log-decay as it stands in memory (0 past the end)
+      const int t = first_token(j);
+      const __amdgpu_buffer_rsrc_t r = buffer_rsrc(gp + t, p.gfix ? 0 : min(C, len - t) * (int)sizeof(E));
+      return (unsigned)buffer_ld_elem(r, lane, gp);
     };
-    Op q[MODE == LA_OUT ? KS : 1];
-    auto load_q = [&](int j) {
+    auto decay = [&](unsigned u, int j) {
+      asm volatile("" : "+v"(u));  // not where the load is issued, which would wait for it
+      if (p.gfix) return lane < len - first_token(j) ? fixed : 0.f;
+      if constexpr (sizeof(E) == 2) return elem_bits_to_f32((unsigned short)u);
+      else return elem_bits_to_f32(u);
+    };
+    typedef Op Query[MODE == LA_OUT ? KS : 1];
+    const E *const qp = (const E *)p.q + row0 * p.dk;
+    auto load_q = [&](Query &q, int j) {
       if constexpr (MODE == LA_OUT) {
         const int t = first_token(j), rows = min(C, len - t);
-        const __amdgpu_buffer_rsrc_t rq = buffer_rsrc((const E *)p.q + (row0 + t) * p.dk, rows * p.dk * (int)sizeof(E));
+        const __amdgpu_buffer_rsrc_t rq = buffer_rsrc(qp + (size_t)t * p.dk, rows * p.dk * (int)sizeof(E));
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const int c = k * KG + VL * g;
@@ -253,128 +271,162 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         }
       }
     };
-    float gn[2] = {0.f, 0.f};
-    if (c0 < c1) {
-      load_q(c0);
-      if (wave == 4) {
-        const float g0 = load_g(c0), g1 = c0 + 1 < c1 ? load_g(c0 + 1) : 0.f;
-        if (c0 + 2 < c1) gn[0] = load_g(c0 + 2);
-        if (c0 + 3 < c1) gn[1] = load_g(c0 + 3);
-        scan_decays<C>(&s_d[c0 % 3], &g0);
-        if (c0 + 1 < c1) scan_decays<C>(&s_d[(c0 + 1) % 3], &g1);
-      }
-      lds_barrier();
-    }
-    for (int j = c0; j < c1; ++j) {
-      lds_barrier();
-      if (wave == 4 && j + 2 < c1) {
-        scan_decays<C>(&s_d[(j + 2) % 3], &gn[0]);
-        gn[0] = gn[1];
-        if (j + 4 < c1) gn[1] = load_g(j + 4);
-      }
-      if constexpr (MODE == LA_OUT) {
-        const E *const X = s_x[j & 1], *const Y = s_y[j & 1], *const S = s_s[j & 1];
-        const Decays<C> &d = s_d[j % 3];
-        // P^T: keys 16 kt + 4 g + e against the strip's query li
-        f32x4 pt[NS];
-        const float th = d.hi[16 * strip + li], tl = d.lo[16 * strip + li];
+    unsigned gn[LA_AHEAD];
+    Query qs[LA_AHEAD];
+    const unsigned g0 = load_g(c0), g1 = load_g(within(c0 + 1));
 #pragma unroll
-        for (int kt = 0; kt < NS; ++kt) {
-          pt[kt] = zero4();
-          if (kt <= strip) {
+    for (int i = 0; i < LA_AHEAD; ++i) gn[i] = load_g(within(c0 + 2 + i));
+#pragma unroll
+    for (int i = 0; i < LA_AHEAD; ++i) load_q(qs[i], within(c0 + i));
+    if (wave == 4) {
+      float x = decay(g0, c0);
+      scan_decays<C>(&s_d[c0 % 3], &x);
+      x = decay(g1, within(c0 + 1));
+      scan_decays<C>(&s_d[(c0 + 1) % 3], &x);
+    }
+    lds_barrier();
+    // A strip's code is its own: its scores and their keys are as many as its number says, and in
+    // one run of instructions.
+    auto run = [&](auto which) {
+      constexpr int ST = decltype(which)::value;
+      auto step = [&](int j, Query &q, unsigned &gj) {  // gj: the decay of chunk j + 2
+        lds_barrier();
+        if (ST == 0 && wave == 4) {
+          const float x = decay(gj, within(j + 2));
+          gj = load_g(within(j + 2 + LA_AHEAD));
+          scan_decays<C>(&s_d[(j + 2) % 3], &x);  // behind the last chunk: nobody reads it
+        }
+        if constexpr (MODE == LA_OUT) {
+          const E *const X = s_x[j & 1], *const Y = s_y[j & 1], *const S = s_s[j & 1];
+          const Decays<C> &d = s_d[j % 3];
+          // P^T: keys 16 kt + 4 g + e against the strip's query li
+          f32x4 pt[NS];
+#pragma unroll
+          for (int kt = 0; kt < NS; ++kt) {
+            pt[kt] = zero4();
+            if (kt > ST) continue;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
               pt[kt] = Ops<E>::mma_grp(L::nat(X + (16 * kt + li) * LDX, k * KG, g), q[k], pt[kt]);
           }
-        }
-        f32x4 o[CT];  // o^T: columns 4 g + e of query li
-        const float f = d.out[16 * strip + li];
+          f32x4 o[CT];  // o^T: columns 4 g + e of query li
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          o[c] = zero4();
+          for (int c = 0; c < CT; ++c) {
+            o[c] = zero4();
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            o[c] = Ops<E>::mma_grp(L::nat(S + (16 * (ct0 + c) + li) * LDX, k * KG, g), q[k], o[c]);
-        }
-        if (j + 1 < c1) load_q(j + 1);
+            for (int k = 0; k < KS; ++k)
+              o[c] = Ops<E>::mma_grp(L::nat(S + (16 * (ct0 + c) + li) * LDX, k * KG, g), q[k], o[c]);
+          }
+          load_q(q, within(j + LA_AHEAD));
+          // earlier keys: the decay to the end of their 16, and from there
+          const float th = d.hi[16 * ST + li], tl = d.lo[16 * ST + li], f = d.out[16 * ST + li];
 #pragma unroll
-        for (int kt = 0; kt < NS; ++kt)
-          if (kt <= strip) {
-            const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * kt + 4 * g]);
-            const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * kt + 4 * g]);
+          for (int kt = 0; kt < ST; ++kt) {
+            const f32x4 near = *reinterpret_cast<const f32x4 *>(&d.near[16 * kt + 4 * g]);
+            const float far = __builtin_amdgcn_exp2f((th - d.hi[16 * kt + 15]) + (tl - d.lo[16 * kt + 15]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pt[kt][e] *= near[e] * far;
+          }
+          {
+            const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * ST + 4 * g]);
+            const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * ST + 4 * g]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              pt[kt][e] = kt < strip || 4 * g + e <= li
-                              ? pt[kt][e] * __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) : 0.f;
+              pt[ST][e] = 4 * g + e <= li ? pt[ST][e] * __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) : 0.f;
           }
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+          for (int c = 0; c < CT; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[c][e] *= f;
+            for (int e = 0; e < 4; ++e) o[c][e] *= f;
 #pragma unroll
-        for (int kb = 0; kb < C; kb += KG)
-          if (kb / 16 <= strip) {
+          for (int kb = 0; kb < C; kb += KG) {
+            if (kb / 16 > ST) continue;
             const Op w = Ops<E>::b_from_d(&pt[kb / 16]);
 #pragma unroll
             for (int c = 0; c < CT; ++c)
               o[c] = Ops<E>::mma_grp(L::tr(Y, LDY, kb, 16 * (ct0 + c), lane), w, o[c]);
           }
-        const int t = first_token(j) + 16 * strip + li;
-        if (t < len) {
+          const int t = first_token(j) + 16 * ST + li;
+          if (t < len) {
 #pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const int col = col0 + 16 * (ct0 + c) + 4 * g;
-            if (col < p.dv) store4((E *)p.o + (row0 + t) * p.dv + col, o[c]);
+            for (int c = 0; c < CT; ++c) {
+              const int col = col0 + 16 * (ct0 + c) + 4 * g;
+              if (col < p.dv) store4((E *)p.o + (row0 + t) * p.dv + col, o[c]);
+            }
           }
         }
+      };
+      int j = c0;
+      for (; j + LA_AHEAD <= c1; j += LA_AHEAD) {
+#pragma unroll
+        for (int i = 0; i < LA_AHEAD; ++i) step(j + i, qs[i], gn[i]);
       }
+#pragma unroll
+      for (int i = 0; i < LA_AHEAD - 1; ++i)
+        if (j + i < c1) step(j + i, qs[i], gn[i]);
+    };
+    if (strip == 0) run(std::integral_constant<int, 0>{});
+    else if (strip == 1) run(std::integral_constant<int, 1>{});
+    if constexpr (NS > 2) {
+      if (strip == 2) run(std::integral_constant<int, 2>{});
+      else if (strip == 3) run(std::integral_constant<int, 3>{});
     }
     return;
   }
 
   // the state
   const int tid = threadIdx.x;
-  uint4 xr[XP], yr[YP];
-  auto load = [&](int j) {
+  struct Rows {
+    u32x4 x[XP], y[YP];
+  } ahead[LA_AHEAD];
+  const E *const xp = (const E *)(rev ? p.dir[1].x : p.dir[0].x) + row0 * p.dk;
+  const E *const yp = (const E *)(rev ? p.dir[1].y : p.dir[0].y) + row0 * p.dv;
+  auto load = [&](Rows &to, int j) {
     const int t = first_token(j), rows = min(C, len - t);
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc((const E *)dir.x + (row0 + t) * p.dk, rows * p.dk * (int)sizeof(E));
-    const __amdgpu_buffer_rsrc_t ry = buffer_rsrc((const E *)dir.y + (row0 + t) * p.dv, rows * p.dv * (int)sizeof(E));
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(xp + (size_t)t * p.dk, rows * p.dk * (int)sizeof(E));
+    const __amdgpu_buffer_rsrc_t ry = buffer_rsrc(yp + (size_t)t * p.dv, rows * p.dv * (int)sizeof(E));
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
       const int pc = tid + 256 * i, r = pc / (DK / VL), c = pc % (DK / VL) * VL;
-      xr[i] = buffer_ld16(rx, c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000);
+      to.x[i] = __builtin_bit_cast(u32x4, buffer_ld16(rx, c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000));
     }
 #pragma unroll
     for (int i = 0; i < YP; ++i) {
       const int pc = tid + 256 * i, r = pc / (NV / VL), c = col0 + pc % (NV / VL) * VL;
-      yr[i] = buffer_ld16(ry, c < p.dv ? (r * p.dv + c) * (int)sizeof(E) : 0x40000000);
+      to.y[i] = __builtin_bit_cast(u32x4, buffer_ld16(ry, c < p.dv ? (r * p.dv + c) * (int)sizeof(E) : 0x40000000));
     }
   };
-  auto put = [&](int j) {  // chunk j's rows from registers
-    E *const dx = s_x[j & 1];
+  typedef float Scale[YP];
+  auto scales = [&](int j, Scale &f) {  // y's, of chunk j
     const Decays<C> &d = s_d[j % 3];
-    const float *const fs = rev ? d.out : d.left;
+#pragma unroll
+    for (int i = 0; i < YP; ++i) f[i] = (rev ? d.out : d.left)[(tid + 256 * i) / (NV / VL)];
+  };
+  auto put = [&](const Rows &from, int j, const Scale &f) {  // chunk j's rows from registers
+    E *const dx = s_x[j & 1];
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
       const int pc = tid + 256 * i;
-      *reinterpret_cast<uint4 *>(dx + pc / (DK / VL) * LDX + pc % (DK / VL) * VL) = xr[i];
+      *reinterpret_cast<u32x4 *>(dx + pc / (DK / VL) * LDX + pc % (DK / VL) * VL) = from.x[i];
     }
 #pragma unroll
     for (int i = 0; i < YP; ++i) {
       const int pc = tid + 256 * i, r = pc / (NV / VL), at = r * LDY + pc % (NV / VL) * VL;
-      const float f = fs[r];
       E e[VL], w[L::TERMS][VL];
-      __builtin_memcpy(e, &yr[i], 16);
+      u32x4 y = from.y[i];
+      // taken apart here: the compiler would do so, and wait for the load, where it is issued
+      asm volatile("" : "+v"(y));
+      __builtin_memcpy(e, &y, 16);
+      if constexpr (MODE == LA_OUT) *reinterpret_cast<u32x4 *>(s_y[j & 1] + at) = y;
 #pragma unroll
       for (int u = 0; u < VL; ++u) {
-        float v = Elem<E>::to_f32(e[u]) * f;
+        float v = Elem<E>::to_f32(e[u]) * f[i];
 #pragma unroll
         for (int k = 0; k < L::TERMS; ++k) {
           w[k][u] = Elem<E>::from_f32(v);
           v -= Elem<E>::to_f32(w[k][u]);
         }
       }
-      if constexpr (MODE == LA_OUT) *reinterpret_cast<uint4 *>(s_y[j & 1] + at) = yr[i];
 #pragma unroll
       for (int k = 0; k < L::TERMS; ++k) {
         uint4 v;
@@ -402,7 +454,10 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         }
   };
   const size_t ssize = (size_t)p.dk * p.dv;
-  if (c0 < c1) load(c0);
+  if (c0 < c1) {
+#pragma unroll
+    for (int i = 0; i < LA_AHEAD; ++i) load(ahead[i], within(c0 + i));
+  }
   if (seg == 0) {
     const bool copied = MODE != LA_ENDS && p.segs > 1 && c1 < nch;
     const float *s0 = dir.s0 ? (copied ? dir.seg_s + (nh * p.segs + p.segs - 1) * ssize : dir.s0 + nh * ssize) : nullptr;
@@ -443,19 +498,35 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
   double total = 0.0;
   if (c0 < c1) {
     lds_barrier();
-    put(c0);
+    Scale f;
+    scales(c0, f);
+    put(ahead[0], c0, f);
     publish(c0);
-    if (c0 + 1 < c1) load(c0 + 1);
+    load(ahead[0], within(c0 + LA_AHEAD));
   }
 
-  for (int j = c0; j < c1; ++j) {
+  auto step = [&](int j, Rows &next) {  // next: chunk j + 1's rows
     lds_barrier();
-    if (j + 1 < c1) put(j + 1);
-    if (j + 2 < c1) load(j + 2);
+    // all that is read from LDS first: its operations stay in order
     const E *const X = s_x[j & 1];
     const Decays<C> &d = s_d[j % 3];
-    if (MODE == LA_ENDS) total += d.tot;
     const float f = d.all;
+    Scale fs;
+    scales(within(j + 1), fs);
+    Op w[L::TERMS][NC], a[RT];
+    auto operands = [&](int kb) {
+#pragma unroll
+      for (int k = 0; k < L::TERMS; ++k)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) w[k][c] = L::tr(s_w[j & 1][k], LDY, kb, 16 * c, lane);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) a[i] = L::tr(X, LDX, kb, 16 * (wave * RT + i), lane);
+    };
+    operands(0);
+    if (MODE == LA_ENDS) total += d.tot;
+    __builtin_amdgcn_sched_barrier(0);
+    put(next, j + 1, fs);  // behind the last chunk: into a buffer that nobody reads
+    load(next, within(j + 1 + LA_AHEAD));
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -464,22 +535,24 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         for (int e = 0; e < 4; ++e) acc[i][c][e] *= f;
 #pragma unroll
     for (int kb = 0; kb < C; kb += KG) {
-      Op w[L::TERMS][NC];
+      if (kb) operands(kb);
 #pragma unroll
       for (int k = 0; k < L::TERMS; ++k)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) w[k][c] = L::tr(s_w[j & 1][k], LDY, kb, 16 * c, lane);
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const Op a = L::tr(X, LDX, kb, 16 * (wave * RT + i), lane);
-#pragma unroll
-        for (int k = 0; k < L::TERMS; ++k)
-#pragma unroll
-          for (int c = 0; c < NC; ++c) acc[i][c] = Ops<E>::mma_grp(a, w[k][c], acc[i][c]);
-      }
+          for (int c = 0; c < NC; ++c) acc[i][c] = Ops<E>::mma_grp(a[i], w[k][c], acc[i][c]);
     }
     if (j + 1 < c1) publish(j + 1);
+  };
+  int j = c0;
+  for (; j + LA_AHEAD <= c1; j += LA_AHEAD) {
+#pragma unroll
+    for (int i = 0; i < LA_AHEAD; ++i) step(j + i, ahead[(i + 1) % LA_AHEAD]);
   }
+#pragma unroll
+  for (int i = 0; i < LA_AHEAD - 1; ++i)
+    if (j + i < c1) step(j + i, ahead[(i + 1) % LA_AHEAD]);
   if constexpr (MODE == LA_ENDS) {
     float *const to = dir.seg_s + (nh * p.segs + seg) * ssize;
     each([&](float a, size_t at) { return to[at] = a; });
