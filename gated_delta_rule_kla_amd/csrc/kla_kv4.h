@@ -44,6 +44,8 @@ __device__ __forceinline__ void ld8(const E *p, float *f) {
     for (int j = 0; j < PER; ++j) f[i + j] = Elem<E>::to_f32(e[j]);
   }
 }
+constexpr int KV_MAX_PER = 8192;  // tokens of a run whose pages are kept in LDS
+
 typedef bf16 bf16x8v __attribute__((ext_vector_type(8)));
 
 // eight channels in a dword as four bf16 pairs

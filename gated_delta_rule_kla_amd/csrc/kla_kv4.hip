@@ -196,8 +196,6 @@ struct KvDecodeParams {
   float *part_o, *part_ml;  // [N Hq, splits, D], [N Hq, splits, 2] where splits > 1
 };
 
-constexpr int KV_MAX_PER = 8192;  // tokens of a run
-
 template <typename E, int D, bool ONCE>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void kla_kv4_decode_kernel(KvDecodeParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;  // bf16 terms of q and P

@@ -146,17 +146,16 @@ __device__ void attend_row(const KvChunkParams &p, const E *q, int n, int head, 
   *l_ = l;
 }
 
-// KS groups of NW / KS waves share the rows and take every KS-th part of BN keys of a tile.
-template <typename E, int D, int NW, int KS, int BN>
+// Tiles of BN keys, 32 rows to a wave.
+template <typename E, int D, int NW, int BN>
 __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;           // bf16 terms of q and of the weights
-  constexpr int BM = 32 * NW / KS, KT = KS * BN, KB = BN / 32;
+  constexpr int BM = 32 * NW, KB = BN / 32;
   constexpr int KJ = D / 16, DB = D / 32, PPR = D / 8, PPK = D / 32;  // PPK: blocks of 32 channels
-  constexpr int NP = 2 * KT * PPK / (64 * NW);         // blocks of a thread, keys before values
-  constexpr int NBUF = KT * D * 8 <= 65536 ? 2 : 1;
-  static_assert(NP * 64 * NW == 2 * KT * PPK, "blocks");
-  __shared__ __attribute__((aligned(1024))) bf16 s_kv[2][NBUF][KT * D];
-  __shared__ int s_none[NBUF][KT / 16];                // 16 keys of a missing page
+  constexpr int NP = 2 * BN * PPK / (64 * NW);         // blocks of a thread, keys before values
+  static_assert(NP * 64 * NW == 2 * BN * PPK, "blocks");
+  __shared__ __attribute__((aligned(1024))) bf16 s_kv[2][2][BN * D];
+  __shared__ int s_none[2][BN / 16];                // 16 keys of a missing page
 
   unsigned id = blockIdx.x;
   const int head = id % p.kv.Hkv;
@@ -165,12 +164,12 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   RowTile rt;
   if (!row_tile<BM>(p.cu, p.N, p.T, p.G, slot, &rt)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 31, h = lane >> 5, group = KS == 1 ? 0 : wave / (NW / KS);
+  const int r = lane & 31, h = lane >> 5;
   const int n = rt.n, lq = (int)(rt.rows / p.G);
   const int len = max(p.lens[n], 0), off = len - lq;
   const int lo = split * p.per, hi = (int)min((long long)readable(p.kv, len, p.max_len), (long long)lo + p.per);
   // the row of this lane (past the end: the last one) and the last key that it sees
-  const int w0 = rt.first + 32 * (wave % (NW / KS));
+  const int w0 = rt.first + 32 * wave;
   auto last_seen = [&](long long row) { return min((int)(min(row, rt.rows - 1) / p.G) + off, hi - 1); };
   const long long mine = w0 + r;
   const int row = (int)min(mine, rt.rows - 1), ti = row / p.G;
@@ -185,7 +184,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
     for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  const int steps = end > lo ? (end - lo + KT - 1) / KT : 0;
+  const int steps = end > lo ? (end - lo + BN - 1) / BN : 0;
   // codes and scales of a tile as they are loaded; pages a tile ahead of them
   u32x4 code[NP];
   unsigned scale[NP];
@@ -193,14 +192,14 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   auto find = [&](int t) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int pos = lo + t * KT + (tid + 64 * NW * i) % (KT * PPK) / PPK;
+      const int pos = lo + t * BN + (tid + 64 * NW * i) % (BN * PPK) / PPK;
       page[i] = pos < end ? p.kv.table[(size_t)n * p.kv.max_pages + pos / p.kv.page] : -1;
     }
   };
   auto load = [&](int t) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int pc = tid + 64 * NW * i, j = pc / (KT * PPK), b = pc % PPK, pos = lo + t * KT + pc % (KT * PPK) / PPK;
+      const int pc = tid + 64 * NW * i, j = pc / (BN * PPK), b = pc % PPK, pos = lo + t * BN + pc % (BN * PPK) / PPK;
       const bool there = page[i] >= 0 && page[i] < p.kv.num_pages;
       code[i] = u32x4{0, 0, 0, 0};
       scale[i] = 127;
@@ -216,7 +215,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   auto put = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int pc = tid + 64 * NW * i, j = pc / (KT * PPK), key = pc % (KT * PPK) / PPK, b = pc % PPK;
+      const int pc = tid + 64 * NW * i, j = pc / (BN * PPK), key = pc % (BN * PPK) / PPK, b = pc % PPK;
       const int swz = j ? (key & 3) << 2 & (PPR - 1) : key & (PPR - 1);
       const float s = __builtin_bit_cast(float, (scale[i] & 255) << 23);
       bf16 *const to = s_kv[j][buf] + key * D;
@@ -238,27 +237,20 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   bf16x8 q[KJ][NT];
 #pragma unroll
   for (int j = 0; j < KJ; ++j) q_terms<E, NT>((const E *)p.q + qrow * D + 16 * j + 8 * h, p.sign, q[j]);
-  if (NBUF == 2 && steps > 0) {
+  if (steps > 0) {
     put(0);
     if (steps > 1) load(1);
     if (steps > 2) find(2);
   }
   for (int t = 0; t < steps; ++t) {
-    const int buf = NBUF == 2 ? t & 1 : 0;
+    const int buf = t & 1;
     lds_barrier();
-    if constexpr (NBUF == 2) {
-      if (t + 1 < steps) put(buf ^ 1);
-      if (t + 2 < steps) load(t + 2);
-      if (t + 3 < steps) find(t + 3);
-    } else {
-      put(0);
-      if (t + 1 < steps) load(t + 1);
-      if (t + 2 < steps) find(t + 2);
-      lds_barrier();
-    }
-    const int key0 = lo + t * KT + group * BN;
+    if (t + 1 < steps) put(buf ^ 1);
+    if (t + 2 < steps) load(t + 2);
+    if (t + 3 < steps) find(t + 3);
+    const int key0 = lo + t * BN;
     if (key0 > wlast || w0 >= rt.rows) continue;
-    const bf16 *const kt = s_kv[0][buf] + group * BN * D, *const vt = s_kv[1][buf] + group * BN * D;
+    const bf16 *const kt = s_kv[0][buf], *const vt = s_kv[1][buf];
     f32x16 x[KB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
@@ -272,9 +264,9 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
 #pragma unroll
         for (int u = NT - 1; u >= 0; --u) x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[j][u], x[kb], 0, 0, 0);
       }
-    int none = 0;  // bit i: keys 16 i .. 16 i + 15 of the part are missing
+    int none = 0;  // bit i: keys 16 i .. 16 i + 15 of the tile are missing
 #pragma unroll
-    for (int i = 0; i < 2 * KB; ++i) none |= s_none[buf][group * 2 * KB + i] << i;
+    for (int i = 0; i < 2 * KB; ++i) none |= s_none[buf][i] << i;
     if (key0 + BN - 1 > wfirst || none) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
@@ -331,37 +323,6 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
     }
   }
   l += __shfl_xor(l, 32);
-  if constexpr (KS > 1) {
-    // the other groups' results through LDS, lane to lane: the layouts are the same
-    constexpr int WG = NW / KS, SIZE = (4 * DB + 1) * 64;  // waves of a group, f32x4 of a wave
-    static_assert((KS - 1) * WG * SIZE * 16 <= 4 * NBUF * KT * D, "exchange");
-    f32x4 *const ex = reinterpret_cast<f32x4 *>(s_kv) + lane;
-    __syncthreads();
-    if (group > 0) {
-      f32x4 *const to = ex + (wave - WG) * SIZE;
-#pragma unroll
-      for (int j = 0; j < DB; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[(4 * j + i) * 64] = f32x4{acc[j][4 * i], acc[j][4 * i + 1], acc[j][4 * i + 2], acc[j][4 * i + 3]};
-      to[4 * DB * 64] = f32x4{m, l, 0.f, 0.f};
-    }
-    __syncthreads();
-    if (group > 0) return;
-#pragma unroll
-    for (int g = 1; g < KS; ++g) {
-      const f32x4 *const from = ex + (wave + (g - 1) * WG) * SIZE;
-      const f32x4 ml = from[4 * DB * 64];
-      const float mn = fmaxf(m, ml[0]), base = mn == -INFINITY ? 0.f : mn;
-      const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(ml[0] - base);
-      m = mn;
-      l = l * f0 + ml[1] * f1;
-#pragma unroll
-      for (int j = 0; j < DB; ++j)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[j][i] = acc[j][i] * f0 + from[(4 * j + i / 4) * 64][i % 4] * f1;
-    }
-  }
-
   // Results: lane (r, h) holds row w0 + r, channels 32 j + 8 (i / 4) + 4 h + i % 4.  A value that
   // is not finite, times the zero weight of a row that does not see it, is NaN in the matrix
   // product: rows whose results are not finite are computed again from the keys they see, one by one.
@@ -423,6 +384,287 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   }
 }
 
+// Few rows (a draft's tokens, single tokens): 16 RB rows of a sequence and key head to a
+// workgroup, and a run of keys, of which its four waves take tiles of 32 in turn, each with its
+// own running maximum, sum and output; nothing is shared until the end.  Layouts are those of
+// the single-token kernel (kla_kv4.hip): K's codes become operands as they arrive, lane (r, c)
+// holding channels c D/4 and up of key r; the scores have keys 4 c + i of the two 16-key halves
+// in a lane's registers and rows along the lanes, and so are the second product's operand as
+// they stand; V goes through the wave's own LDS in 4 bits.  Bound: HBM, and the conversions, which all row blocks share.
+template <typename E, int D, int RB, bool ONCE>
+__global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
+  constexpr int NT = sizeof(E) == 2 ? 1 : 3;  // bf16 terms of q and of the weights
+  constexpr int KJ = D / 32, DW = D / 16, BM = 16 * RB;
+  __shared__ int s_page[KV_MAX_PER / 16];
+  __shared__ float s_o[4][16][D + 4];
+  __shared__ float s_ml[4][16][2];
+  __shared__ __attribute__((aligned(16))) uint8_t s_v[4][32 * D / 2];
+  __shared__ unsigned s_sc[4][64];
+  __shared__ int s_bad;
+
+  unsigned id = blockIdx.x;
+  const int head = id % p.kv.Hkv;
+  id /= p.kv.Hkv;
+  const int slot = id % p.slots, split = id / p.slots;
+  RowTile rt;
+  if (!row_tile<BM>(p.cu, p.N, p.T, p.G, slot, &rt)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, c = lane >> 4, n = rt.n, lq = (int)(rt.rows / p.G);
+  const int len = max(p.lens[n], 0), off = len - lq;
+  const int lo = split * p.per, hi = (int)min((long long)readable(p.kv, len, p.max_len), (long long)lo + p.per);
+  auto last_seen = [&](long long row) { return min((int)(min(row, rt.rows - 1) / p.G) + off, hi - 1); };
+  auto q_row = [&](long long row) {
+    const int ti = (int)(row / p.G);
+    return ((size_t)rt.b * p.Hq + head * p.G + (int)(row % p.G)) * p.T + rt.t0 + ti;
+  };
+  const int gn = (int)min((long long)BM, rt.rows - rt.first);       // rows of the tile
+  const int end = last_seen(rt.first + BM - 1) + 1, all = last_seen(rt.first);  // keys of the tile, of its first row
+  if (tid == 0) s_bad = 0;
+  for (int i = tid; i < (max(end - lo, 0) + 31) / 32 * 2; i += 256) {
+    const int t = lo + 16 * i;
+    int page = -1;
+    if (t < end) {
+      page = p.kv.table[(size_t)n * p.kv.max_pages + t / p.kv.page];
+      if (page >= p.kv.num_pages) page = -1;
+    }
+    s_page[i] = page;
+  }
+  bf16x8 q[RB][KJ][NT];
+  int lim[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const long long row = min(rt.first + 16 * b + (long long)r, rt.rows - 1);
+    lim[b] = last_seen(row);
+    const E *const qp = (const E *)p.q + q_row(row) * D;
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) q_terms<E, NT>(qp + c * (D / 4) + 8 * j, p.sign, q[b][j]);
+  }
+  __syncthreads();
+
+  f32x4 acc[RB][DW];
+  float m[RB], l[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    m[b] = -INFINITY;
+    l[b] = 0.f;
+#pragma unroll
+    for (int j = 0; j < DW; ++j) acc[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  constexpr int VP = D / 64, LPR = D / 32;  // pieces of V a lane loads, lanes of a row of V
+  struct Tile {
+    unsigned k[2][KJ];
+    u32x4 v[VP];
+    unsigned sc;
+    int id0, id1;
+  } next;
+  auto load = [&](Tile &x, int t) {
+    x.id0 = __builtin_amdgcn_readfirstlane(s_page[(t - lo) >> 4]);
+    x.id1 = __builtin_amdgcn_readfirstlane(s_page[((t - lo) >> 4) + 1]);
+    const size_t pg = (size_t)p.kv.Hkv * p.kv.page;
+    // rows of the two 16-token blocks (page 0 where there is none: masked below)
+    const size_t r0 = (size_t)max(x.id0, 0) * 2 * pg + (size_t)head * p.kv.page + t % p.kv.page;
+    const size_t r1 = (size_t)max(x.id1, 0) * 2 * pg + (size_t)head * p.kv.page + (t + 16) % p.kv.page;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t *a = p.kv.codes + ((h ? r1 : r0) + r) * (D / 2) + c * (D / 8);
+      if constexpr (D == 128) {
+        const u32x4 u = ld16<ONCE>(a);
+        x.k[h][0] = u[0], x.k[h][1] = u[1], x.k[h][2] = u[2], x.k[h][3] = u[3];
+      } else {
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 u = *reinterpret_cast<const u32x2 *>(a);
+        x.k[h][0] = u[0], x.k[h][1] = u[1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      const int key = lane / LPR + 64 / LPR * i;
+      x.v[i] = ld16<ONCE>(p.kv.codes + ((key < 16 ? r0 : r1) + pg + key % 16) * (D / 2) + 16 * (lane % LPR));
+    }
+    const uint8_t *a = p.kv.scales + ((lane & 16 ? r1 : r0) + (lane & 15) + (lane & 32 ? pg : 0)) * (D / 32);
+    if constexpr (D == 128) x.sc = *reinterpret_cast<const unsigned *>(a);
+    else x.sc = *reinterpret_cast<const unsigned short *>(a);
+  };
+
+  int t = lo + 32 * wave;
+  if (t < end) load(next, t);
+  for (; t < end; t += 128) {
+    const Tile x0 = next;
+    if (t + 128 < end) load(next, t + 128);
+    // V and the scales through the wave's own LDS; key 16 h + 4 c + e at slot 16 h + 4 e + c
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      const int key = lane / LPR + 64 / LPR * i, slot_ = (key & 16) + 4 * (key & 3) + ((key >> 2) & 3);
+      *reinterpret_cast<u32x4 *>(s_v[wave] + slot_ * (D / 2) + 16 * (lane % LPR)) = x0.v[i];
+    }
+    s_sc[wave][lane] = x0.sc;
+    const uint8_t *sc8 = reinterpret_cast<const uint8_t *>(s_sc[wave]);
+    const int id0 = x0.id0, id1 = x0.id1;
+    // scores of keys t + 16 h + 4 c + i against rows 16 b + r
+    float x[RB][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f32x4 s[RB];
+#pragma unroll
+      for (int b = 0; b < RB; ++b) s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const float sc = __builtin_bit_cast(float, (unsigned)sc8[4 * (16 * h + r) + (D == 128 ? c : c / 2)] << 23);
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) {
+        unsigned w[4];
+        cvt8(x0.k[h][j], sc, w);
+        bf16x8 a;
+        __builtin_memcpy(&a, w, 16);
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int u = 0; u < NT; ++u) s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[b][j][u], s[b], 0, 0, 0);
+      }
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[b][4 * h + i] = s[b][i] * p.c;
+    }
+    unsigned va[8];
+    float vf[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint8_t *a = s_v[wave] + ((e & 4) * 4 + 4 * (e & 3) + c) * (D / 2);
+      unsigned short half;
+      if constexpr (D == 128) __builtin_memcpy(&va[e], __builtin_assume_aligned(a + 4 * r, 4), 4);
+      else __builtin_memcpy(&half, __builtin_assume_aligned(a + 2 * r, 2), 2), va[e] = half;
+      vf[e] = __builtin_bit_cast(float, (unsigned)sc8[4 * (32 + 16 * (e >> 2) + 4 * c + (e & 3)) + r * DW / 32] << 23);
+    }
+    if (id0 < 0 || id1 < 0 || t + 31 > all) {
+      // keys that a row does not see have no score; those of no row, and of missing pages, a value
+      // of zero whatever the memory behind them holds
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int key = t + 16 * (e >> 2) + 4 * c + (e & 3);
+        const bool none = (e < 4 ? id0 : id1) < 0 || key >= end;
+#pragma unroll
+        for (int b = 0; b < RB; ++b) x[b][e] = none || key > lim[b] ? -INFINITY : x[b][e];
+        va[e] = none ? 0u : va[e];
+        vf[e] = none ? 1.f : vf[e];
+      }
+    }
+    bf16x8 pt[RB][NT];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      float top = x[b][0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, x[b][e]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      // the maximum moves by 2^LAG at least, as in kla_attn_tile.h
+      if (__any(top > m[b] + LAG)) {
+        const float mn = top > m[b] + LAG ? top : m[b];
+        const float al = __builtin_amdgcn_exp2f(m[b] - (mn == -INFINITY ? 0.f : mn));
+        l[b] *= al;
+#pragma unroll
+        for (int j = 0; j < DW; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[b][j][i] *= al;
+        m[b] = mn;
+      }
+      const float base = m[b] == -INFINITY ? 0.f : m[b];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float v = __builtin_amdgcn_exp2f(x[b][e] - base);
+        l[b] += v;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          pt[b][u][e] = (bf16)v;
+          v -= (float)pt[b][u][e];
+        }
+      }
+    }
+    // V: pairs of channels of each key, then pairs of keys of each channel
+    unsigned w[8][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cvt8(va[e], vf[e], w[e]);
+#pragma unroll
+    for (int j = 0; j < DW; ++j) {
+      unsigned a[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        a[e] = __builtin_amdgcn_perm(w[2 * e + 1][j / 2], w[2 * e][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+      bf16x8 av;
+      __builtin_memcpy(&av, a, 16);
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) acc[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, pt[b][u], acc[b][j], 0, 0, 0);
+    }
+  }
+
+  // join the waves, 16 rows at a time
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    l[b] += __shfl_xor(l[b], 16);
+    l[b] += __shfl_xor(l[b], 32);
+    if (b) __syncthreads();
+    if (c == 0) {
+      s_ml[wave][r][0] = m[b];
+      s_ml[wave][r][1] = l[b];
+    }
+#pragma unroll
+    for (int j = 0; j < DW; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_o[wave][r][(4 * c + i) * DW + j] = acc[b][j][i];
+    __syncthreads();
+    for (int i = tid; i < min(gn - 16 * b, 16) * D; i += 256) {
+      const int g = i / D, d = i % D;
+      float mm = s_ml[0][g][0];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) mm = fmaxf(mm, s_ml[w][g][0]);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f, oo = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(s_ml[w][g][0] - base);
+        ll = fmaf(s_ml[w][g][1], f, ll);
+        oo = fmaf(s_o[w][g][d], f, oo);
+      }
+      if (!(fabsf(fmaf(oo, 0.f, ll)) < INFINITY)) atomicOr(&s_bad, 1 << (16 * b + g));
+      const size_t qr = q_row(rt.first + 16 * b + g), part = qr * p.splits + split;
+      if (p.splits == 1) {
+        ((E *)p.o)[qr * D + d] = Elem<E>::from_f32(ll == 0.f ? 0.f : oo / ll);
+        if (d == 0 && p.lse) p.lse[qr] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.693147181f;
+      } else {
+        p.part_o[part * D + d] = oo;
+        if (d == 0) {
+          p.part_ml[part * 2] = mm;
+          p.part_ml[part * 2 + 1] = ll;
+        }
+      }
+    }
+  }
+  // rows whose results are not finite, again from the keys that they see alone, one by one
+  __syncthreads();
+  int bad = __builtin_amdgcn_readfirstlane(s_bad);
+  for (int i = 0; bad; ++i, bad &= bad - 1) {
+    if (i % 4 != wave) continue;
+    const long long row = rt.first + __builtin_ctz(bad);
+    const size_t qr = q_row(row), part = qr * p.splits + split;
+    constexpr int CPL = D / 64;
+    float rm, rl, a[CPL];
+    attend_row<E, D>(p, (const E *)p.q + qr * D, n, head, lo, last_seen(row) + 1, &rm, &rl, a);
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+      if (p.splits > 1) p.part_o[part * D + CPL * lane + k] = a[k];
+      else ((E *)p.o)[qr * D + CPL * lane + k] = Elem<E>::from_f32(rl == 0.f ? 0.f : a[k] / rl);
+    }
+    if (lane == 0) {
+      if (p.splits > 1) {
+        p.part_ml[part * 2] = rm;
+        p.part_ml[part * 2 + 1] = rl;
+      } else if (p.lse) {
+        p.lse[qr] = rl == 0.f ? -INFINITY : (rm + __builtin_amdgcn_logf(rl)) * 0.693147181f;
+      }
+    }
+  }
+}
+
 // The runs of one query: D / 4 lanes to a row.
 template <typename E, int D>
 __global__ __launch_bounds__(256) void kla_kv4_chunk_join_kernel(KvChunkParams p) {
@@ -454,45 +696,58 @@ __global__ __launch_bounds__(256) void kla_kv4_chunk_join_kernel(KvChunkParams p
 
 // ---- the weight that queries give to cached tokens -------------------------------------------------
 //
-// w_j += sum over the rows that see key j of exp(scale q . k_j - lse).  Each wave owns KPW keys, their
-// channels as left operands in registers (lane (r, h): channels h D/2 and up of key r, eight to a
-// product, q's taken in the same order), and goes over the rows 32 at a time: one product, one
-// exponential and an addition a score, the sums in registers with rows along the lanes until the
-// end.  A key's sum is made by one wave in one order.
+// w_j += sum over the rows that see key j of exp(scale q . k_j - lse).  One product, one
+// exponential and an addition a score; a key's sum is made by one workgroup in one order.
 struct KvWeighParams {
   KvParams kv;
   const void *q;
   const float *lse;
   const int32_t *lens, *cu;
-  float c, sign;
+  float c;  // scale log2(e)
   float *w;
   int N, B, Hq, G, T, W;
-  int max_len, blocks;  // key blocks of a sequence
+  int max_len, blocks, per;  // workgroups of a sequence, keys of one
 };
 
+// A sequence's queries and keys.
+struct WeighSpan {
+  int t0, lq, off, end;
+  size_t q0;  // row of the batch's first query of query head 0
+};
+__device__ __forceinline__ WeighSpan weigh_span(const KvWeighParams &p, int n) {
+  const int t0 = p.cu ? min(max(p.cu[n], 0), p.T) : 0;
+  const int lq = p.cu ? min(max(p.cu[n + 1], t0), p.T) - t0 : p.T;
+  const int len = max(p.lens[n], 0);
+  return {t0, lq, len - lq, readable(p.kv, len, p.max_len), (p.cu ? 0 : (size_t)n) * p.Hq * p.T + t0};
+}
+// log2(e) lse of a row, infinite where it gives nothing: past the end, or with a query that sees nothing
+__device__ __forceinline__ float weigh_base(float lse, bool there) {
+  return there && fabsf(lse) < INFINITY ? lse * 1.44269504f : INFINITY;
+}
+
+// Many rows: 64 keys to a workgroup, in each of its four waves as left operands in registers
+// (lane (r, h): channels h D/2 and up of key r, eight to a product, q's taken in the same
+// order).  The waves take the rows in turn, 32 at a time, the next ones' loads ahead, and keep sums
+// with rows along the lanes until the end.
 template <typename E, int D>
 __global__ __launch_bounds__(256) void kla_kv4_weigh_kernel(KvWeighParams p) {
-  constexpr int NT = sizeof(E) == 2 ? 1 : 3, KJ = D / 16, KB = 2, KPW = 32 * KB;
+  constexpr int NT = sizeof(E) == 2 ? 1 : 3, KJ = D / 16, KB = 2;
+  constexpr int QP = D / 2 * (int)sizeof(E) / 16;  // 16-byte pieces of half a query
+  __shared__ float s_sum[4][32 * KB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
   unsigned id = blockIdx.x;
   const int head = id % p.kv.Hkv;
   id /= p.kv.Hkv;
-  const int n = id % p.N, block = id / p.N;
-  const int t0 = p.cu ? min(max(p.cu[n], 0), p.T) : 0;
-  const int lq = p.cu ? min(max(p.cu[n + 1], t0), p.T) - t0 : p.T;
-  const int len = max(p.lens[n], 0), off = len - lq, end = readable(p.kv, len, p.max_len);
-  const int key0 = (block * 4 + wave) * KPW;
-  if (key0 >= end || lq == 0) return;
+  const int n = id % p.N, key0 = (int)(id / p.N) * 32 * KB;
+  const WeighSpan s = weigh_span(p, n);
+  if (key0 >= s.end || s.lq == 0) return;
 
-  // the wave's keys: 32 kb + r
-  bf16x8 k[KB][KJ];
-  bool there[KB];
+  bf16x8 k[KB][KJ];  // keys 32 kb + r
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     const int pos = key0 + 32 * kb + r;
-    const long long row = pos < end ? kv_row(p.kv, n, pos, 0, head) : -1;
-    there[kb] = row >= 0;
+    const long long row = pos < s.end ? kv_row(p.kv, n, pos, 0, head) : -1;
     unsigned code[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; i += 4) {
@@ -503,9 +758,9 @@ __global__ __launch_bounds__(256) void kla_kv4_weigh_kernel(KvWeighParams p) {
     }
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
-      const unsigned s = row >= 0 ? p.kv.scales[row * (D / 32) + (h * (D / 2) + 8 * j) / 32] : 127u;
+      const unsigned sc = row >= 0 ? p.kv.scales[row * (D / 32) + (h * (D / 2) + 8 * j) / 32] : 127u;
       unsigned w[4];
-      cvt8(code[j], __builtin_bit_cast(float, s << 23), w);
+      cvt8(code[j], __builtin_bit_cast(float, sc << 23), w);
       __builtin_memcpy(&k[kb][j], w, 16);
     }
   }
@@ -515,17 +770,32 @@ __global__ __launch_bounds__(256) void kla_kv4_weigh_kernel(KvWeighParams p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) sum[kb][i] = 0.f;
 
-  // from the first token that sees the wave's first key
-  const long long rows = (long long)lq * p.G;
-  const int first = max(key0 - off, 0);
-  for (long long r0 = (long long)first * p.G; r0 < rows; r0 += 32) {
+  // rows from the first token that sees the first key on
+  const long long rows = (long long)s.lq * p.G;
+  const size_t h0 = s.q0 + (size_t)head * p.G * p.T;
+  struct Query {
+    u32x4 q[QP];
+    float lse;
+    int lim;  // the last key that it sees
+    bool there;
+  };
+  auto load = [&](Query &x, long long r0) {
     const long long row = min(r0 + r, rows - 1);
     const int ti = (int)(row / p.G);
-    const size_t qrow = ((size_t)p.B == 1 && p.cu ? 0 : (size_t)n) * p.Hq * p.T + (size_t)(head * p.G + (int)(row % p.G)) * p.T + t0 + ti;
-    float lse = p.lse[qrow];
-    // a query that sees nothing gives nothing, nor does a row past the end
-    lse = lse == -INFINITY || r0 + r >= rows ? INFINITY : lse;
-    const float base = lse * 1.44269504f;
+    const size_t at = h0 + (size_t)(row - (long long)ti * p.G) * p.T + ti;
+#pragma unroll
+    for (int i = 0; i < QP; ++i) x.q[i] = *reinterpret_cast<const u32x4 *>((const E *)p.q + at * D + h * (D / 2) + i * (16 / (int)sizeof(E)));
+    x.lse = p.lse[at];
+    x.lim = ti + s.off;
+    x.there = r0 + r < rows;
+  };
+  long long r0 = (long long)max(key0 - s.off, 0) * p.G + 32 * wave;
+  Query next;
+  load(next, r0);
+  for (; r0 < rows; r0 += 128) {
+    const Query cur = next;
+    load(next, r0 + 128);
+    const float base = weigh_base(cur.lse, cur.there);
     f32x16 x[KB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
@@ -534,45 +804,185 @@ __global__ __launch_bounds__(256) void kla_kv4_weigh_kernel(KvWeighParams p) {
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
       bf16x8 q[NT];
-      q_terms<E, NT>((const E *)p.q + qrow * D + h * (D / 2) + 8 * j, p.sign, q);
+      if constexpr (NT == 1) {
+        q[0] = __builtin_bit_cast(bf16x8, cur.q[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const unsigned bits = cur.q[2 * j + i / 4][i % 4];
+          float f = __builtin_bit_cast(float, bits);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            q[u][i] = (bf16)f;
+            f -= (float)q[u][i];
+          }
+        }
+      }
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int u = NT - 1; u >= 0; --u) x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[kb][j], q[u], x[kb], 0, 0, 0);
     }
-    const int lim = ti + off;  // the last key that the row sees
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float e = __builtin_amdgcn_exp2f(fmaf(x[kb][i], p.c, -base));
         const int key = key0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4;
-        sum[kb][i] += key <= lim && base < INFINITY ? e : 0.f;
+        sum[kb][i] += key <= cur.lim && base < INFINITY ? e : 0.f;
       }
   }
+  // over the rows of a wave; lane (r, h) of the first 16 keeps key 8 (r / 4) + 4 h + r % 4
 #pragma unroll
-  for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-#pragma unroll
-      for (int w = 16; w >= 1; w >>= 1) sum[kb][i] += __shfl_xor(sum[kb][i], w);
-    }
-  // lane (r, h) writes key 8 (r / 4 % 4) + 4 h + r % 4 of part r / 16: register r % 16 of either half
-  const unsigned long long ok[KB] = {__ballot(there[0]), __ballot(there[1])};
-#pragma unroll
-  for (int kb = 0; kb < KB; ++kb)
+  for (int kb = 0; kb < KB; ++kb) {
+    float mine = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int at = 8 * (i / 4) + 4 * h + i % 4, key = key0 + 32 * kb + at;
-      if (r == i && key < end && (ok[kb] >> at & 1)) {
-        float *const to = p.w + ((size_t)n * p.kv.Hkv + head) * p.W + key;
-        *to += sum[kb][i];
-      }
+      float v = sum[kb][i];
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) v += __shfl_xor(v, w);
+      mine = r == i ? v : mine;
     }
+    if (r < 16) s_sum[wave][32 * kb + 8 * (r / 4) + 4 * h + r % 4] = mine;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32 * KB) {
+    const int key = key0 + threadIdx.x;
+    if (key < s.end && kv_row(p.kv, n, key, 0, head) >= 0) {
+      float v = s_sum[0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) v += s_sum[w][threadIdx.x];
+      p.w[((size_t)n * p.kv.Hkv + head) * p.W + key] += v;
+    }
+  }
 }
 
-// How a chunk call runs: tiles of 32, 128 or 256 rows by the rows of a sequence (the host's mean),
-// and runs of keys as many as make about 512 workgroups, of 512 keys at least.
+// Few rows: 16 RB of them stay in registers as left operands and the keys stream past, 32 at a
+// time to each of four waves (lane (r, c): channels c D/4 and up of keys r and 16 + r).  A score
+// tile has a row in each register and keys along the lanes, so a key's sum is additions within
+// a lane and two exchanges.  More rows than that: the keys again for the next ones.
+template <typename E, int D, int RB>
+__global__ __launch_bounds__(256) void kla_kv4_weigh_few_kernel(KvWeighParams p) {
+  constexpr int NT = sizeof(E) == 2 ? 1 : 3, KJ = D / 32, BM = 16 * RB;
+  __shared__ int s_page[KV_MAX_PER / 16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, c = lane >> 4;
+  unsigned id = blockIdx.x;
+  const int head = id % p.kv.Hkv;
+  id /= p.kv.Hkv;
+  const int n = id % p.N, lo = (int)(id / p.N) * p.per;
+  const WeighSpan s = weigh_span(p, n);
+  const int hi = (int)min((long long)s.end, (long long)lo + p.per);
+  if (lo >= hi || s.lq == 0) return;
+  for (int i = threadIdx.x; i < (hi - lo + 31) / 32 * 2; i += 256) {
+    const int t = lo + 16 * i;
+    int page = -1;
+    if (t < hi) {
+      page = p.kv.table[(size_t)n * p.kv.max_pages + t / p.kv.page];
+      if (page >= p.kv.num_pages) page = -1;
+    }
+    s_page[i] = page;
+  }
+  __syncthreads();
+  const long long rows = (long long)s.lq * p.G;
+  const size_t h0 = s.q0 + (size_t)head * p.G * p.T;
+  float *const weights = p.w + ((size_t)n * p.kv.Hkv + head) * p.W;
+  for (long long row0 = 0; row0 < rows; row0 += BM) {
+    bf16x8 q[RB][KJ][NT];
+    float base[RB][4];
+    int lim[RB][4];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      auto at = [&](long long row, int *ti) {
+        *ti = (int)(row / p.G);
+        return h0 + (size_t)(row - (long long)*ti * p.G) * p.T + *ti;
+      };
+      int ti;
+      const E *const qp = (const E *)p.q + at(min(row0 + 16 * b + r, rows - 1), &ti) * D;
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) q_terms<E, NT>(qp + c * (D / 4) + 8 * j, 1.f, q[b][j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long row = row0 + 16 * b + 4 * c + i;
+        const size_t a = at(min(row, rows - 1), &ti);
+        base[b][i] = weigh_base(p.lse[a], row < rows);
+        lim[b][i] = base[b][i] < INFINITY ? ti + s.off : -1;
+      }
+    }
+    const int all = s.off + (int)(row0 / p.G);  // the last key that the first row sees
+    struct Tile {
+      unsigned k[2][KJ];
+      unsigned sc[2];
+      float w;
+      int id0, id1;
+    } next;
+    auto load = [&](Tile &x, int t) {
+      x.id0 = __builtin_amdgcn_readfirstlane(s_page[(t - lo) >> 4]);
+      x.id1 = __builtin_amdgcn_readfirstlane(s_page[((t - lo) >> 4) + 1]);
+      const size_t pg = (size_t)p.kv.Hkv * p.kv.page;
+      const size_t b0 = (size_t)max(x.id0, 0) * 2 * pg + (size_t)head * p.kv.page + t % p.kv.page;
+      const size_t b1 = (size_t)max(x.id1, 0) * 2 * pg + (size_t)head * p.kv.page + (t + 16) % p.kv.page;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const size_t row = (h ? b1 : b0) + r;
+        const uint8_t *a = p.kv.codes + row * (D / 2) + c * (D / 8);
+        if constexpr (D == 128) {
+          const u32x4 u = ld16<false>(a);
+          x.k[h][0] = u[0], x.k[h][1] = u[1], x.k[h][2] = u[2], x.k[h][3] = u[3];
+        } else {
+          typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+          const u32x2 u = *reinterpret_cast<const u32x2 *>(a);
+          x.k[h][0] = u[0], x.k[h][1] = u[1];
+        }
+        x.sc[h] = p.kv.scales[row * (D / 32) + (D == 128 ? c : c / 2)];
+      }
+      x.w = weights[min(t + (lane & 31), hi - 1)];
+    };
+    int t = lo + 32 * wave;
+    if (t < hi) load(next, t);
+    for (; t < hi; t += 128) {
+      const Tile x0 = next;
+      if (t + 128 < hi) load(next, t + 128);
+      float sum[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4 x[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) x[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const float sc = __builtin_bit_cast(float, x0.sc[h] << 23);
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+          unsigned w[4];
+          cvt8(x0.k[h][j], sc, w);
+          bf16x8 a;
+          __builtin_memcpy(&a, w, 16);
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int u = NT - 1; u >= 0; --u) x[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[b][j][u], a, x[b], 0, 0, 0);
+        }
+        const int key = t + 16 * h + r;
+        float v = 0.f;
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(x[b][i], p.c, -base[b][i]));
+            v += key <= lim[b][i] ? e : 0.f;
+          }
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+        sum[h] = v;
+      }
+      const int key = t + (lane & 31);
+      if (lane < 32 && key < hi && (lane < 16 ? x0.id0 : x0.id1) >= 0) weights[key] = x0.w + (lane < 16 ? sum[0] : sum[1]);
+    }
+  }
+}
+
+// How a chunk call runs, by the rows of a sequence (the host's mean): tiles of 16 or 32 rows
+// where those are few, of 128 or 256 else; and runs of keys as many as make about 512
+// workgroups (few rows: 1,024), of 512 keys at least.
 struct ChunkPlan {
   int BM, slots, splits, per;
 };
@@ -580,40 +990,66 @@ ChunkPlan chunk_plan(const Kv4ChunkArgs &a) {
   const long long G = a.Hq / a.c.Hkv, seqs = std::max(a.N, 1);
   const long long rows = (long long)a.B * a.T * G, mean = (rows + seqs - 1) / seqs;
   ChunkPlan p;
-  p.BM = mean <= 64 ? 32 : mean <= 512 || a.dtype != 0 ? 128 : 256;
+  p.BM = mean <= 16 || (mean <= 64 && a.dtype != 0) ? 16 : mean <= 64 ? 32 : mean <= 512 || a.dtype != 0 ? 128 : 256;
   const long long tiles = a.cu ? (long long)a.T * G / p.BM + a.N : seqs * (((long long)a.T * G + p.BM - 1) / p.BM);
   p.slots = (int)std::min<long long>(tiles, 0x7fffffff);
   const long long busy = seqs * ((mean + p.BM - 1) / p.BM) * a.c.Hkv;
-  long long want = std::max<long long>(1, 512 / std::max<long long>(1, busy));
-  want = std::min(want, std::max<long long>(1, a.max_len / 512));
+  long long want = std::max<long long>(1, (p.BM <= 32 ? 1024 : 512) / std::max<long long>(1, busy));
+  want = std::min(want, std::max<long long>(1, a.max_len / (p.BM <= 32 ? 384 : 512)));
   const long long len = (a.max_len + want - 1) / want;
   p.per = (int)std::max<long long>(128, (len + 127) / 128 * 128);
+  if (p.BM <= 32) p.per = std::min(p.per, KV_MAX_PER);
   p.splits = (int)std::max<long long>(1, ((long long)a.max_len + p.per - 1) / p.per);
   return p;
 }
 
-template <typename E, int D, int NW, int KS, int BN>
-hipError_t launch_chunk_t(const KvChunkParams &p, hipStream_t st) {
-  const long long grid = (long long)p.slots * p.kv.Hkv * p.splits;
-  hipLaunchKernelGGL((kla_kv4_chunk_kernel<E, D, NW, KS, BN>), dim3((unsigned)grid), dim3(64 * NW), 0, st, p);
+template <typename E, int D>
+hipError_t launch_chunk(const KvChunkParams &p, int BM, hipStream_t st) {
+  const dim3 grid((unsigned)((long long)p.slots * p.kv.Hkv * p.splits));
+  auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, p); };
+  // few rows: codes past the caches where those do not keep them from call to call anyway
+  // (kla_kv4.hip); two row blocks of fp32 queries would not fit the registers
+  const bool once = (double)p.N * p.kv.Hkv * p.max_len * (D + D / 16) >= 96 << 20;
+  if (BM == 16) {
+    if (once) go(kla_kv4_rows_kernel<E, D, 1, true>, 256);
+    else go(kla_kv4_rows_kernel<E, D, 1, false>, 256);
+  } else if constexpr (sizeof(E) == 2) {
+    if (BM == 32) {
+      if (once) go(kla_kv4_rows_kernel<E, D, 2, true>, 256);
+      else go(kla_kv4_rows_kernel<E, D, 2, false>, 256);
+    } else if (BM == 128) {
+      go(kla_kv4_chunk_kernel<E, D, 4, 64>, 256);
+    } else {
+      go(kla_kv4_chunk_kernel<E, D, 8, 8192 / D>, 512);
+    }
+  } else {
+    go(kla_kv4_chunk_kernel<E, D, 4, 4096 / D>, 256);
+  }
   if (p.splits > 1) {
     const size_t rows = (size_t)p.B * p.Hq * p.T, per = 256 / (D / 4);
     hipLaunchKernelGGL((kla_kv4_chunk_join_kernel<E, D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, p);
   }
   return hipGetLastError();
 }
-template <typename E, int D>
-hipError_t launch_chunk(const KvChunkParams &p, int BM, hipStream_t st) {
-  if (BM == 32) return launch_chunk_t<E, D, 4, 4, 32>(p, st);
-  if constexpr (sizeof(E) == 2) {
-    if (BM == 256) return launch_chunk_t<E, D, 8, 1, 8192 / D>(p, st);
-    return launch_chunk_t<E, D, 4, 1, 64>(p, st);
-  } else {
-    return launch_chunk_t<E, D, 4, 1, 4096 / D>(p, st);
-  }
-}
 
-int weigh_blocks(const Kv4ChunkArgs &a) { return (a.max_len + 255) / 256; }
+// How the weights are made: rows of a sequence (the host's mean) that a wave holds, in blocks of
+// 16, with keys streaming past in runs; 0: more, with 64 keys to a workgroup.
+struct WeighPlan {
+  int RB, blocks, per;
+};
+WeighPlan weigh_plan(const Kv4ChunkArgs &a) {
+  const long long G = a.Hq / a.c.Hkv, seqs = std::max(a.N, 1);
+  const long long mean = ((long long)a.B * a.T * G + seqs - 1) / seqs;
+  WeighPlan p;
+  p.RB = mean <= 16 ? 1 : mean <= 32 && a.dtype == 0 ? 2 : 0;
+  p.per = 64;
+  if (p.RB) {
+    const long long want = std::max<long long>(1, 2048 / (seqs * a.c.Hkv)), len = (a.max_len + want - 1) / want;
+    p.per = (int)std::min<long long>(KV_MAX_PER, std::max<long long>(256, (len + 127) / 128 * 128));
+  }
+  p.blocks = (int)(((long long)a.max_len + p.per - 1) / p.per);
+  return p;
+}
 
 }  // namespace
 
@@ -631,7 +1067,7 @@ bool kv4_chunk_grid_fits(const Kv4ChunkArgs &a) {
 }
 
 bool kv4_weigh_grid_fits(const Kv4ChunkArgs &a) {
-  return (double)a.T * (a.Hq / a.c.Hkv) <= 2147418112.0 && launch_fits((double)weigh_blocks(a) * a.N * a.c.Hkv, 256);
+  return (double)a.T * (a.Hq / a.c.Hkv) <= 2147418112.0 && launch_fits((double)weigh_plan(a).blocks * a.N * a.c.Hkv, 256);
 }
 
 hipError_t launch_attn_kv4_chunk(const Kv4ChunkArgs &a, void *workspace, hipStream_t st) {
@@ -667,8 +1103,7 @@ hipError_t launch_attn_kv4_weigh(const Kv4ChunkArgs &a, float *weights, int W, h
   p.lse = a.lse;
   p.lens = a.lens;
   p.cu = a.cu;
-  p.c = (a.scale == 0.f ? 1.f : std::fabs(a.scale)) * 1.44269504f;
-  p.sign = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
+  p.c = a.scale * 1.44269504f;
   p.w = weights;
   p.N = a.N;
   p.B = a.B;
@@ -677,17 +1112,21 @@ hipError_t launch_attn_kv4_weigh(const Kv4ChunkArgs &a, float *weights, int W, h
   p.T = a.T;
   p.W = W;
   p.max_len = a.max_len;
-  p.blocks = weigh_blocks(a);
-  const dim3 grid((unsigned)((long long)p.blocks * p.N * a.c.Hkv));
+  const WeighPlan plan = weigh_plan(a);
+  p.blocks = plan.blocks;
+  p.per = plan.per;
   if (a.max_len == 0) return hipSuccess;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((long long)p.blocks * p.N * a.c.Hkv)), dim3(256), 0, st, p);
+    return hipGetLastError();
+  };
   if (a.dtype == 0) {
-    if (a.D == 128) hipLaunchKernelGGL((kla_kv4_weigh_kernel<bf16, 128>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((kla_kv4_weigh_kernel<bf16, 64>), grid, dim3(256), 0, st, p);
-  } else {
-    if (a.D == 128) hipLaunchKernelGGL((kla_kv4_weigh_kernel<float, 128>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((kla_kv4_weigh_kernel<float, 64>), grid, dim3(256), 0, st, p);
+    if (plan.RB == 1) return a.D == 128 ? go(kla_kv4_weigh_few_kernel<bf16, 128, 1>) : go(kla_kv4_weigh_few_kernel<bf16, 64, 1>);
+    if (plan.RB == 2) return a.D == 128 ? go(kla_kv4_weigh_few_kernel<bf16, 128, 2>) : go(kla_kv4_weigh_few_kernel<bf16, 64, 2>);
+    return a.D == 128 ? go(kla_kv4_weigh_kernel<bf16, 128>) : go(kla_kv4_weigh_kernel<bf16, 64>);
   }
-  return hipGetLastError();
+  if (plan.RB == 1) return a.D == 128 ? go(kla_kv4_weigh_few_kernel<float, 128, 1>) : go(kla_kv4_weigh_few_kernel<float, 64, 1>);
+  return a.D == 128 ? go(kla_kv4_weigh_kernel<float, 128>) : go(kla_kv4_weigh_kernel<float, 64>);
 }
 
 }  // namespace kla
