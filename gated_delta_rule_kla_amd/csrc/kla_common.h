@@ -33,6 +33,21 @@ template <> struct Elem<float> {
 __device__ __forceinline__ uint4 ldg16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
 __device__ __forceinline__ void stg16(void *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
 
+// The last of 0 .. n-1 for which ok holds, where it holds up to some place (0 if nowhere), found
+// by all lanes of a wave, 64 places a step: what a step reads of memory comes at once.
+template <class F>
+__device__ __forceinline__ int wave_last_where(int n, F ok) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 63) / 64, at = lane * step;
+    const int k = max(__popcll(__ballot(at < n && ok(lo + at))), 1) - 1;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // PGDN's preconditioner weight of one key coordinate ("Preconditioned DeltaNet",
 // §2.C: the inverse of the accumulated diagonal key moments, squashed in log space
 // into [1/band, band]): with the coordinate's accumulator a, the mean accumulator m

@@ -41,26 +41,21 @@ struct KvChunkParams {
 // A row tile: its sequence, the sequence's rows, first query row of the batch and batch row, and
 // the tile's first row.
 struct RowTile {
-  int n, b, t0, first;
-  long long rows;
+  int n, b, t0, first, rows;
 };
 template <int BM>
 __device__ __forceinline__ bool row_tile(const int32_t *cu, int N, int T, int G, int slot, RowTile *r) {
   if (!cu) {
     const int per = (int)(((long long)T * G + BM - 1) / BM);
-    *r = RowTile{slot / per, slot / per, 0, slot % per * BM, (long long)T * G};
+    *r = RowTile{slot / per, slot / per, 0, slot % per * BM, T * G};
     return true;
   }
   // sequence n has the slots cu[n] G / BM + n and up: never another's
   auto base = [&](int n) { return (long long)min(max(cu[n], 0), T) * G / BM + n; };
-  int lo = 0, hi = N;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (base(mid) <= slot) lo = mid; else hi = mid;
-  }
+  const int lo = wave_last_where(N, [&](int n) { return base(n) <= slot; });
   const int a = min(max(cu[lo], 0), T), z = min(max(cu[lo + 1], a), T);
   const long long first = (slot - base(lo)) * BM;
-  *r = RowTile{lo, 0, a, (int)first, (long long)(z - a) * G};
+  *r = RowTile{lo, 0, a, (int)first, (z - a) * G};
   return first >= 0 && first < r->rows;
 }
 
@@ -165,15 +160,15 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   if (!row_tile<BM>(p.cu, p.N, p.T, p.G, slot, &rt)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-  const int n = rt.n, lq = (int)(rt.rows / p.G);
+  const int n = rt.n, lq = rt.rows / p.G;
   const int len = max(p.lens[n], 0), off = len - lq;
   const int lo = split * p.per, hi = (int)min((long long)readable(p.kv, len, p.max_len), (long long)lo + p.per);
   // the row of this lane (past the end: the last one) and the last key that it sees
   const int w0 = rt.first + 32 * wave;
-  auto last_seen = [&](long long row) { return min((int)(min(row, rt.rows - 1) / p.G) + off, hi - 1); };
-  const long long mine = w0 + r;
-  const int row = (int)min(mine, rt.rows - 1), ti = row / p.G;
-  const size_t qrow = ((size_t)rt.b * p.Hq + head * p.G + row % p.G) * p.T + rt.t0 + ti;
+  auto last_seen = [&](int row) { return min((int)((unsigned)min(row, rt.rows - 1) / (unsigned)p.G) + off, hi - 1); };
+  const int mine = w0 + r, row = min(mine, rt.rows - 1);
+  const unsigned ti = (unsigned)row / (unsigned)p.G;
+  const size_t qrow = ((size_t)rt.b * p.Hq + head * p.G + (row - ti * p.G)) * p.T + rt.t0 + ti;
   const int lim = last_seen(row), wfirst = last_seen(w0), wlast = last_seen(w0 + 31);
   const int end = last_seen(rt.first + BM - 1) + 1;    // keys of the workgroup
 
@@ -401,6 +396,7 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t s_v[4][32 * D / 2];
   __shared__ unsigned s_sc[4][64];
   __shared__ int s_bad;
+  __shared__ size_t s_row[BM];  // places of the tile's rows among the queries
 
   unsigned id = blockIdx.x;
   const int head = id % p.kv.Hkv;
@@ -409,17 +405,18 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   RowTile rt;
   if (!row_tile<BM>(p.cu, p.N, p.T, p.G, slot, &rt)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, c = lane >> 4, n = rt.n, lq = (int)(rt.rows / p.G);
+  const int r = lane & 15, c = lane >> 4, n = rt.n, lq = rt.rows / p.G;
   const int len = max(p.lens[n], 0), off = len - lq;
   const int lo = split * p.per, hi = (int)min((long long)readable(p.kv, len, p.max_len), (long long)lo + p.per);
-  auto last_seen = [&](long long row) { return min((int)(min(row, rt.rows - 1) / p.G) + off, hi - 1); };
-  auto q_row = [&](long long row) {
-    const int ti = (int)(row / p.G);
-    return ((size_t)rt.b * p.Hq + head * p.G + (int)(row % p.G)) * p.T + rt.t0 + ti;
+  auto last_seen = [&](int row) { return min((int)((unsigned)min(row, rt.rows - 1) / (unsigned)p.G) + off, hi - 1); };
+  auto q_row = [&](int row) {
+    const unsigned ti = (unsigned)row / (unsigned)p.G;
+    return ((size_t)rt.b * p.Hq + head * p.G + (row - ti * p.G)) * p.T + rt.t0 + ti;
   };
-  const int gn = (int)min((long long)BM, rt.rows - rt.first);       // rows of the tile
+  const int gn = min(BM, rt.rows - rt.first);  // rows of the tile
   const int end = last_seen(rt.first + BM - 1) + 1, all = last_seen(rt.first);  // keys of the tile, of its first row
   if (tid == 0) s_bad = 0;
+  if (tid < gn) s_row[tid] = q_row(rt.first + tid);
   for (int i = tid; i < (max(end - lo, 0) + 31) / 32 * 2; i += 256) {
     const int t = lo + 16 * i;
     int page = -1;
@@ -433,7 +430,7 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   int lim[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
-    const long long row = min(rt.first + 16 * b + (long long)r, rt.rows - 1);
+    const int row = min(rt.first + 16 * b + r, rt.rows - 1);
     lim[b] = last_seen(row);
     const E *const qp = (const E *)p.q + q_row(row) * D;
 #pragma unroll
@@ -626,7 +623,7 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
         oo = fmaf(s_o[w][g][d], f, oo);
       }
       if (!(fabsf(fmaf(oo, 0.f, ll)) < INFINITY)) atomicOr(&s_bad, 1 << (16 * b + g));
-      const size_t qr = q_row(rt.first + 16 * b + g), part = qr * p.splits + split;
+      const size_t qr = s_row[16 * b + g], part = qr * p.splits + split;
       if (p.splits == 1) {
         ((E *)p.o)[qr * D + d] = Elem<E>::from_f32(ll == 0.f ? 0.f : oo / ll);
         if (d == 0 && p.lse) p.lse[qr] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.693147181f;
@@ -644,11 +641,11 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   int bad = __builtin_amdgcn_readfirstlane(s_bad);
   for (int i = 0; bad; ++i, bad &= bad - 1) {
     if (i % 4 != wave) continue;
-    const long long row = rt.first + __builtin_ctz(bad);
-    const size_t qr = q_row(row), part = qr * p.splits + split;
+    const int at = __builtin_ctz(bad);
+    const size_t qr = s_row[at], part = qr * p.splits + split;
     constexpr int CPL = D / 64;
     float rm, rl, a[CPL];
-    attend_row<E, D>(p, (const E *)p.q + qr * D, n, head, lo, last_seen(row) + 1, &rm, &rl, a);
+    attend_row<E, D>(p, (const E *)p.q + qr * D, n, head, lo, last_seen(rt.first + at) + 1, &rm, &rl, a);
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
       if (p.splits > 1) p.part_o[part * D + CPL * lane + k] = a[k];

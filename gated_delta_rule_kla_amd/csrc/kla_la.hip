@@ -594,12 +594,7 @@ __global__ __launch_bounds__(C * 4) void kla_la_grad_kernel(LaGradParams p) {
   const int g = lane >> 4, li = lane & 15;
   int n = 0;
   if (p.cu) {
-    int lo = 0, hi = p.N;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (min(max(p.cu[mid], 0), p.T) / C + mid <= slot) lo = mid; else hi = mid;
-    }
-    n = lo;
+    n = wave_last_where(p.N, [&](int i) { return min(max(p.cu[i], 0), p.T) / C + i <= slot; });
   } else {
     n = slot / ((p.T + C - 1) / C);
   }
