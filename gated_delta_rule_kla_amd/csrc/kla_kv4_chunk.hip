@@ -390,11 +390,21 @@ template <typename E, int D, int RB, bool ONCE>
 __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;  // bf16 terms of q and of the weights
   constexpr int KJ = D / 32, DW = D / 16, BM = 16 * RB;
-  __shared__ int s_page[KV_MAX_PER / 16];
-  __shared__ float s_o[4][16][D + 4];
-  __shared__ float s_ml[4][16][2];
-  __shared__ __attribute__((aligned(16))) uint8_t s_v[4][32 * D / 2];
-  __shared__ unsigned s_sc[4][64];
+  // what the tiles need, and what joining the waves needs behind them
+  struct Tiles {
+    uint8_t v[4][32 * D / 2];
+    unsigned sc[4][64];
+    int page[KV_MAX_PER / 16];
+  };
+  struct Joined {
+    float o[4][16][D / 2 + 4], ml[4][16][2], f[4][16], m[16], l[16];
+  };
+  union Lds {
+    Tiles t;
+    Joined j;
+  };
+  __shared__ __attribute__((aligned(16))) Lds lds;
+  int *const s_page = lds.t.page;
   __shared__ int s_bad;
   __shared__ size_t s_row[BM];  // places of the tile's rows among the queries
 
@@ -492,10 +502,10 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
       const int key = lane / LPR + 64 / LPR * i, slot_ = (key & 16) + 4 * (key & 3) + ((key >> 2) & 3);
-      *reinterpret_cast<u32x4 *>(s_v[wave] + slot_ * (D / 2) + 16 * (lane % LPR)) = x0.v[i];
+      *reinterpret_cast<u32x4 *>(lds.t.v[wave] + slot_ * (D / 2) + 16 * (lane % LPR)) = x0.v[i];
     }
-    s_sc[wave][lane] = x0.sc;
-    const uint8_t *sc8 = reinterpret_cast<const uint8_t *>(s_sc[wave]);
+    lds.t.sc[wave][lane] = x0.sc;
+    const uint8_t *sc8 = reinterpret_cast<const uint8_t *>(lds.t.sc[wave]);
     const int id0 = x0.id0, id1 = x0.id1;
     // scores of keys t + 16 h + 4 c + i against rows 16 b + r
     float x[RB][8];
@@ -519,13 +529,13 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[b][4 * h + i] = s[b][i] * p.c;
+        for (int i = 0; i < 4; ++i) x[b][4 * h + i] = s[b][i];
     }
     unsigned va[8];
     float vf[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint8_t *a = s_v[wave] + ((e & 4) * 4 + 4 * (e & 3) + c) * (D / 2);
+      const uint8_t *a = lds.t.v[wave] + ((e & 4) * 4 + 4 * (e & 3) + c) * (D / 2);
       unsigned short half;
       if constexpr (D == 128) __builtin_memcpy(&va[e], __builtin_assume_aligned(a + 4 * r, 4), 4);
       else __builtin_memcpy(&half, __builtin_assume_aligned(a + 2 * r, 2), 2), va[e] = half;
@@ -551,7 +561,7 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[b][e]);
       top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
+      top = fmaxf(top, __shfl_xor(top, 32)) * p.c;
       // the maximum moves by 2^LAG at least, as in kla_attn_tile.h
       if (__any(top > m[b] + LAG)) {
         const float mn = top > m[b] + LAG ? top : m[b];
@@ -566,7 +576,7 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
       const float base = m[b] == -INFINITY ? 0.f : m[b];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float v = __builtin_amdgcn_exp2f(x[b][e] - base);
+        float v = __builtin_amdgcn_exp2f(fmaf(x[b][e], p.c, -base));
         l[b] += v;
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
@@ -594,44 +604,60 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
     }
   }
 
-  // join the waves, 16 rows at a time
+  // join the waves, 16 rows at a time and half of the channels (DW / 2 of each lane's)
+  constexpr int DH = DW / 2;
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     l[b] += __shfl_xor(l[b], 16);
     l[b] += __shfl_xor(l[b], 32);
-    if (b) __syncthreads();
+    const int rows = min(gn - 16 * b, 16);
+    __syncthreads();
     if (c == 0) {
-      s_ml[wave][r][0] = m[b];
-      s_ml[wave][r][1] = l[b];
+      lds.j.ml[wave][r][0] = m[b];
+      lds.j.ml[wave][r][1] = l[b];
     }
 #pragma unroll
-    for (int j = 0; j < DW; ++j)
+    for (int half = 0; half < 2; ++half) {
+      if (half) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s_o[wave][r][(4 * c + i) * DW + j] = acc[b][j][i];
-    __syncthreads();
-    for (int i = tid; i < min(gn - 16 * b, 16) * D; i += 256) {
-      const int g = i / D, d = i % D;
-      float mm = s_ml[0][g][0];
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int w = 1; w < 4; ++w) mm = fmaxf(mm, s_ml[w][g][0]);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f, oo = 0.f;
+        for (int j = 0; j < DH; ++j) lds.j.o[wave][r][(4 * c + i) * DH + j] = acc[b][half * DH + j][i];
+      __syncthreads();
+      if (half == 0) {
+        if (tid < 16) {
+          float mm = lds.j.ml[0][tid][0], ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = __builtin_amdgcn_exp2f(s_ml[w][g][0] - base);
-        ll = fmaf(s_ml[w][g][1], f, ll);
-        oo = fmaf(s_o[w][g][d], f, oo);
+          for (int w = 1; w < 4; ++w) mm = fmaxf(mm, lds.j.ml[w][tid][0]);
+          const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float f = __builtin_amdgcn_exp2f(lds.j.ml[w][tid][0] - base);
+            lds.j.f[w][tid] = f;
+            ll = fmaf(lds.j.ml[w][tid][1], f, ll);
+          }
+          lds.j.m[tid] = mm;
+          lds.j.l[tid] = ll;
+        }
+        __syncthreads();
       }
-      if (!(fabsf(fmaf(oo, 0.f, ll)) < INFINITY)) atomicOr(&s_bad, 1 << (16 * b + g));
-      const size_t qr = s_row[16 * b + g], part = qr * p.splits + split;
-      if (p.splits == 1) {
-        ((E *)p.o)[qr * D + d] = Elem<E>::from_f32(ll == 0.f ? 0.f : oo / ll);
-        if (d == 0 && p.lse) p.lse[qr] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.693147181f;
-      } else {
-        p.part_o[part * D + d] = oo;
-        if (d == 0) {
-          p.part_ml[part * 2] = mm;
-          p.part_ml[part * 2 + 1] = ll;
+      for (int i = tid; i < rows * (D / 2); i += 256) {
+        const int g = i / (D / 2), e = i % (D / 2), d = e / DH * DW + half * DH + e % DH;
+        const float mm = lds.j.m[g], ll = lds.j.l[g];
+        float oo = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) oo = fmaf(lds.j.o[w][g][e], lds.j.f[w][g], oo);
+        if (!(fabsf(fmaf(oo, 0.f, ll)) < INFINITY)) atomicOr(&s_bad, 1 << (16 * b + g));
+        const size_t qr = s_row[16 * b + g], part = qr * p.splits + split;
+        if (p.splits == 1) {
+          ((E *)p.o)[qr * D + d] = Elem<E>::from_f32(ll == 0.f ? 0.f : oo / ll);
+          if (d == 0 && p.lse) p.lse[qr] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.693147181f;
+        } else {
+          p.part_o[part * D + d] = oo;
+          if (d == 0) {
+            p.part_ml[part * 2] = mm;
+            p.part_ml[part * 2 + 1] = ll;
+          }
         }
       }
     }
