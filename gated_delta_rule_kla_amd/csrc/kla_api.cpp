@@ -837,11 +837,12 @@ kla_status_t kla_attn_kv4_weigh(const void *q, const float *lse, const void *cod
   return from_hip(kla::launch_attn_kv4_weigh(a, weights, max_tokens, reinterpret_cast<hipStream_t>(stream)));
 }
 
-size_t kla_kv4_evict_workspace_bytes(int num_seqs, int Hkv, int D, int budget) {
-  if (check_kv4(Hkv, D, 1, 16, 1, num_seqs, KLA_DT_BF16) != KLA_OK || budget <= 0 || budget > kMaxTokens ||
+size_t kla_kv4_evict_workspace_bytes(int num_seqs, int Hkv, int D, int budget, int page_size, int max_pages) {
+  if (check_kv4(Hkv, D, 1, page_size, max_pages, num_seqs, KLA_DT_BF16) != KLA_OK || num_seqs == 0 || budget <= 0 ||
+      budget > kMaxTokens || (long long)max_pages * page_size > kMaxTokens ||
       !kla::kv4_evict_grid_fits(num_seqs, Hkv, budget))
     return 0;
-  return kla::kv4_evict_workspace_bytes(num_seqs, Hkv, D, budget);
+  return kla::kv4_evict_workspace_bytes(num_seqs, Hkv, D, budget, (long long)max_pages * page_size);
 }
 
 kla_status_t kla_kv4_evict(void *codes, void *scales, const int32_t *block_table, const int32_t *seq_lens,
@@ -858,7 +859,7 @@ kla_status_t kla_kv4_evict(void *codes, void *scales, const int32_t *block_table
   if (misaligned(codes) || misaligned(scales) || misaligned4(block_table) || misaligned4(seq_lens) ||
       misaligned(weights) || misaligned4(new_lens) || misaligned4(kept) || misaligned(workspace))
     return KLA_ERR_ALIGN;
-  const size_t need = kla::kv4_evict_workspace_bytes(num_seqs, Hkv, D, budget);
+  const size_t need = kla::kv4_evict_workspace_bytes(num_seqs, Hkv, D, budget, (long long)max_pages * page_size);
   if (workspace == nullptr || workspace_bytes < need) return KLA_ERR_WORKSPACE;
   const kla::Kv4Cache c{codes, scales, block_table, num_pages, page_size, max_pages, Hkv};
   return from_hip(kla::launch_kv4_evict(c, seq_lens, new_lens, kept, weights, num_seqs, D, max_tokens, budget, recent,

@@ -218,7 +218,7 @@ hipError_t launch_attn_kv4_chunk(const Kv4ChunkArgs &a, void *workspace, hipStre
 bool kv4_weigh_grid_fits(const Kv4ChunkArgs &a);
 hipError_t launch_attn_kv4_weigh(const Kv4ChunkArgs &a, float *weights, int W, hipStream_t stream);
 // The cache cut to a budget (kla_kv4_evict.hip).
-size_t kv4_evict_workspace_bytes(int N, int Hkv, int D, int budget);
+size_t kv4_evict_workspace_bytes(int N, int Hkv, int D, int budget, long long room);  // tokens of a block table
 bool kv4_evict_grid_fits(int N, int Hkv, int budget);
 hipError_t launch_kv4_evict(const Kv4Cache &c, const int32_t *lens, int32_t *new_lens, int32_t *kept, float *weights,
                             int N, int D, int W, int budget, int recent, void *workspace, hipStream_t stream);

@@ -130,7 +130,7 @@ def lib() -> ctypes.CDLL:
         L.kla_attn_kv4_weigh.restype = i32
         L.kla_kv4_evict.argtypes = [vp] * 7 + [i32] * 9 + [vp, sz, vp]
         L.kla_kv4_evict.restype = i32
-        L.kla_kv4_evict_workspace_bytes.argtypes = [i32] * 4
+        L.kla_kv4_evict_workspace_bytes.argtypes = [i32] * 6
         L.kla_kv4_evict_workspace_bytes.restype = sz
         L.kla_status_str.argtypes = [i32]
         L.kla_status_str.restype = ctypes.c_char_p
@@ -1267,9 +1267,9 @@ def attn_kv4_weigh(
           _ptr(cu_seqlens), _ptr(host), *sizes, *cache, W, _DTYPES[q.dtype])
 
 
-def kv4_evict_workspace_bytes(N: int, Hkv: int, D: int, budget: int) -> int:
+def kv4_evict_workspace_bytes(N: int, Hkv: int, D: int, budget: int, page_size: int, max_pages: int) -> int:
     """Workspace bytes kv4_evict needs (kla_kv4_evict_workspace_bytes)."""
-    return lib().kla_kv4_evict_workspace_bytes(N, Hkv, D, min(int(budget), _INT32))
+    return lib().kla_kv4_evict_workspace_bytes(N, Hkv, D, min(int(budget), _INT32), page_size, max_pages)
 
 
 def kv4_evict(
@@ -1303,7 +1303,7 @@ def kv4_evict(
         raise ValueError(f"budget {budget} and recent {recent}: expected 1 <= budget and 0 <= recent <= budget")
     new_lens = torch.empty_like(seq_lens)
     kept = torch.empty((N, Hkv, budget), dtype=torch.int32, device=dev)
-    ws = _scratch(workspace, lib().kla_kv4_evict_workspace_bytes(N, Hkv, D, budget), dev)
+    ws = _scratch(workspace, lib().kla_kv4_evict_workspace_bytes(N, Hkv, D, budget, page, M), dev)
     _call("kla_kv4_evict", dev, codes.data_ptr(), scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
           weights.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), budget, recent, N, Hkv, D, P, page, M, W, _ptr(ws),
           0 if ws is None else ws.numel())

@@ -827,8 +827,9 @@ kla_status_t kla_kv4_evict(void *codes, void *scales, const int32_t *block_table
                            int max_tokens, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Device workspace of kla_kv4_evict (host-only, no HIP call): D + 32 bytes per sequence, key head
- * and token of the budget; 0 for arguments it would reject. */
-size_t kla_kv4_evict_workspace_bytes(int num_seqs, int Hkv, int D, int budget);
+ * and token of the budget, and for few sequences of many tokens 24 KiB per 4,096 of those; 0 for
+ * arguments it would reject. */
+size_t kla_kv4_evict_workspace_bytes(int num_seqs, int Hkv, int D, int budget, int page_size, int max_pages);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *kla_status_str(kla_status_t s);

@@ -154,3 +154,28 @@ def test_captured_and_replayed(N):
             torch.cuda.synchronize()
             out.append([x.clone() for x in (codes, scales, w, *(got if r is None else r))])
         assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def hard(w):
+    w = w - 3
+    w[..., 3::17] = float("nan")
+    w[..., 5::31] = float("inf")
+    w[..., 6::31] = -float("inf")
+    w[..., 7::29] = 1e-42
+    return w
+
+
+@pytest.mark.parametrize("f", [None, hard, torch.zeros_like, lambda w: (w * 2).round() / 2])
+@pytest.mark.parametrize("budget,recent", [(1, 0), (3000, 3000), (5000, 700), (11999, 1)])
+def test_choices_in_parts(f, budget, recent):
+    """Few sequences of many tokens, in parts of 4,096; also ones that end in an earlier part."""
+    check([20000, 300, 12000, 12288, 8193], 1, 64, 64, budget, recent, f)
+
+
+def test_choices_of_large_batches_and_odd_rows():
+    check([9000] * 40, 4, 64, 16, 2000, 5, hard)
+    codes, scales, table, w = make([9001, 5000], 1, 64, 16)
+    odd = torch.zeros(2, 1, w.shape[2] + 3, device=DEV)
+    odd[..., :w.shape[2]] = w
+    got = [kla.kv4_evict(codes.clone(), scales.clone(), table, i32([9001, 5000]), x, 1234, 56) for x in (w.clone(), odd)]
+    assert torch.equal(got[0][1], got[1][1])

@@ -78,7 +78,8 @@ def test_refusals_of_eviction():
     assert cut(codes=FAKE + 8) == ALIGN and cut(new=FAKE + 2) == ALIGN
     assert cut(ws=None) == WORKSPACE and cut(wsb=100) == WORKSPACE
     assert cut(N=0) == OK
-    assert kla.lib().kla_kv4_evict_workspace_bytes(2, 4, 64, 0) == 0
+    assert kla.lib().kla_kv4_evict_workspace_bytes(2, 4, 64, 0, 16, 4) == 0
+    assert kla.lib().kla_kv4_evict_workspace_bytes(2, 4, 64, 10, 16, 4) >= 2 * 4 * 10 * 96
 
 
 def test_weights_sum_to_the_queries():
