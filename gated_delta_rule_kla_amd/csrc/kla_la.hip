@@ -37,8 +37,7 @@ namespace kla {
 
 namespace {
 
-constexpr int LA_NV = 32;         // state columns of a scan workgroup
-constexpr int LA_AHEAD = 3;       // chunks that a scan's loads run ahead
+constexpr int LA_NV = 32;         // state columns of the smaller slices
 constexpr float LA_FORGET = -65536.f;  // log2 of the smallest decay
 
 // Chunks and operands by element type.  A 16-byte operand holds VL contraction values of a row
@@ -117,31 +116,21 @@ struct Decays {
   double tot;
 };
 
-// by one wave; g[i]: the log-decay of token 64 i + lane (0 past the chunk's tokens)
+// by one wave; g: the lane's log-decay (0 past the chunk's tokens)
 template <int C>
-__device__ __forceinline__ void scan_decays(Decays<C> *d, const float *g) {
-  constexpr int N = (C + 63) / 64;
+__device__ __forceinline__ void scan_decays(Decays<C> *d, float g) {
   const int lane = threadIdx.x & 63;
-  double c[N], rest[N], tot = 0.0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    double x = (double)g[i] * 1.4426950408889634;
-    x = x < LA_FORGET ? LA_FORGET : x;  // a NaN stays
-    if (64 * i + lane >= C) x = 0.0;
-    c[i] = scan_double(x, &rest[i]) + tot;
-    tot = lane_double(c[i], 63);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int t = 64 * i + lane;
-    if (t < C) {
-      const float hi = (float)c[i];
-      d->hi[t] = hi;
-      d->lo[t] = (float)(c[i] - (double)hi);
-      d->out[t] = __builtin_amdgcn_exp2f((float)c[i]);
-      d->left[t] = __builtin_amdgcn_exp2f((float)(tot - c[i]));
-      d->near[t] = __builtin_amdgcn_exp2f((float)rest[i]);
-    }
+  double x = (double)g * 1.4426950408889634, rest;
+  x = x < LA_FORGET ? LA_FORGET : x;  // a NaN stays
+  if (lane >= C) x = 0.0;
+  const double c = scan_double(x, &rest), tot = lane_double(c, 63);
+  if (lane < C) {
+    const float hi = (float)c;
+    d->hi[lane] = hi;
+    d->lo[lane] = (float)(c - (double)hi);
+    d->out[lane] = __builtin_amdgcn_exp2f((float)c);
+    d->left[lane] = __builtin_amdgcn_exp2f((float)(tot - c));
+    d->near[lane] = __builtin_amdgcn_exp2f((float)rest);
   }
   if (lane == 0) {
     d->all = __builtin_amdgcn_exp2f((float)tot);
@@ -170,7 +159,7 @@ struct LaParams {
   int N, H, T, dk, dv;
   int slices, segs, seg_chunks;
   unsigned half;              // workgroups of a direction
-  int slots, group;           // state slots of a head, chunks to a state
+  int slots;                  // chunk slots of a head (states)
 };
 
 // Sequence n: its first row among a head's, its length, and its first slot of C tokens.
@@ -183,7 +172,7 @@ __device__ __forceinline__ void la_span(const int32_t *cu, int n, int T, int C, 
   *t0 = a, *len = z - a, *slot0 = a / C + n;
 }
 
-// The scan over a sequence's chunks.  A workgroup holds LA_NV columns of the state.  Four waves
+// The scan over a sequence's chunks.  A workgroup holds NV columns of the state.  Four waves
 // own the state, a quarter of its rows each, in fp32: they bring x and y to LDS a chunk ahead of
 // their use (from registers that hold the chunks after that), with y's scaled copy, update the
 // state, and leave a copy of it in the element type in LDS.  Beside them four waves compute the
@@ -193,21 +182,22 @@ __device__ __forceinline__ void la_span(const int32_t *cu, int n, int T, int C, 
 //
 // OUT: outputs and the final state.  ENDS: a segment's end state only, where few sequences leave
 // CUs idle and are cut: all segments but the last are scanned once for that, and the other modes
-// start each from those before it.  STORE: the state at the start of every `group` chunks, and of
-// the reverse direction the state's gradient at their end, for the gradients.
+// start each from those before it.  STORE: the state at every chunk's start, and of the
+// reverse direction the state's gradient at its end, for the gradients.
 enum { LA_OUT, LA_ENDS, LA_STORE };
 constexpr int la_threads(int mode) { return mode == LA_OUT ? 512 : 320; }
 
-template <typename E, int DK, int MODE>
+template <typename E, int DK, int MODE, int NV>
 __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams p) {
   using L = La<E>;
   using Op = typename L::Op;
-  constexpr int C = L::C, KG = L::KG, VL = L::VL, NV = LA_NV;
+  constexpr int C = L::C, KG = L::KG, VL = L::VL;
   constexpr int PAD = LdsPad<E>::V, LDX = DK + PAD, LDY = NV + PAD;
   constexpr int XP = C * DK / VL / 256, YP = C * NV / VL / 256;  // 16-byte pieces of a thread
   constexpr int RT = DK / 64;                                  // row tiles of a wave
   constexpr int NC = NV / 16, NS = C / 16, CT = NC * NS / 4;   // column tiles, strips, a wave's output tiles
   constexpr int KS = DK / KG;
+  constexpr int AHEAD = 3;  // chunks that loads run ahead
   static_assert(XP * 256 * VL == C * DK && YP * 256 * VL == C * NV && CT * 4 == NC * NS, "tiles");
   __shared__ __attribute__((aligned(16))) E s_x[2][C * LDX];
   __shared__ __attribute__((aligned(16))) E s_y[MODE == LA_OUT ? 2 : 1][MODE == LA_OUT ? C * LDY : 8];
@@ -227,7 +217,7 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
   const long long nh = pair / p.segs;
   const int n = nh / p.H, h = nh % p.H;
   int t0, len, slot0;
-  la_span(p.cu, n, p.T, C * p.group, &t0, &len, &slot0);
+  la_span(p.cu, n, p.T, C, &t0, &len, &slot0);
   const int nch = (len + C - 1) / C;
   // the chunks in processed order
   const int c0 = seg * p.seg_chunks, c1 = seg == p.segs - 1 ? nch : min(nch, c0 + p.seg_chunks);
@@ -271,18 +261,16 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         }
       }
     };
-    unsigned gn[LA_AHEAD];
-    Query qs[LA_AHEAD];
+    unsigned gn[AHEAD];
+    Query qs[AHEAD];
     const unsigned g0 = load_g(c0), g1 = load_g(within(c0 + 1));
 #pragma unroll
-    for (int i = 0; i < LA_AHEAD; ++i) gn[i] = load_g(within(c0 + 2 + i));
+    for (int i = 0; i < AHEAD; ++i) gn[i] = load_g(within(c0 + 2 + i));
 #pragma unroll
-    for (int i = 0; i < LA_AHEAD; ++i) load_q(qs[i], within(c0 + i));
+    for (int i = 0; i < AHEAD; ++i) load_q(qs[i], within(c0 + i));
     if (wave == 4) {
-      float x = decay(g0, c0);
-      scan_decays<C>(&s_d[c0 % 3], &x);
-      x = decay(g1, within(c0 + 1));
-      scan_decays<C>(&s_d[(c0 + 1) % 3], &x);
+      scan_decays<C>(&s_d[c0 % 3], decay(g0, c0));
+      scan_decays<C>(&s_d[(c0 + 1) % 3], decay(g1, within(c0 + 1)));
     }
     lds_barrier();
     // A strip's code is its own: its scores and their keys are as many as its number says, and in
@@ -293,8 +281,8 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         lds_barrier();
         if (ST == 0 && wave == 4) {
           const float x = decay(gj, within(j + 2));
-          gj = load_g(within(j + 2 + LA_AHEAD));
-          scan_decays<C>(&s_d[(j + 2) % 3], &x);  // behind the last chunk: nobody reads it
+          gj = load_g(within(j + 2 + AHEAD));
+          scan_decays<C>(&s_d[(j + 2) % 3], x);  // behind the last chunk: nobody reads it
         }
         if constexpr (MODE == LA_OUT) {
           const E *const X = s_x[j & 1], *const Y = s_y[j & 1], *const S = s_s[j & 1];
@@ -317,7 +305,7 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
             for (int k = 0; k < KS; ++k)
               o[c] = Ops<E>::mma_grp(L::nat(S + (16 * (ct0 + c) + li) * LDX, k * KG, g), q[k], o[c]);
           }
-          load_q(q, within(j + LA_AHEAD));
+          load_q(q, within(j + AHEAD));
           // earlier keys: the decay to the end of their 16, and from there
           const float th = d.hi[16 * ST + li], tl = d.lo[16 * ST + li], f = d.out[16 * ST + li];
 #pragma unroll
@@ -357,12 +345,12 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         }
       };
       int j = c0;
-      for (; j + LA_AHEAD <= c1; j += LA_AHEAD) {
+      for (; j + AHEAD <= c1; j += AHEAD) {
 #pragma unroll
-        for (int i = 0; i < LA_AHEAD; ++i) step(j + i, qs[i], gn[i]);
+        for (int i = 0; i < AHEAD; ++i) step(j + i, qs[i], gn[i]);
       }
 #pragma unroll
-      for (int i = 0; i < LA_AHEAD - 1; ++i)
+      for (int i = 0; i < AHEAD - 1; ++i)
         if (j + i < c1) step(j + i, qs[i], gn[i]);
     };
     if (strip == 0) run(std::integral_constant<int, 0>{});
@@ -378,7 +366,7 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
   const int tid = threadIdx.x;
   struct Rows {
     u32x4 x[XP], y[YP];
-  } ahead[LA_AHEAD];
+  } ahead[AHEAD];
   const E *const xp = (const E *)(rev ? p.dir[1].x : p.dir[0].x) + row0 * p.dk;
   const E *const yp = (const E *)(rev ? p.dir[1].y : p.dir[0].y) + row0 * p.dv;
   auto load = [&](Rows &to, int j) {
@@ -456,7 +444,7 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
   const size_t ssize = (size_t)p.dk * p.dv;
   if (c0 < c1) {
 #pragma unroll
-    for (int i = 0; i < LA_AHEAD; ++i) load(ahead[i], within(c0 + i));
+    for (int i = 0; i < AHEAD; ++i) load(ahead[i], within(c0 + i));
   }
   if (seg == 0) {
     const bool copied = MODE != LA_ENDS && p.segs > 1 && c1 < nch;
@@ -482,17 +470,14 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         for (int c = 0; c < NC; ++c) store4(d + (16 * c + li) * LDX + 16 * (wave * RT + i) + 4 * g, acc[i][c]);
     }
     if constexpr (MODE == LA_STORE) {
-      const int chunk = first_token(j) / C;
-      if (rev ? (chunk + 1) % p.group == 0 || chunk == nch - 1 : chunk % p.group == 0) {
-        E *const to = (E *)dir.states + ((size_t)h * p.slots + slot0 + chunk / p.group) * ssize;
+      E *const to = (E *)dir.states + ((size_t)h * p.slots + slot0 + first_token(j) / C) * ssize;
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const int r = 16 * (wave * RT + i) + 4 * g, col = col0 + 16 * c + li;
-            if (r < p.dk && col < p.dv) store4(to + (size_t)col * p.dk + r, acc[i][c]);
-          }
-      }
+        for (int c = 0; c < NC; ++c) {
+          const int r = 16 * (wave * RT + i) + 4 * g, col = col0 + 16 * c + li;
+          if (r < p.dk && col < p.dv) store4(to + (size_t)col * p.dk + r, acc[i][c]);
+        }
     }
   };
   double total = 0.0;
@@ -502,7 +487,7 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
     scales(c0, f);
     put(ahead[0], c0, f);
     publish(c0);
-    load(ahead[0], within(c0 + LA_AHEAD));
+    load(ahead[0], within(c0 + AHEAD));
   }
 
   auto step = [&](int j, Rows &next) {  // next: chunk j + 1's rows
@@ -513,20 +498,24 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
     const float f = d.all;
     Scale fs;
     scales(within(j + 1), fs);
-    Op w[L::TERMS][NC], a[RT];
-    auto operands = [&](int kb) {
+    constexpr int CW = NC < 2 ? NC : 2;  // column tiles whose operands are held at a time
+    Op w[L::TERMS][CW], a[RT];
+    auto scaled = [&](int kb, int c0) {
 #pragma unroll
       for (int k = 0; k < L::TERMS; ++k)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) w[k][c] = L::tr(s_w[j & 1][k], LDY, kb, 16 * c, lane);
+        for (int c = 0; c < CW; ++c) w[k][c] = L::tr(s_w[j & 1][k], LDY, kb, 16 * (c0 + c), lane);
+    };
+    auto rows = [&](int kb) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) a[i] = L::tr(X, LDX, kb, 16 * (wave * RT + i), lane);
     };
-    operands(0);
+    scaled(0, 0);
+    rows(0);
     if (MODE == LA_ENDS) total += d.tot;
     __builtin_amdgcn_sched_barrier(0);
     put(next, j + 1, fs);  // behind the last chunk: into a buffer that nobody reads
-    load(next, within(j + 1 + LA_AHEAD));
+    load(next, within(j + 1 + AHEAD));
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -535,24 +524,28 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         for (int e = 0; e < 4; ++e) acc[i][c][e] *= f;
 #pragma unroll
     for (int kb = 0; kb < C; kb += KG) {
-      if (kb) operands(kb);
+      if (kb) rows(kb);
 #pragma unroll
-      for (int k = 0; k < L::TERMS; ++k)
+      for (int cc = 0; cc < NC; cc += CW) {
+        if (kb || cc) scaled(kb, cc);
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+        for (int k = 0; k < L::TERMS; ++k)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) acc[i][c] = Ops<E>::mma_grp(a[i], w[k][c], acc[i][c]);
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int c = 0; c < CW; ++c) acc[i][cc + c] = Ops<E>::mma_grp(a[i], w[k][c], acc[i][cc + c]);
+      }
     }
     if (j + 1 < c1) publish(j + 1);
   };
   int j = c0;
-  for (; j + LA_AHEAD <= c1; j += LA_AHEAD) {
+  for (; j + AHEAD <= c1; j += AHEAD) {
 #pragma unroll
-    for (int i = 0; i < LA_AHEAD; ++i) step(j + i, ahead[(i + 1) % LA_AHEAD]);
+    for (int i = 0; i < AHEAD; ++i) step(j + i, ahead[(i + 1) % AHEAD]);
   }
 #pragma unroll
-  for (int i = 0; i < LA_AHEAD - 1; ++i)
-    if (j + i < c1) step(j + i, ahead[(i + 1) % LA_AHEAD]);
+  for (int i = 0; i < AHEAD - 1; ++i)
+    if (j + i < c1) step(j + i, ahead[(i + 1) % AHEAD]);
   if constexpr (MODE == LA_ENDS) {
     float *const to = dir.seg_s + (nh * p.segs + seg) * ssize;
     each([&](float a, size_t at) { return to[at] = a; });
@@ -578,11 +571,11 @@ struct LaGradParams {
   int N, B, H, T, dk, dv, slots;
 };
 
-template <typename E, int DK, int C>
-__global__ __launch_bounds__(C * 4) void kla_la_grad_kernel(LaGradParams p) {
+template <typename E, int DK>
+__global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams p) {
   using L = La<E>;
   using Op = typename L::Op;
-  constexpr int KG = L::KG, VL = L::VL, NV = LA_NV, NS = C / 16, NT = 64 * NS;
+  constexpr int C = L::C, KG = L::KG, VL = L::VL, NV = LA_NV, NS = C / 16, NT = 64 * NS;
   constexpr int PAD = LdsPad<E>::V, LDX = DK + PAD, LDY = NV + PAD;
   constexpr int KS = DK / KG, RB = DK / 16, NC = NV / 16;
   __shared__ __attribute__((aligned(16))) E s_q[C * LDX], s_k[C * LDX], s_v[C * LDY], s_o[C * LDY], s_s[NV * LDX], s_m[NV * LDX];
@@ -620,13 +613,7 @@ __global__ __launch_bounds__(C * 4) void kla_la_grad_kernel(LaGradParams p) {
       b[i] = buffer_ld16(rk, at);
     }
     if (wave == 0) {
-      constexpr int NG = (C + 63) / 64;
-      float gl[NG];
-#pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const int t = 64 * i + lane;
-        gl[i] = t >= rows ? 0.f : p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + t]);
-      }
+      const float gl = lane >= rows ? 0.f : p.gfix ? p.gfix[h] : Elem<E>::to_f32(((const E *)p.g)[row0 + lane]);
       scan_decays<C>(&s_d, gl);
     }
 #pragma unroll
@@ -650,7 +637,7 @@ __global__ __launch_bounds__(C * 4) void kla_la_grad_kernel(LaGradParams p) {
 
   // a slice's rows and states: in registers while the one before it is in use
   constexpr int YP = C * NV / VL / NT, XT = NV * DK / VL, XP = (XT + NT - 1) / NT;
-  uint4 rv[YP], ro[YP], rs[XP], rm[XP];
+  u32x4 rv[YP], ro[YP], rs[XP], rm[XP];
   auto load = [&](int c0) {
     const int cols = min(NV, p.dv - c0);
     const __amdgpu_buffer_rsrc_t bv = buffer_rsrc((const E *)p.v + row0 * p.dv, rows * p.dv * (int)sizeof(E));
@@ -662,15 +649,15 @@ __global__ __launch_bounds__(C * 4) void kla_la_grad_kernel(LaGradParams p) {
     for (int i = 0; i < YP; ++i) {
       const int pc = tid + NT * i, r = pc / (NV / VL), c = c0 + pc % (NV / VL) * VL;
       const int at = c < p.dv ? (r * p.dv + c) * (int)sizeof(E) : 0x40000000;
-      rv[i] = buffer_ld16(bv, at);
-      ro[i] = buffer_ld16(bo, at);
+      rv[i] = __builtin_bit_cast(u32x4, buffer_ld16(bv, at));
+      ro[i] = __builtin_bit_cast(u32x4, buffer_ld16(bo, at));
     }
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
       const int pc = tid + NT * i, r = pc / (DK / VL), c = pc % (DK / VL) * VL;
       const int at = pc < XT && c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000;
-      rs[i] = buffer_ld16(bs, at);
-      rm[i] = buffer_ld16(bm, at);
+      rs[i] = __builtin_bit_cast(u32x4, buffer_ld16(bs, at));
+      rm[i] = __builtin_bit_cast(u32x4, buffer_ld16(bm, at));
     }
   };
   load(0);
@@ -679,23 +666,25 @@ __global__ __launch_bounds__(C * 4) void kla_la_grad_kernel(LaGradParams p) {
 #pragma unroll
     for (int i = 0; i < YP; ++i) {
       const int pc = tid + NT * i, at = pc / (NV / VL) * LDY + pc % (NV / VL) * VL;
-      *reinterpret_cast<uint4 *>(s_v + at) = rv[i];
-      *reinterpret_cast<uint4 *>(s_o + at) = ro[i];
+      *reinterpret_cast<u32x4 *>(s_v + at) = rv[i];
+      *reinterpret_cast<u32x4 *>(s_o + at) = ro[i];
     }
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
       const int pc = tid + NT * i, at = pc / (DK / VL) * LDX + pc % (DK / VL) * VL;
+      u32x4 x = rs[i], y = rm[i];
+      asm volatile("" : "+v"(x), "+v"(y));  // taken apart here, not where the loads are issued
       if (XT % NT == 0 || pc < XT) {
-        *reinterpret_cast<uint4 *>(s_s + at) = rs[i];
-        *reinterpret_cast<uint4 *>(s_m + at) = rm[i];
+        *reinterpret_cast<u32x4 *>(s_s + at) = x;
+        *reinterpret_cast<u32x4 *>(s_m + at) = y;
       }
       E a[VL], b[VL];
-      __builtin_memcpy(a, &rs[i], 16);
-      __builtin_memcpy(b, &rm[i], 16);
+      __builtin_memcpy(a, &x, 16);
+      __builtin_memcpy(b, &y, 16);
 #pragma unroll
       for (int e = 0; e < VL; ++e) dot = fmaf(Elem<E>::to_f32(a[e]), Elem<E>::to_f32(b[e]), dot);
     }
-    if (c0 + NV < p.dv) load(c0 + NV);
+    load(c0 + NV < p.dv ? c0 + NV : c0);  // (not under a condition: it would be waited for)
     lds_barrier();
     if (c0 == 0) {  // the scores of the wave's keys, once
 #pragma unroll
@@ -837,42 +826,27 @@ __global__ __launch_bounds__(C * 4) void kla_la_grad_kernel(LaGradParams p) {
   }
   __syncthreads();
   if (wave == 0) {
-    // 64 tokens at a time from the end, lane l token 63 - l of them, so that sums from a token
-    // on are prefix sums
-    constexpr int NG = (C + 63) / 64;
-    float dg[NG], behind[NG], x = 0.f, sum = 0.f, all = 0.f;
+    // lane l: token C - 1 - l, so that sums from a token on are prefix sums
+    const int t = C - 1 - lane;
+    float ahead = 0.f, before = 0.f, x = 0.f;
+    if (t >= 0) {
+      ahead = s_read[t];
+      before = s_write[t];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) ahead += s_row[i][t];
+    }
 #pragma unroll
     for (int i = 0; i < NS; ++i) x += s_dot[i];
-#pragma unroll
-    for (int u = NG - 1; u >= 0; --u) {
-      const int t = min(C, 64 * u + 64) - 1 - lane;
-      float ahead = 0.f, before = 0.f;
-      if (t >= 64 * u) {
-        ahead = s_read[t];
-        before = s_write[t];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) ahead += s_row[i][t];
-      }
-      dg[u] = wave_inclusive_scan(ahead) + sum;
-      behind[u] = wave_inclusive_scan(before) + all;
-      sum = lane_value(dg[u], 63);
-      all = lane_value(behind[u], 63);
-    }
-    float part = 0.f;
-#pragma unroll
-    for (int u = 0; u < NG; ++u) {
-      const int t = min(C, 64 * u + 64) - 1 - lane;
-      // writes in front of t: all of them less those from t on
-      const float d = dg[u] + (all - behind[u]) + s_d.all * x;
-      if (t >= 64 * u && t < rows) {
-        if (p.dg_chunk) part += d;
-        else ((E *)p.dg)[row0 + t] = Elem<E>::from_f32(d);
-      }
-    }
+    const float sum = wave_inclusive_scan(ahead), behind = wave_inclusive_scan(before);
+    // writes in front of t: all of them less those from t on
+    const float dg = sum + (lane_value(behind, 63) - behind) + s_d.all * x;
     if (p.dg_chunk) {
+      float v = t >= 0 && t < rows ? dg : 0.f;
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) part += __shfl_xor(part, off);
-      if (lane == 0) p.dg_chunk[(size_t)h * p.slots + slot] = part;
+      for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+      if (lane == 0) p.dg_chunk[(size_t)h * p.slots + slot] = v;
+    } else if (t >= 0 && t < rows) {
+      ((E *)p.dg)[row0 + t] = Elem<E>::from_f32(dg);
     }
   }
 }
@@ -961,31 +935,40 @@ __global__ __launch_bounds__(256) void kla_la_step_kernel(LaStepParams p) {
   }
 }
 
-template <typename E, int DK, int MODE>
-hipError_t launch_scan_t(const LaParams &p, hipStream_t st) {
-  hipLaunchKernelGGL((kla_la_scan_kernel<E, DK, MODE>), dim3(MODE == LA_OUT ? p.half : 2 * p.half), dim3(la_threads(MODE)), 0,
-                     st, p);
+// Workgroups of a scan's direction, in slices of NV columns.
+long long la_workgroups(long long seqs, int H, int segs, int dv, int NV) {
+  return (seqs * H * segs + 7) / 8 * 8 * ((dv + NV - 1) / NV);
+}
+
+template <typename E, int DK, int MODE, int NV>
+hipError_t launch_scan_t(LaParams p, int dirs, hipStream_t st) {
+  p.slices = (p.dv + NV - 1) / NV;
+  p.half = (unsigned)la_workgroups(p.N, p.H, p.segs, p.dv, NV);
+  hipLaunchKernelGGL((kla_la_scan_kernel<E, DK, MODE, NV>), dim3(dirs * p.half), dim3(la_threads(MODE)), 0, st, p);
   return hipGetLastError();
 }
+// Slices of 64 columns, which read x half as often, where they still make a workgroup to a CU and
+// where their rows, states and scaled values fit LDS (T=65536 dv=256 of 16 heads: 832 us, with 32
+// columns 1,025).  Not where states are stored, for which the registers do not suffice (16 packed
+// documents backward 685 us, with 32 columns 610).
 template <typename E, int MODE>
-hipError_t launch_scan(const LaParams &p, hipStream_t st) {
-  if (p.dk <= 64) return launch_scan_t<E, 64, MODE>(p, st);
-  if (p.dk <= 128) return launch_scan_t<E, 128, MODE>(p, st);
-  return launch_scan_t<E, 256, MODE>(p, st);
+hipError_t launch_scan(const LaParams &p, int dirs, hipStream_t st) {
+  if constexpr (sizeof(E) == 2 && MODE != LA_STORE) {
+    if (p.dk <= 128 && p.dv > LA_NV && dirs * la_workgroups(p.N, p.H, p.segs, p.dv, 2 * LA_NV) >= 256) {
+      if (p.dk <= 64) return launch_scan_t<E, 64, MODE, 2 * LA_NV>(p, dirs, st);
+      return launch_scan_t<E, 128, MODE, 2 * LA_NV>(p, dirs, st);
+    }
+  }
+  if (p.dk <= 64) return launch_scan_t<E, 64, MODE, LA_NV>(p, dirs, st);
+  if (p.dk <= 128) return launch_scan_t<E, 128, MODE, LA_NV>(p, dirs, st);
+  return launch_scan_t<E, 256, MODE, LA_NV>(p, dirs, st);
 }
 
 int la_chunk(int dtype) { return dtype == 0 ? La<bf16>::C : La<float>::C; }
 
-// Chunks to a state of the backward: two where the gradients' workgroup can hold them.
-int la_group(const LaArgs &a) { return a.dtype == 0 && a.dk <= 128 ? 2 : 1; }
-
 int la_slots(const LaArgs &a) {
-  const int C = la_chunk(a.dtype) * la_group(a);
+  const int C = la_chunk(a.dtype);
   return a.cu_seqlens ? a.T / C + a.num_seqs : a.num_seqs * ((a.T + C - 1) / C);
-}
-
-long long la_workgroups(const LaArgs &a, int segs) {
-  return ((long long)a.num_seqs * a.H * segs + 7) / 8 * 8 * ((a.dv + LA_NV - 1) / LA_NV);
 }
 
 // Segments of the scans, where their workgroups leave CUs idle: as many as make two rounds of
@@ -1045,10 +1028,7 @@ LaParams la_params(const LaArgs &a, const LaSpace &s) {
   p.T = a.T;
   p.dk = a.dk;
   p.dv = a.dv;
-  p.slices = (a.dv + LA_NV - 1) / LA_NV;
   la_segments(a, &p.segs, &p.seg_chunks);
-  p.half = (unsigned)la_workgroups(a, p.segs);
-  p.group = 1;
   for (int i = 0; i < 2; ++i) {
     p.dir[i].seg_s = (float *)(ws + s.seg_s[i]);
     p.dir[i].seg_g = (double *)(ws + s.seg_g[i]);
@@ -1060,38 +1040,25 @@ LaParams la_params(const LaArgs &a, const LaSpace &s) {
   return p;
 }
 
-// The segments' end states, of the forward direction or of both.
-template <typename E>
-hipError_t launch_ends(const LaParams &p, bool both, hipStream_t st) {
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(both ? 2 * p.half : p.half), dim3(la_threads(LA_ENDS)), 0, st, p);
-    return hipGetLastError();
-  };
-  if (p.dk <= 64) return go(kla_la_scan_kernel<E, 64, LA_ENDS>);
-  if (p.dk <= 128) return go(kla_la_scan_kernel<E, 128, LA_ENDS>);
-  return go(kla_la_scan_kernel<E, 256, LA_ENDS>);
-}
-
 template <typename E>
 hipError_t la_fwd_t(const LaArgs &a, hipStream_t st) {
   LaParams p = la_params(a, la_space(a, false));
   p.dir[0].send = a.final_state;
   if (p.segs > 1)
-    if (const hipError_t e = launch_ends<E>(p, false, st); e != hipSuccess) return e;
-  return launch_scan<E, LA_OUT>(p, st);
+    if (const hipError_t e = launch_scan<E, LA_ENDS>(p, 1, st); e != hipSuccess) return e;
+  return launch_scan<E, LA_OUT>(p, 1, st);
 }
 
-template <typename E, int DK, int C>
+template <typename E, int DK>
 hipError_t launch_grad_t(const LaGradParams &p, hipStream_t st) {
-  hipLaunchKernelGGL((kla_la_grad_kernel<E, DK, C>), dim3((unsigned)((long long)p.slots * p.H)), dim3(C * 4), 0, st, p);
+  hipLaunchKernelGGL((kla_la_grad_kernel<E, DK>), dim3((unsigned)((long long)p.slots * p.H)), dim3(La<E>::C * 4), 0, st, p);
   return hipGetLastError();
 }
 template <typename E>
 hipError_t launch_grad(const LaGradParams &p, hipStream_t st) {
-  constexpr bool B = sizeof(E) == 2;  // chunks: la_group
-  if (p.dk <= 64) return launch_grad_t<E, 64, B ? 128 : 32>(p, st);
-  if (p.dk <= 128) return launch_grad_t<E, 128, B ? 128 : 32>(p, st);
-  return launch_grad_t<E, 256, B ? 64 : 32>(p, st);
+  if (p.dk <= 64) return launch_grad_t<E, 64>(p, st);
+  if (p.dk <= 128) return launch_grad_t<E, 128>(p, st);
+  return launch_grad_t<E, 256>(p, st);
 }
 
 template <typename E>
@@ -1103,15 +1070,14 @@ hipError_t la_bwd_t(const LaArgs &a, const LaGrads &b, hipStream_t st) {
     return hipGetLastError();
   }
   LaParams p = la_params(a, s);
-  p.group = la_group(a);
   p.slots = la_slots(a);
   p.dir[1].x = a.q;
   p.dir[1].y = b.dout;
   p.dir[1].s0 = b.dfinal_state;
   p.dir[1].send = b.dinitial_state;
   hipError_t e;
-  if (p.segs > 1 && (e = launch_ends<E>(p, true, st)) != hipSuccess) return e;
-  if ((e = launch_scan<E, LA_STORE>(p, st)) != hipSuccess) return e;
+  if (p.segs > 1 && (e = launch_scan<E, LA_ENDS>(p, 2, st)) != hipSuccess) return e;
+  if ((e = launch_scan<E, LA_STORE>(p, 2, st)) != hipSuccess) return e;
   LaGradParams gp{};
   gp.q = a.q;
   gp.k = a.k;
