@@ -180,31 +180,29 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   float m = -INFINITY, l = 0.f;
 
   const int steps = end > lo ? (end - lo + BN - 1) / BN : 0;
-  // codes and scales of a tile as they are loaded; pages a tile ahead of them
+  // Codes and scales of a tile as they are loaded; pages a tile ahead of them.  Every load is made,
+  // from the first page where there is none: behind a branch the compiler waits for it there.
   u32x4 code[NP];
   unsigned scale[NP];
   int page[NP];
+  int state[NP];  // of a block: 0 cached, 1 past the end, 2 missing
   auto find = [&](int t) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int pos = lo + t * BN + (tid + 64 * NW * i) % (BN * PPK) / PPK;
-      page[i] = pos < end ? p.kv.table[(size_t)n * p.kv.max_pages + pos / p.kv.page] : -1;
+      const unsigned pos = min((unsigned)lo + t * BN + (tid + 64 * NW * i) % (BN * PPK) / PPK, (unsigned)end - 1);
+      page[i] = p.kv.table[(size_t)n * p.kv.max_pages + pos / (unsigned)p.kv.page];
     }
   };
   auto load = [&](int t) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int pc = tid + 64 * NW * i, j = pc / (BN * PPK), b = pc % PPK, pos = lo + t * BN + pc % (BN * PPK) / PPK;
+      const int pc = tid + 64 * NW * i, j = pc / (BN * PPK), b = pc % PPK;
+      const unsigned pos = (unsigned)lo + t * BN + pc % (BN * PPK) / PPK, last = end - 1;
       const bool there = page[i] >= 0 && page[i] < p.kv.num_pages;
-      code[i] = u32x4{0, 0, 0, 0};
-      scale[i] = 127;
-      if (there) {
-        const size_t at = (((size_t)page[i] * 2 + j) * p.kv.Hkv + head) * p.kv.page + pos % p.kv.page;
-        code[i] = *reinterpret_cast<const u32x4 *>(p.kv.codes + at * (D / 2) + 16 * b);
-        scale[i] = p.kv.scales[at * (D / 32) + b];
-      } else if (pos < end) {
-        scale[i] = 0x100 | 127;  // missing
-      }
+      state[i] = pos > last ? 1 : there ? 0 : 2;
+      const size_t at = (((size_t)(there ? page[i] : 0) * 2 + j) * p.kv.Hkv + head) * p.kv.page + min(pos, last) % (unsigned)p.kv.page;
+      code[i] = *reinterpret_cast<const u32x4 *>(p.kv.codes + at * (D / 2) + 16 * b);
+      scale[i] = p.kv.scales[at * (D / 32) + b];
     }
   };
   auto put = [&](int buf) {
@@ -212,37 +210,38 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
     for (int i = 0; i < NP; ++i) {
       const int pc = tid + 64 * NW * i, j = pc / (BN * PPK), key = pc % (BN * PPK) / PPK, b = pc % PPK;
       const int swz = j ? (key & 3) << 2 & (PPR - 1) : key & (PPR - 1);
-      const float s = __builtin_bit_cast(float, (scale[i] & 255) << 23);
+      asm volatile("" : "+v"(code[i]));
+      const float s = __builtin_bit_cast(float, state[i] ? 0x3f800000u : scale[i] << 23);
       bf16 *const to = s_kv[j][buf] + key * D;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         unsigned w[4];
-        cvt8(code[i][k], s, w);
+        cvt8(state[i] ? 0u : code[i][k], s, w);
         *reinterpret_cast<u32x4 *>(to + 8 * ((4 * b + k) ^ swz)) = u32x4{w[0], w[1], w[2], w[3]};
       }
-      if (j == 0 && b == 0 && key % 16 == 0) s_none[buf][key / 16] = scale[i] >> 8;
+      if (j == 0 && b == 0 && key % 16 == 0) s_none[buf][key / 16] = state[i] >> 1;
     }
   };
 
   if (steps > 0) {
     find(0);
     load(0);
-    if (steps > 1) find(1);
+    find(1);
   }
   bf16x8 q[KJ][NT];
 #pragma unroll
   for (int j = 0; j < KJ; ++j) q_terms<E, NT>((const E *)p.q + qrow * D + 16 * j + 8 * h, p.sign, q[j]);
   if (steps > 0) {
     put(0);
-    if (steps > 1) load(1);
-    if (steps > 2) find(2);
+    load(1);
+    find(2);
   }
   for (int t = 0; t < steps; ++t) {
     const int buf = t & 1;
     lds_barrier();
-    if (t + 1 < steps) put(buf ^ 1);
-    if (t + 2 < steps) load(t + 2);
-    if (t + 3 < steps) find(t + 3);
+    put(buf ^ 1);
+    load(t + 2);
+    find(t + 3);
     const int key0 = lo + t * BN;
     if (key0 > wlast || w0 >= rt.rows) continue;
     const bf16 *const kt = s_kv[0][buf], *const vt = s_kv[1][buf];
