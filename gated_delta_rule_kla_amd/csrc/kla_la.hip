@@ -24,10 +24,15 @@
 //          sum_{i >= t > j} D_ij (q_i . k_j)(do_i . v_j) + sum_{i >= t} (the state's part of q_i . dq_i)
 //          + sum_{j < t} (the later chunks' part of k_j . dk_j) + exp(tot) <M, S>
 //
+// The S and M of the chunks are kept in fp16 with powers of two, and rounded on to bf16 for the
+// products; <M, S>, which is most of dg where decays are weak, takes the fp16 values: from bf16
+// ones dg was off by 1.8 times what its own rounding to bf16 makes (16 heads, 26,339 tokens).
+//
 // (in dg every term is a sum of products that belong to it; the shorter form, q . dq - k . dk
 // summed from t to the sequence's end, loses what the terms have in common, and with operands of
 // eight bits little is left of it).
 #include <algorithm>
+#include <type_traits>
 
 #include "kla_common.h"
 #include "kla_internal.h"
@@ -46,6 +51,12 @@ template <typename E> struct La;
 template <> struct La<bf16> {
   static constexpr int C = 64, KG = 32, VL = 8, TERMS = 3;
   typedef bf16x8 Op;
+  typedef _Float16 Stored;
+  static __device__ __forceinline__ void store(_Float16 *p, f32x4 v, float unit) {
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<f16x4 *>(p) =
+        f16x4{(_Float16)(v[0] * unit), (_Float16)(v[1] * unit), (_Float16)(v[2] * unit), (_Float16)(v[3] * unit)};
+  }
   static __device__ __forceinline__ Op nat(const bf16 *row, int kb, int g) {
     return *reinterpret_cast<const bf16x8 *>(row + kb + 8 * g);
   }
@@ -63,6 +74,8 @@ template <> struct La<bf16> {
 template <> struct La<float> {
   static constexpr int C = 32, KG = 16, VL = 4, TERMS = 1;
   typedef f32x4 Op;
+  typedef float Stored;
+  static __device__ __forceinline__ void store(float *p, f32x4 v, float) { *reinterpret_cast<f32x4 *>(p) = v; }
   static __device__ __forceinline__ Op nat(const float *row, int kb, int g) {
     return *reinterpret_cast<const f32x4 *>(row + kb + 4 * g);
   }
@@ -138,13 +151,26 @@ __device__ __forceinline__ void scan_decays(Decays<C> *d, float g) {
   }
 }
 
+// The largest of a wave's numbers, in all lanes.
+__device__ __forceinline__ unsigned wave_max(unsigned v) {
+  auto step = [&](auto ctrl) { v = max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xF, 0xF, false)); };
+  step(std::integral_constant<int, 0x111>{});
+  step(std::integral_constant<int, 0x112>{});
+  step(std::integral_constant<int, 0x114>{});
+  step(std::integral_constant<int, 0x118>{});
+  const unsigned a = max((unsigned)__builtin_amdgcn_readlane((int)v, 15), (unsigned)__builtin_amdgcn_readlane((int)v, 31));
+  const unsigned b = max((unsigned)__builtin_amdgcn_readlane((int)v, 47), (unsigned)__builtin_amdgcn_readlane((int)v, 63));
+  return max(a, b);
+}
+
 // One direction of a scan: the factors of the state's updates (k, v; reverse: q, dout), the state
 // at the first processed chunk and behind the last.
 struct LaDir {
   const void *x, *y;
   const float *s0;  // or nullptr
   float *send;      // or nullptr
-  void *states;     // [H, slots, dv, dk] element type
+  void *states;     // [H, slots, dv, dk] fp32, or fp16 for bf16 elements
+  float *units;     // [H, slots, slices, 4] of the fp16 states: a power of two to each slice and wave
   float *seg_s;     // [N H segs, dk, dv] states behind all segments but the last; in the last's
                     // place the initial state (final_state may be the same memory)
   double *seg_g;    // [N H segs] log2 of their decays
@@ -470,13 +496,40 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
         for (int c = 0; c < NC; ++c) store4(d + (16 * c + li) * LDX + 16 * (wave * RT + i) + 4 * g, acc[i][c]);
     }
     if constexpr (MODE == LA_STORE) {
-      E *const to = (E *)dir.states + ((size_t)h * p.slots + slot0 + first_token(j) / C) * ssize;
+      const size_t place = (size_t)h * p.slots + slot0 + first_token(j) / C;
+      typedef typename L::Stored St;
+      St *const to = (St *)dir.states + place * ssize;
+      float unit = 1.f;
+      if constexpr (sizeof(E) == 2) {  // the largest finite magnitude becomes 2^14 to 2^15
+        unsigned top = 0;
+        auto largest = [&](bool finite) {
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x = acc[i][c][e];
+                const unsigned b = __builtin_bit_cast(unsigned, x) & 0x7fffffffu;
+                top = max(top, finite && b >= 0x7f800000u ? 0u : b);
+              }
+          top = wave_max(top);
+        };
+        largest(false);
+        if (top >= 0x7f800000u) {
+          top = 0;
+          largest(true);
+        }
+        const unsigned x = min(268u - (top >> 23), 253u);
+        unit = __builtin_bit_cast(float, x << 23);
+        if (lane == 0) dir.units[(place * p.slices + slice) * 4 + wave] = __builtin_bit_cast(float, (254u - x) << 23);
+      }
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const int r = 16 * (wave * RT + i) + 4 * g, col = col0 + 16 * c + li;
-          if (r < p.dk && col < p.dv) store4(to + (size_t)col * p.dk + r, acc[i][c]);
+          if (r < p.dk && col < p.dv) L::store(to + (size_t)col * p.dk + r, acc[i][c], unit);
         }
     }
   };
@@ -564,12 +617,33 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
 // LA_NV.
 struct LaGradParams {
   const void *q, *k, *v, *g, *dout, *states, *dstates;
+  const float *units, *dunits;
   const float *gfix;
   void *dq, *dk_, *dv_, *dg;
   float *dg_chunk;  // [H, slots] sums over a chunk's tokens, where decays are fixed
   const int32_t *cu;
   int N, B, H, T, dk, dv, slots;
 };
+
+// Eight fp16 values and their unit as bf16; the sum of eight products of such values.
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x4 restored(u32x4 s, float unit) {
+  const f16x8 a = __builtin_bit_cast(f16x8, s);
+  bf16x8 x;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = (bf16)((float)a[e] * unit);
+  return __builtin_bit_cast(u32x4, x);
+}
+__device__ __forceinline__ float dot8(u32x4 a, u32x4 b) {
+  float x = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const unsigned u = a[e], w = b[e];
+    x = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, u), __builtin_bit_cast(f16x2, w), x, false);
+  }
+  return x;
+}
 
 template <typename E, int DK>
 __global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams p) {
@@ -638,11 +712,14 @@ __global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams 
   // a slice's rows and states: in registers while the one before it is in use
   constexpr int YP = C * NV / VL / NT, XT = NV * DK / VL, XP = (XT + NT - 1) / NT;
   u32x4 rv[YP], ro[YP], rs[XP], rm[XP];
+  float us[XP], um[XP];  // units of the states
+  const size_t place = (size_t)h * p.slots + slot;
+  const int slices = (p.dv + NV - 1) / NV;
   auto load = [&](int c0) {
     const int cols = min(NV, p.dv - c0);
     const __amdgpu_buffer_rsrc_t bv = buffer_rsrc((const E *)p.v + row0 * p.dv, rows * p.dv * (int)sizeof(E));
     const __amdgpu_buffer_rsrc_t bo = buffer_rsrc((const E *)p.dout + row0 * p.dv, rows * p.dv * (int)sizeof(E));
-    const size_t at0 = ((size_t)h * p.slots + slot) * p.dk * p.dv + (size_t)c0 * p.dk;
+    const size_t at0 = place * p.dk * p.dv + (size_t)c0 * p.dk;
     const __amdgpu_buffer_rsrc_t bs = buffer_rsrc((const E *)p.states + at0, cols * p.dk * (int)sizeof(E));
     const __amdgpu_buffer_rsrc_t bm = buffer_rsrc((const E *)p.dstates + at0, cols * p.dk * (int)sizeof(E));
 #pragma unroll
@@ -658,6 +735,11 @@ __global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams 
       const int at = pc < XT && c < p.dk ? (r * p.dk + c) * (int)sizeof(E) : 0x40000000;
       rs[i] = __builtin_bit_cast(u32x4, buffer_ld16(bs, at));
       rm[i] = __builtin_bit_cast(u32x4, buffer_ld16(bm, at));
+      if constexpr (sizeof(E) == 2) {
+        const size_t u = (place * slices + c0 / NV) * 4 + c / (DK / 4);
+        us[i] = p.units[u];
+        um[i] = p.dunits[u];
+      }
     }
   };
   load(0);
@@ -674,15 +756,21 @@ __global__ __launch_bounds__(La<E>::C * 4) void kla_la_grad_kernel(LaGradParams 
       const int pc = tid + NT * i, at = pc / (DK / VL) * LDX + pc % (DK / VL) * VL;
       u32x4 x = rs[i], y = rm[i];
       asm volatile("" : "+v"(x), "+v"(y));  // taken apart here, not where the loads are issued
+      if constexpr (sizeof(E) == 2) {
+        dot = fmaf(dot8(x, y) * us[i], um[i], dot);
+        x = restored(x, us[i]);
+        y = restored(y, um[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VL; ++e) {
+          const unsigned a = x[e], b = y[e];
+          dot = fmaf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b), dot);
+        }
+      }
       if (XT % NT == 0 || pc < XT) {
         *reinterpret_cast<u32x4 *>(s_s + at) = x;
         *reinterpret_cast<u32x4 *>(s_m + at) = y;
       }
-      E a[VL], b[VL];
-      __builtin_memcpy(a, &x, 16);
-      __builtin_memcpy(b, &y, 16);
-#pragma unroll
-      for (int e = 0; e < VL; ++e) dot = fmaf(Elem<E>::to_f32(a[e]), Elem<E>::to_f32(b[e]), dot);
     }
     load(c0 + NV < p.dv ? c0 + NV : c0);  // (not under a condition: it would be waited for)
     lds_barrier();
@@ -987,9 +1075,10 @@ void la_segments(const LaArgs &a, int *segs, int *chunks) {
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 // The workspace: the segments' states and decays (backward: of both directions); the backward's
-// states and gradients of states of all chunks, and the fixed decays' partial sums.
+// states and gradients of states of all chunks with their units, and the fixed decays' partial
+// sums.
 struct LaSpace {
-  size_t seg_s[2], seg_g[2], states[2], dg, total;
+  size_t seg_s[2], seg_g[2], states[2], units[2], dg, total;
 };
 LaSpace la_space(const LaArgs &a, bool bwd) {
   int segs, chunks;
@@ -1008,7 +1097,10 @@ LaSpace la_space(const LaArgs &a, bool bwd) {
   }
   if (bwd) {
     const size_t n = (size_t)la_slots(a) * a.H;
-    for (int i = 0; i < 2; ++i) s.states[i] = take(n * state * (a.dtype == 0 ? 2 : 4));
+    for (int i = 0; i < 2; ++i) {
+      s.states[i] = take(n * state * (a.dtype == 0 ? 2 : 4));
+      s.units[i] = take(a.dtype == 0 ? n * ((a.dv + LA_NV - 1) / LA_NV) * 4 * sizeof(float) : 0);
+    }
     s.dg = take(n * sizeof(float));
   }
   s.total = at;
@@ -1033,6 +1125,7 @@ LaParams la_params(const LaArgs &a, const LaSpace &s) {
     p.dir[i].seg_s = (float *)(ws + s.seg_s[i]);
     p.dir[i].seg_g = (double *)(ws + s.seg_g[i]);
     p.dir[i].states = ws + s.states[i];
+    p.dir[i].units = (float *)(ws + s.units[i]);
   }
   p.dir[0].x = a.k;
   p.dir[0].y = a.v;
@@ -1087,6 +1180,8 @@ hipError_t la_bwd_t(const LaArgs &a, const LaGrads &b, hipStream_t st) {
   gp.dout = b.dout;
   gp.states = p.dir[0].states;
   gp.dstates = p.dir[1].states;
+  gp.units = p.dir[0].units;
+  gp.dunits = p.dir[1].units;
   gp.dq = b.dq;
   gp.dk_ = b.dk;
   gp.dv_ = b.dv;
