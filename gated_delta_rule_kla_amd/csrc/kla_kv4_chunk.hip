@@ -8,9 +8,9 @@
 // group's G, token i.  A workgroup takes a tile of a sequence's rows and a run of its keys; its
 // waves hold 32 rows each and share tiles of keys and values in LDS, converted to bf16 on the
 // way (exact: four significand bits and a power of two), 32 channels and their scale to a
-// thread.  The products, the running maximum and sum, and the layouts are kla_attn.hip's.  Keys are split
-// over workgroups where the rows alone leave CUs idle: each run then leaves its maximum, sum and
-// unnormalised output, which a second kernel joins.
+// thread.  The products, the running maximum and sum, and the layouts are kla_attn.hip's.  Keys are
+// split over workgroups where the rows alone leave CUs idle: each run then leaves its maximum, sum
+// and unnormalised output, which a second kernel joins.
 #include <algorithm>
 #include <cmath>
 
@@ -141,7 +141,9 @@ __device__ void attend_row(const KvChunkParams &p, const E *q, int n, int head, 
   *l_ = l;
 }
 
-// Tiles of BN keys, 32 rows to a wave.
+// Tiles of BN keys, 32 rows to a wave.  2,048 new tokens behind 60,000, 16 heads over 2: 1,005 us,
+// 1.02 PFLOP/s.  Bound: the vector ALU (softmax, conversions and addresses, about as many issue
+// cycles as the matrix products take) beside a clock that falls with the matrix cores' use.
 template <typename E, int D, int NW, int BN>
 __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;           // bf16 terms of q and of the weights
@@ -384,7 +386,10 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
 // the single-token kernel (kla_kv4.hip): K's codes become operands as they arrive, lane (r, c)
 // holding channels c D/4 and up of key r; the scores have keys 4 c + i of the two 16-key halves
 // in a lane's registers and rows along the lanes, and so are the second product's operand as
-// they stand; V goes through the wave's own LDS in 4 bits.  Bound: HBM, and the conversions, which all row blocks share.
+// they stand; V goes through the wave's own LDS in 4 bits.  64 sequences of 4,096 to 16,384 cached
+// tokens (326 MB) and five new ones, 16 heads over 4: 109 us, 3.0 TB/s.  Bound: the vector ALU, about
+// 270 instructions per tile of 32 keys, the conversions 64 of them, which all row blocks share;
+// the softmax over tiles that the new tokens fill to five eighths.
 template <typename E, int D, int RB, bool ONCE>
 __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;  // bf16 terms of q and of the weights
@@ -751,6 +756,7 @@ __device__ __forceinline__ float weigh_base(float lse, bool there) {
 // (lane (r, h): channels h D/2 and up of key r, eight to a product, q's taken in the same
 // order).  The waves take the rows in turn, 32 at a time, the next ones' loads ahead, and keep sums
 // with rows along the lanes until the end.
+// Bound: latency: the keys' operands are made once for all rows, by every wave.
 template <typename E, int D>
 __global__ __launch_bounds__(256) void kla_kv4_weigh_kernel(KvWeighParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3, KJ = D / 16, KB = 2;
@@ -882,7 +888,9 @@ __global__ __launch_bounds__(256) void kla_kv4_weigh_kernel(KvWeighParams p) {
 // Few rows: 16 RB of them stay in registers as left operands and the keys stream past, 32 at a
 // time to each of four waves (lane (r, c): channels c D/4 and up of keys r and 16 + r).  A score
 // tile has a row in each register and keys along the lanes, so a key's sum is additions within
-// a lane and two exchanges.  More rows than that: the keys again for the next ones.
+// a lane and two exchanges.  More rows than that: the keys again for the next ones.  64 sequences
+// of 4,096 to 16,384 cached tokens, one new one: 53 us.  Bound: HBM (K's codes and the weights in
+// and out, 3.4 TB/s) and the latency of a wave's few tiles.
 template <typename E, int D, int RB>
 __global__ __launch_bounds__(256) void kla_kv4_weigh_few_kernel(KvWeighParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3, KJ = D / 32, BM = 16 * RB;
@@ -1002,9 +1010,14 @@ __global__ __launch_bounds__(256) void kla_kv4_weigh_few_kernel(KvWeighParams p)
   }
 }
 
-// How a chunk call runs, by the rows of a sequence (the host's mean): tiles of 16 or 32 rows
-// where those are few, of 128 or 256 else; and runs of keys as many as make about 512
-// workgroups (few rows: 1,024), of 512 keys at least.
+// How a chunk call runs, by the rows of a sequence (the host's mean).  Up to 128 rows go in tiles
+// of 16 or 32: 64 sequences of 4,096 to 16,384 cached tokens, 16 heads over 4, with 24 new ones 318
+// us (256 rows to a tile: 359; fp32, 8 sequences: 83, in tiles of 128 rows 140).  More go in tiles of
+// 256, whose waves without rows only bring keys (40 new tokens 500 us, in tiles of 128 rows 735;
+// 100 new 905 against 1,287; 64 new, whose rows fill both, 872 against 771; one sequence of 60,000 and
+// 2,048 new ones 1,005 against 2,100); fp32 operands are three terms, and the registers hold 128.
+// Keys go in runs, as many as make about 512 workgroups (256: 1,143 us, 512: 1,163, 1,024: 1,194
+// where the rows alone make 256; with few rows 1,024), of 512 keys at least.
 struct ChunkPlan {
   int BM, slots, splits, per;
 };
@@ -1012,7 +1025,7 @@ ChunkPlan chunk_plan(const Kv4ChunkArgs &a) {
   const long long G = a.Hq / a.c.Hkv, seqs = std::max(a.N, 1);
   const long long rows = (long long)a.B * a.T * G, mean = (rows + seqs - 1) / seqs;
   ChunkPlan p;
-  p.BM = mean <= 16 || (mean <= 64 && a.dtype != 0) ? 16 : mean <= 64 ? 32 : mean <= 512 || a.dtype != 0 ? 128 : 256;
+  p.BM = mean <= 16 || (mean <= 128 && a.dtype != 0) ? 16 : mean <= 128 ? 32 : a.dtype != 0 ? 128 : 256;
   const long long tiles = a.cu ? (long long)a.T * G / p.BM + a.N : seqs * (((long long)a.T * G + p.BM - 1) / p.BM);
   p.slots = (int)std::min<long long>(tiles, 0x7fffffff);
   const long long busy = seqs * ((mean + p.BM - 1) / p.BM) * a.c.Hkv;
@@ -1030,7 +1043,7 @@ hipError_t launch_chunk(const KvChunkParams &p, int BM, hipStream_t st) {
   const dim3 grid((unsigned)((long long)p.slots * p.kv.Hkv * p.splits));
   auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, p); };
   // few rows: codes past the caches where those do not keep them from call to call anyway
-  // (kla_kv4.hip); two row blocks of fp32 queries would not fit the registers
+  // (kla_kv4.hip; 326 MB of codes and five new tokens 123 us, through the caches 125); two row blocks of fp32 queries would not fit the registers
   const bool once = (double)p.N * p.kv.Hkv * p.max_len * (D + D / 16) >= 96 << 20;
   if (BM == 16) {
     if (once) go(kla_kv4_rows_kernel<E, D, 1, true>, 256);
@@ -1039,8 +1052,6 @@ hipError_t launch_chunk(const KvChunkParams &p, int BM, hipStream_t st) {
     if (BM == 32) {
       if (once) go(kla_kv4_rows_kernel<E, D, 2, true>, 256);
       else go(kla_kv4_rows_kernel<E, D, 2, false>, 256);
-    } else if (BM == 128) {
-      go(kla_kv4_chunk_kernel<E, D, 4, 64>, 256);
     } else {
       go(kla_kv4_chunk_kernel<E, D, 8, 8192 / D>, 512);
     }
@@ -1055,7 +1066,12 @@ hipError_t launch_chunk(const KvChunkParams &p, int BM, hipStream_t st) {
 }
 
 // How the weights are made: rows of a sequence (the host's mean) that a wave holds, in blocks of
-// 16, with keys streaming past in runs; 0: more, with 64 keys to a workgroup.
+// 16, with keys streaming past in runs; 0: more, with 64 keys to a workgroup.  Up to 384 rows the
+// keys pass by for every 32 (64 sequences of 4,096 to 16,384 cached tokens, 16 heads over 4: one
+// new token 41 us against 666 with 64 keys to a workgroup, 24 new 163 against 710, 64 new 408
+// against 900; 8 such sequences, 64 new 98 against 122, 100 new 154 against 152, 200 new 286 against
+// 224).  fp32 rows are three terms, 16 of them at a time up to 128 (8 sequences, 24 new 77 against
+// 117, 64 new 193 against 174).
 struct WeighPlan {
   int RB, blocks, per;
 };
@@ -1063,7 +1079,7 @@ WeighPlan weigh_plan(const Kv4ChunkArgs &a) {
   const long long G = a.Hq / a.c.Hkv, seqs = std::max(a.N, 1);
   const long long mean = ((long long)a.B * a.T * G + seqs - 1) / seqs;
   WeighPlan p;
-  p.RB = mean <= 16 ? 1 : mean <= 32 && a.dtype == 0 ? 2 : 0;
+  p.RB = a.dtype == 0 ? mean <= 16 ? 1 : mean <= 384 ? 2 : 0 : mean <= 128 ? 1 : 0;
   p.per = 64;
   if (p.RB) {
     const long long want = std::max<long long>(1, 2048 / (seqs * a.c.Hkv)), len = (a.max_len + want - 1) / want;

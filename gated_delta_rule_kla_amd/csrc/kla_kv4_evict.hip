@@ -8,10 +8,11 @@
 // weight that stays, eleven bits of the weights' order at a time (a histogram in LDS per pass, wide
 // enough that a wave's tokens seldom meet in a bin; integer counts, so the order of the atomics
 // changes nothing); then each wave goes over its part of the tokens and writes the positions
-// that stay, at places counted ahead.  Few (sequence, head)s: the same in parts, over four launches.  Then the rows that change place go
-// to a workspace and from there to their places: kept rows move towards the front over rows that
-// others still have to read.
-// Bound: the choice by its passes over the weights (from L2), the moves by HBM.
+// that stay, at places counted ahead.  Few (sequence, head)s: the same in parts, over four
+// launches.  Then the rows that change place go to a workspace and from there to their places: kept
+// rows move towards the front over rows that others still have to read.
+// Bound: the choice by its passes over the weights (from L2), the moves by HBM (a batch's eviction
+// 250 us, 3.9 TB/s of what it has to move twice; one sequence of 131,071 tokens cut to 32,768 58 us).
 #include <algorithm>
 
 #include "kla_common.h"
@@ -386,7 +387,9 @@ __global__ __launch_bounds__(256) void kla_kv4_shift_kernel(KvEvictParams p, int
 int row_bytes(int D) { return D + 32; }  // codes, 2 D / 32 scales, the weight
 
 // Parts of a choice: one workgroup for all tokens of a (sequence, head), unless those are few
-// enough that parts of 4,096 tokens do not make more than 256.
+// enough that parts of 4,096 tokens do not make more than 256 (one sequence of 131,071 tokens and
+// two heads 59 us, in one piece 182; a batch of 64 sequences and four heads 193 us in one piece
+// each, in parts 259).
 int evict_parts(int N, int Hkv, long long room) {
   const long long pairs = (long long)N * Hkv, parts = (room + EV_PART - 1) / EV_PART;
   return parts > 2 && pairs * parts <= 256 ? (int)parts : 1;

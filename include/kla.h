@@ -554,9 +554,9 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
  * Supported: dk and dv multiples of 16 up to 256, either dtype.  Tokens go in chunks (64 in BF16,
  * 32 in F32).  With BF16 the scores q.k and the state that a chunk's outputs read are rounded to
  * bf16 once (half a step of 2^-8, as o itself is), the state is summed in fp32 from products of
- * 16 bits; F32 is fp32 throughout.  Where g > 0 makes a product of decays overflow fp32, outputs
- * are not finite even if the recurrence would be; a value that is not finite reaches all outputs
- * of its chunk, of its own and of later chunks, and no other sequence.  Sizes whose launch would
+ * 24 bits (three bf16 terms); F32 is fp32 throughout.  Where g > 0 makes a product of decays
+ * overflow fp32, outputs are not finite even if the recurrence would be; a value that is not finite
+ * reaches all outputs of its chunk, of its own and of later chunks, and no other sequence.  Sizes whose launch would
  * have more than 2^32 threads are refused (KLA_ERR_SHAPE).  Results repeat bit for bit.  Status
  * codes as kla_chunk_fwd.
  */
@@ -583,9 +583,10 @@ kla_status_t kla_la_chunk_fwd(const void *q, const void *k, const void *v, const
  *   dinitial_state  [N, H, dk, dv] fp32 (written), or NULL (not computed)
  *   workspace       kla_la_chunk_bwd_workspace_bytes(...) bytes
  *
- * Gradient buffers must not alias the inputs.  With BF16 each of the two states and of the two
- * matrices of scores is rounded to bf16 once; dg's terms are products with such roundings, summed
- * in fp32 (in 64 bits over a head).  Everything else as kla_la_chunk_fwd.
+ * Gradient buffers must not alias the inputs.  With BF16 each of the two
+ * matrices of scores is rounded to bf16 once, and each of the two states to fp16 (with a power of
+ * two to a part of it) and from there to bf16; dg's terms are products with such roundings, that of
+ * the two states with fp16's alone, summed in fp32 (in 64 bits over a head).  Everything else as kla_la_chunk_fwd.
  */
 kla_status_t kla_la_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const float *decay,
                               const float *initial_state, const void *dout, const float *dfinal_state,
@@ -597,7 +598,8 @@ kla_status_t kla_la_chunk_bwd(const void *q, const void *k, const void *v, const
 
 /* Device workspaces of kla_la_chunk_fwd and kla_la_chunk_bwd (host-only, no HIP call): where few
  * sequences and heads make the library cut long sequences into segments, a state per segment;
- * backward also two states per (chunk, head) in dtype and 4 bytes.  0 for arguments they would
+ * backward also two states per (chunk, head) in dtype, with 16 bytes per 32 columns where that is
+ * BF16, and 4 bytes.  0 for arguments they would
  * reject. */
 size_t kla_la_chunk_workspace_bytes(const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int num_seqs,
                                     int B, int H, int T, int dk, int dv, kla_dtype_t dtype);

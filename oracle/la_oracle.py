@@ -8,7 +8,7 @@ which the same recurrences give from |q|, |k|, |v|, |do| and the states' magnitu
 
 * `u`, a rounding of a factor to the element type (2^-8 for bf16, 0 for fp32, half a step): the
   scores or the state in o, dq, dk and dv; both states in dg;
-* the states themselves: u^2 (two terms of that type), and fp32 sums;
+* the states themselves: u^2 at most (three terms of that type), and fp32 sums;
 * fp32: every decay is a product of at most one factor per chunk and of a chunk's sum of
   log-decays, off by 4 U32 and U32 of its exponent each, and where that exponent is beyond 150 the
   term is nothing; sums over the channels and over a chunk's 64 tokens.
