@@ -737,8 +737,8 @@ size_t kla_attn_kv4_decode_workspace_bytes(int N, int Hq, int Hkv, int D, int ma
 
 /*
  * kla_attn_kv4_chunk_fwd -- causal softmax attention of each sequence's newest tokens over the
- * 4-bit cache, which holds them already (append them first): a chunk of a prompt, the tokens of a draft that
- * is verified, or one token.  With new = a sequence's queries, len = seq_lens[n], off = len - new:
+ * 4-bit cache, which holds them already (append them first): a chunk of a prompt, the tokens of a
+ * draft that is verified, or one token.  With new = a sequence's queries, len = seq_lens[n], off = len - new:
  *
  *     o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j),   j <= i + off
  *     lse_i = ln sum_j p_ij
