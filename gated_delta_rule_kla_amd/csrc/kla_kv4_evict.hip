@@ -11,8 +11,10 @@
 // that stay, at places counted ahead.  Few (sequence, head)s: the same in parts, over four
 // launches.  Then the rows that change place go to a workspace and from there to their places: kept
 // rows move towards the front over rows that others still have to read.
-// Bound: the choice by its passes over the weights (from L2), the moves by HBM (a batch's eviction
-// 250 us, 3.9 TB/s of what it has to move twice; one sequence of 131,071 tokens cut to 32,768 58 us).
+// Bound: the choice by its passes over the weights (from L2), the moves by HBM and the memory-side
+// cache, which holds the workspace in between: 64 sequences of 4,096 to 16,384 tokens and four heads
+// cut to 4,096 tokens, choice 30 us, rows out 34 (200 MB read) and in 25; one sequence of 131,071 and
+// two heads cut to 32,768, choice 39 in four launches, rows 5 and 5.
 #include <algorithm>
 
 #include "kla_common.h"
