@@ -141,8 +141,8 @@ __device__ void attend_row(const KvChunkParams &p, const E *q, int n, int head, 
   *l_ = l;
 }
 
-// Tiles of BN keys, 32 rows to a wave.  2,048 new tokens behind 60,000, 16 heads over 2: 1,005 us,
-// 1.02 PFLOP/s.  Bound: the vector ALU (softmax, conversions and addresses, about as many issue
+// Tiles of BN keys, 32 rows to a wave.  2,048 new tokens behind 60,000, 16 heads over 2: 971 us,
+// 1.06 PFLOP/s.  Bound: the vector ALU (softmax, conversions and addresses, about as many issue
 // cycles as the matrix products take) beside a clock that falls with the matrix cores' use.
 template <typename E, int D, int NW, int BN>
 __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams p) {
@@ -188,21 +188,40 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   unsigned scale[NP];
   int page[NP];
   int state[NP];  // of a block: 0 cached, 1 past the end, 2 missing
-  auto find = [&](int t) {
+  // a block's place in the table and in its page move on by a tile each time (with two divisions
+  // and three products of 64 bits instead 1,005 us)
+  int at_page[NP], at_row[NP], row_[NP];
+  size_t first[NP];  // of page 0
+  const size_t stride = (size_t)2 * p.kv.Hkv * p.kv.page;
+  const int by_page = BN / p.kv.page, by_row = BN % p.kv.page, last_page = (end - 1) / p.kv.page;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int pos = lo + (tid + 64 * NW * i) % (BN * PPK) / PPK;
+    at_page[i] = pos / p.kv.page;
+    at_row[i] = pos % p.kv.page;
+    first[i] = ((size_t)((tid + 64 * NW * i) / (BN * PPK)) * p.kv.Hkv + head) * p.kv.page;
+  }
+  auto find = [&] {  // the next tile's
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const unsigned pos = min((unsigned)lo + t * BN + (tid + 64 * NW * i) % (BN * PPK) / PPK, (unsigned)end - 1);
-      page[i] = p.kv.table[(size_t)n * p.kv.max_pages + pos / (unsigned)p.kv.page];
+      page[i] = p.kv.table[(size_t)n * p.kv.max_pages + min(at_page[i], last_page)];
+      row_[i] = at_row[i];
+      at_page[i] += by_page;
+      at_row[i] += by_row;
+      if (at_row[i] >= p.kv.page) {
+        at_row[i] -= p.kv.page;
+        ++at_page[i];
+      }
     }
   };
   auto load = [&](int t) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int pc = tid + 64 * NW * i, j = pc / (BN * PPK), b = pc % PPK;
+      const int pc = tid + 64 * NW * i, b = pc % PPK;
       const unsigned pos = (unsigned)lo + t * BN + pc % (BN * PPK) / PPK, last = end - 1;
       const bool there = page[i] >= 0 && page[i] < p.kv.num_pages;
       state[i] = pos > last ? 1 : there ? 0 : 2;
-      const size_t at = (((size_t)(there ? page[i] : 0) * 2 + j) * p.kv.Hkv + head) * p.kv.page + min(pos, last) % (unsigned)p.kv.page;
+      const size_t at = (unsigned)(there ? page[i] : 0) * stride + first[i] + row_[i];
       code[i] = *reinterpret_cast<const u32x4 *>(p.kv.codes + at * (D / 2) + 16 * b);
       scale[i] = p.kv.scales[at * (D / 32) + b];
     }
@@ -226,9 +245,9 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   };
 
   if (steps > 0) {
-    find(0);
+    find();
     load(0);
-    find(1);
+    find();
   }
   bf16x8 q[KJ][NT];
 #pragma unroll
@@ -236,14 +255,14 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   if (steps > 0) {
     put(0);
     load(1);
-    find(2);
+    find();
   }
   for (int t = 0; t < steps; ++t) {
     const int buf = t & 1;
     lds_barrier();
     put(buf ^ 1);
     load(t + 2);
-    find(t + 3);
+    find();
     const int key0 = lo + t * BN;
     if (key0 > wlast || w0 >= rt.rows) continue;
     const bf16 *const kt = s_kv[0][buf], *const vt = s_kv[1][buf];
