@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "kla_common.h"
+#include "kla_index.h"
 #include "kla_internal.h"
 #include "kla_kv4.h"
 
@@ -382,7 +383,7 @@ __global__ __launch_bounds__(256) void kla_kv4_shift_kernel(KvEvictParams p, int
     }
   }
   if constexpr (!TAKE) {
-    for (int i = p.budget + block * 256 + threadIdx.x; i < len; i += blocks * 256) w[i] = 0.f;
+    each_position(p.budget, len, block, blocks, threadIdx.x, [&](long long i) { w[i] = 0.f; });
   }
 }
 
