@@ -14,4 +14,10 @@ __host__ __device__ __forceinline__ void each_position(int from, int to, int blo
   for (long long i = from + block * 256LL + thread; i < to; i += blocks * 256LL) f(i);
 }
 
+// f(place) for the bits that are set, the lowest first.
+template <class F>
+__host__ __device__ __forceinline__ void each_bit(unsigned bits, F f) {
+  for (; bits; bits &= bits - 1) f(__builtin_ctz(bits));
+}
+
 }  // namespace kla

@@ -16,6 +16,7 @@
 
 #include "kla_attn_tile.h"
 #include "kla_common.h"
+#include "kla_index.h"
 #include "kla_internal.h"
 #include "kla_kv4.h"
 #include "kla_ops.h"
@@ -428,7 +429,7 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
   int *const s_page = lds.t.page;
-  __shared__ int s_bad;
+  __shared__ unsigned s_bad;
   __shared__ size_t s_row[BM];  // places of the tile's rows among the queries
 
   unsigned id = blockIdx.x;
@@ -670,7 +671,7 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
         float oo = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) oo = fmaf(lds.j.o[w][g][e], lds.j.f[w][g], oo);
-        if (!(fabsf(fmaf(oo, 0.f, ll)) < INFINITY)) atomicOr(&s_bad, 1 << (16 * b + g));
+        if (!(fabsf(fmaf(oo, 0.f, ll)) < INFINITY)) atomicOr(&s_bad, 1u << (16 * b + g));
         const size_t qr = s_row[16 * b + g], part = qr * p.splits + split;
         if (p.splits == 1) {
           ((E *)p.o)[qr * D + d] = Elem<E>::from_f32(ll == 0.f ? 0.f : oo / ll);
@@ -687,10 +688,9 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   }
   // rows whose results are not finite, again from the keys that they see alone, one by one
   __syncthreads();
-  int bad = __builtin_amdgcn_readfirstlane(s_bad);
-  for (int i = 0; bad; ++i, bad &= bad - 1) {
-    if (i % 4 != wave) continue;
-    const int at = __builtin_ctz(bad);
+  int i = 0;
+  each_bit((unsigned)__builtin_amdgcn_readfirstlane((int)s_bad), [&](int at) {
+    if (i++ % 4 != wave) return;
     const size_t qr = s_row[at], part = qr * p.splits + split;
     constexpr int CPL = D / 64;
     float rm, rl, a[CPL];
@@ -708,7 +708,7 @@ __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
         p.lse[qr] = rl == 0.f ? -INFINITY : (rm + __builtin_amdgcn_logf(rl)) * 0.693147181f;
       }
     }
-  }
+  });
 }
 
 // The runs of one query: D / 4 lanes to a row.

@@ -50,6 +50,17 @@ int main() {
   for (int budget : {1, 4096, 250000000, 1 << 29, (1 << 29) + 1, 1 << 30, most - 1})
     for (int len : {1200000000, most - 100, most})
       if (len > budget) positions(budget, len);
+  // the rows of a tile, the 32nd among them
+  for (unsigned bits : {0u, 1u, 0x80000000u, 0x80010001u, 0xffffffffu, 0x12345678u}) {
+    unsigned seen = 0;
+    int last = -1;
+    kla::each_bit(bits, [&](int i) {
+      expect("bit", i > last && i < 32, i, last);
+      seen |= 1u << i;
+      last = i;
+    });
+    expect("bits", seen == bits, seen, bits);
+  }
   printf("ok: %d failure(s)\n", failures);
   return failures != 0;
 }
