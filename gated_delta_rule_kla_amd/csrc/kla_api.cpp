@@ -860,7 +860,7 @@ kla_status_t kla_kv4_evict(void *codes, void *scales, const int32_t *block_table
       misaligned(weights) || misaligned4(new_lens) || misaligned4(kept) || misaligned(workspace))
     return KLA_ERR_ALIGN;
   const size_t need = kla::kv4_evict_workspace_bytes(num_seqs, Hkv, D, budget, (long long)max_pages * page_size);
-  if (workspace == nullptr || workspace_bytes < need) return KLA_ERR_WORKSPACE;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KLA_ERR_WORKSPACE;
   const kla::Kv4Cache c{codes, scales, block_table, num_pages, page_size, max_pages, Hkv};
   return from_hip(kla::launch_kv4_evict(c, seq_lens, new_lens, kept, weights, num_seqs, D, max_tokens, budget, recent,
                                         workspace, reinterpret_cast<hipStream_t>(stream)));

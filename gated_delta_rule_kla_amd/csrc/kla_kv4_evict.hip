@@ -402,6 +402,7 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 size_t kv4_evict_workspace_bytes(int N, int Hkv, int D, int budget, long long room) {
+  if (budget >= room) return 0;  // nothing can be cut
   const size_t pairs = (size_t)N * Hkv, parts = evict_parts(N, Hkv, room);
   return up(pairs * budget * row_bytes(D)) + (parts > 1 ? pairs * (3 * parts * EV_BINS + 6 + 2 * parts) * sizeof(unsigned) : 0);
 }
@@ -417,18 +418,22 @@ hipError_t launch_kv4_evict(const Kv4Cache &c, const int32_t *lens, int32_t *new
   KvEvictParams p{kv_params(c), lens, new_lens, kept, weights, N, D, W, budget, recent, (u32x4 *)workspace,
                   row_bytes(D)};
   p.parts = evict_parts(N, c.Hkv, room);
+  const bool cut = budget < room;  // else the choice only says what is there
   if (p.parts > 1) {
-    p.hist = (unsigned *)((char *)workspace + up(pairs * budget * row_bytes(D)));
-    p.state = p.hist + pairs * 3 * p.parts * EV_BINS;
-    p.above = p.state + pairs * 6;
     const dim3 grid((unsigned)(pairs * p.parts));
-    hipLaunchKernelGGL((kla_kv4_choose_part_kernel<0>), grid, dim3(EV_PT), 0, st, p);
-    hipLaunchKernelGGL((kla_kv4_choose_part_kernel<1>), grid, dim3(EV_PT), 0, st, p);
-    hipLaunchKernelGGL((kla_kv4_choose_part_kernel<2>), grid, dim3(EV_PT), 0, st, p);
+    if (cut) {
+      p.hist = (unsigned *)((char *)workspace + up(pairs * budget * row_bytes(D)));
+      p.state = p.hist + pairs * 3 * p.parts * EV_BINS;
+      p.above = p.state + pairs * 6;
+      hipLaunchKernelGGL((kla_kv4_choose_part_kernel<0>), grid, dim3(EV_PT), 0, st, p);
+      hipLaunchKernelGGL((kla_kv4_choose_part_kernel<1>), grid, dim3(EV_PT), 0, st, p);
+      hipLaunchKernelGGL((kla_kv4_choose_part_kernel<2>), grid, dim3(EV_PT), 0, st, p);
+    }
     hipLaunchKernelGGL((kla_kv4_choose_part_kernel<3>), grid, dim3(EV_PT), 0, st, p);
   } else {
     hipLaunchKernelGGL(kla_kv4_choose_kernel, dim3((unsigned)pairs), dim3(EV_T), 0, st, p);
   }
+  if (!cut) return hipGetLastError();
   const int blocks = (budget + 63) / 64;
   const dim3 grid((unsigned)(pairs * blocks));
   if (D == 128) {

@@ -817,7 +817,7 @@ kla_status_t kla_attn_kv4_weigh(const void *q, const float *lse, const void *cod
  *   kept        device int32 [N, Hkv, budget] (written): the former position of each token that
  *               stays, -1 behind a shorter sequence's
  *   budget      at least 1;  recent  in [0, budget]  (else KLA_ERR_PARAM)
- *   workspace   kla_kv4_evict_workspace_bytes(...) bytes
+ *   workspace   kla_kv4_evict_workspace_bytes(...) bytes (NULL when that is 0)
  *   others as kla_kv4_append
  *
  * A page in use by two sequences must not be cut.  A token of a missing page moves as zero, one
@@ -829,7 +829,8 @@ kla_status_t kla_kv4_evict(void *codes, void *scales, const int32_t *block_table
                            int max_tokens, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Device workspace of kla_kv4_evict (host-only, no HIP call): D + 32 bytes per sequence, key head
- * and token of the budget, and for few sequences of many tokens 24 KiB per 4,096 of those; 0 for
+ * and token of the budget, and for few sequences of many tokens 24 KiB per 4,096 of those; 0 where
+ * the budget covers all that the block table has room for, since nothing is cut then, and for
  * arguments it would reject. */
 size_t kla_kv4_evict_workspace_bytes(int num_seqs, int Hkv, int D, int budget, int page_size, int max_pages);
 
