@@ -751,8 +751,8 @@ struct KvWeighParams {
   const int32_t *lens, *cu;
   float c;  // scale log2(e)
   float *w;
-  int N, B, Hq, G, T, W;
-  int max_len, blocks, per;  // workgroups of a sequence, keys of one
+  int N, Hq, G, T, W;
+  int max_len, per;  // keys of a workgroup
 };
 
 // A sequence's queries and keys.
@@ -958,7 +958,6 @@ __global__ __launch_bounds__(256) void kla_kv4_weigh_few_kernel(KvWeighParams p)
         lim[b][i] = base[b][i] < INFINITY ? ti + s.off : -1;
       }
     }
-    const int all = s.off + (int)(row0 / p.G);  // the last key that the first row sees
     struct Tile {
       unsigned k[2][KJ];
       unsigned sc[2];
@@ -1163,18 +1162,16 @@ hipError_t launch_attn_kv4_weigh(const Kv4ChunkArgs &a, float *weights, int W, h
   p.c = a.scale * 1.44269504f;
   p.w = weights;
   p.N = a.N;
-  p.B = a.B;
   p.Hq = a.Hq;
   p.G = a.Hq / a.c.Hkv;
   p.T = a.T;
   p.W = W;
   p.max_len = a.max_len;
   const WeighPlan plan = weigh_plan(a);
-  p.blocks = plan.blocks;
   p.per = plan.per;
   if (a.max_len == 0) return hipSuccess;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((long long)p.blocks * p.N * a.c.Hkv)), dim3(256), 0, st, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((long long)plan.blocks * p.N * a.c.Hkv)), dim3(256), 0, st, p);
     return hipGetLastError();
   };
   if (a.dtype == 0) {

@@ -626,7 +626,7 @@ struct LaGradParams {
   void *dq, *dk_, *dv_, *dg;
   float *dg_chunk;  // [H, slots] sums over a chunk's tokens, where decays are fixed
   const int32_t *cu;
-  int N, B, H, T, dk, dv, slots;
+  int N, H, T, dk, dv, slots;
 };
 
 // Eight fp16 values and their unit as bf16; the sum of eight products of such values.
