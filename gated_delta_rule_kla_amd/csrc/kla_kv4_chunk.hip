@@ -142,9 +142,10 @@ __device__ void attend_row(const KvChunkParams &p, const E *q, int n, int head, 
   *l_ = l;
 }
 
-// Tiles of BN keys, 32 rows to a wave.  2,048 new tokens behind 60,000, 16 heads over 2: 971 us,
-// 1.06 PFLOP/s.  Bound: the vector ALU (softmax, conversions and addresses, about as many issue
-// cycles as the matrix products take) beside a clock that falls with the matrix cores' use.
+// Tiles of BN keys, 32 rows to a wave.  2,048 new tokens behind 60,000, 16 heads over 2: 971 to
+// 1,004 us, 1.02 to 1.06 PFLOP/s.  Bound: the vector ALU (softmax, conversions and addresses, about
+// as many issue cycles as the matrix products take) beside a clock that falls with the matrix
+// cores' use.
 template <typename E, int D, int NW, int BN>
 __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;           // bf16 terms of q and of the weights
@@ -189,8 +190,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   unsigned scale[NP];
   int page[NP];
   int state[NP];  // of a block: 0 cached, 1 past the end, 2 missing
-  // a block's place in the table and in its page move on by a tile each time (with two divisions
-  // and three products of 64 bits instead 1,005 us)
+  // a block's place in the table and in its page move on by a tile each time (one box: 971 us; with
+  // two divisions and three products of 64 bits a tile instead 1,005)
   int at_page[NP], at_row[NP], row_[NP];
   size_t first[NP];  // of page 0
   const size_t stride = (size_t)2 * p.kv.Hkv * p.kv.page;
@@ -400,16 +401,16 @@ __global__ __launch_bounds__(64 * NW, 1) void kla_kv4_chunk_kernel(KvChunkParams
   }
 }
 
-// Few rows (a draft's tokens, single tokens): 16 RB rows of a sequence and key head to a
-// workgroup, and a run of keys, of which its four waves take tiles of 32 in turn, each with its
-// own running maximum, sum and output; nothing is shared until the end.  Layouts are those of
-// the single-token kernel (kla_kv4.hip): K's codes become operands as they arrive, lane (r, c)
-// holding channels c D/4 and up of key r; the scores have keys 4 c + i of the two 16-key halves
-// in a lane's registers and rows along the lanes, and so are the second product's operand as
-// they stand; V goes through the wave's own LDS in 4 bits.  64 sequences of 4,096 to 16,384 cached
-// tokens (326 MB) and five new ones, 16 heads over 4: 109 us, 3.0 TB/s.  Bound: the vector ALU, about
-// 270 instructions per tile of 32 keys, the conversions 64 of them, which all row blocks share;
-// the softmax over tiles that the new tokens fill to five eighths.
+// Few rows (a draft's tokens, single tokens): 16 RB rows of a sequence and key head to a workgroup,
+// and a run of keys, of which its four waves take tiles of 32 in turn, each with its own running
+// maximum, sum and output; nothing is shared until the end.  Layouts are those of the single-token
+// kernel (kla_kv4.hip): K's codes become operands as they arrive, lane (r, c) holding channels c
+// D/4 and up of key r; the scores have keys 4 c + i of the two 16-key halves in a lane's registers
+// and rows along the lanes, and so are the second product's operand as they stand; V goes through
+// the wave's own LDS in 4 bits.  64 sequences of 4,096 to 16,384 cached tokens (326 MB) and five
+// new ones, 16 heads over 4: 109 to 117 us, 3.0 TB/s.  Bound: the vector ALU, about 270
+// instructions per tile of 32 keys, the conversions 64 of them, which all row blocks share; the
+// softmax over tiles that the new tokens fill to five eighths.
 template <typename E, int D, int RB, bool ONCE>
 __global__ __launch_bounds__(256, 2) void kla_kv4_rows_kernel(KvChunkParams p) {
   constexpr int NT = sizeof(E) == 2 ? 1 : 3;  // bf16 terms of q and of the weights
@@ -766,7 +767,8 @@ __device__ __forceinline__ WeighSpan weigh_span(const KvWeighParams &p, int n) {
   const int len = max(p.lens[n], 0);
   return {t0, lq, len - lq, readable(p.kv, len, p.max_len), (p.cu ? 0 : (size_t)n) * p.Hq * p.T + t0};
 }
-// log2(e) lse of a row, infinite where it gives nothing: past the end, or with a query that sees nothing
+// log2(e) lse of a row, infinite where it gives nothing: past the end, or with a query that sees
+// nothing
 __device__ __forceinline__ float weigh_base(float lse, bool there) {
   return there && fabsf(lse) < INFINITY ? lse * 1.44269504f : INFINITY;
 }
@@ -908,7 +910,7 @@ __global__ __launch_bounds__(256) void kla_kv4_weigh_kernel(KvWeighParams p) {
 // time to each of four waves (lane (r, c): channels c D/4 and up of keys r and 16 + r).  A score
 // tile has a row in each register and keys along the lanes, so a key's sum is additions within
 // a lane and two exchanges.  More rows than that: the keys again for the next ones.  64 sequences
-// of 4,096 to 16,384 cached tokens, one new one: 53 us.  Bound: HBM (K's codes and the weights in
+// of 4,096 to 16,384 cached tokens, one new one: 50 to 53 us.  Bound: HBM (K's codes and the weights in
 // and out, 3.4 TB/s) and the latency of a wave's few tiles.
 template <typename E, int D, int RB>
 __global__ __launch_bounds__(256) void kla_kv4_weigh_few_kernel(KvWeighParams p) {
@@ -1029,13 +1031,21 @@ __global__ __launch_bounds__(256) void kla_kv4_weigh_few_kernel(KvWeighParams p)
 }
 
 // How a chunk call runs, by the rows of a sequence (the host's mean).  Up to 128 rows go in tiles
-// of 16 or 32: 64 sequences of 4,096 to 16,384 cached tokens, 16 heads over 4, with 24 new ones 318
-// us (256 rows to a tile: 359; fp32, 8 sequences: 83, in tiles of 128 rows 140).  More go in tiles of
-// 256, whose waves without rows only bring keys (40 new tokens 500 us, in tiles of 128 rows 735;
-// 100 new 905 against 1,287; 64 new, whose rows fill both, 872 against 771; one sequence of 60,000 and
-// 2,048 new ones 1,005 against 2,100); fp32 operands are three terms, and the registers hold 128.
-// Keys go in runs, as many as make about 512 workgroups (256: 1,143 us, 512: 1,163, 1,024: 1,194
-// where the rows alone make 256; with few rows 1,024), of 512 keys at least.
+// of 16 or 32, more in tiles of 256, whose waves without rows only bring keys; fp32 operands are
+// three terms, and the registers hold 128 rows.  64 sequences of 4,096 to 16,384 cached tokens, 16
+// heads over 4, in tiles of 32 and of 256 rows (us; of 128 rows no count is the fastest):
+//   24 new tokens each 311 and 354, 40 new 427 and 501, 64 new 621 and 845, 100 new 905 and 894,
+//   200 new 1,695 and 1,442; 8 such sequences 75 and 72, 81 and 90, 103 and 133, 153 and 132, 215
+//   and 232.
+// So from 128 rows to some 300 the smaller tiles would be the better ones yet.  fp32, 8 sequences,
+// in tiles of 16 and of 128 rows: 5 new 50 and 123, 24 new 80 and 133, 64 new 152 and 218.  One
+// sequence of 60,000 and 2,048 new ones takes 1,004, in tiles of 128 rows 1,620.  A batch whose
+// lengths differ much is planned by its mean all the same: 63 single tokens beside 1,000 and beside
+// 2,048 new ones of one sequence take 264 and 517, where the single tokens alone take 75 and the
+// others 145 and 277.
+// Keys go in runs, as many as make about 512 workgroups (that sequence of
+// 60,000, 128 tiles: 256 workgroups 946 us, 512: 958 to 1,004, 1,024: 984; those 64 sequences with
+// five new tokens, 1,024: 116, 512: 112, 256: 117; with few rows 1,024), of 512 keys at least.
 struct ChunkPlan {
   int BM, slots, splits, per;
 };
@@ -1060,8 +1070,10 @@ template <typename E, int D>
 hipError_t launch_chunk(const KvChunkParams &p, int BM, hipStream_t st) {
   const dim3 grid((unsigned)((long long)p.slots * p.kv.Hkv * p.splits));
   auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, p); };
-  // few rows: codes past the caches where those do not keep them from call to call anyway
-  // (kla_kv4.hip; 326 MB of codes and five new tokens 123 us, through the caches 125); two row blocks of fp32 queries would not fit the registers
+  // few rows: codes past the caches where those do not keep them from call to call anyway, by the
+  // single-token step's rule (kla_kv4.hip), which wins there what it does not win here (326 MB of
+  // codes and five new tokens 117 us, through the caches 116); two row blocks of fp32 queries would not
+  // fit the registers
   const bool once = (double)p.N * p.kv.Hkv * p.max_len * (D + D / 16) >= 96 << 20;
   if (BM == 16) {
     if (once) go(kla_kv4_rows_kernel<E, D, 1, true>, 256);
@@ -1085,11 +1097,17 @@ hipError_t launch_chunk(const KvChunkParams &p, int BM, hipStream_t st) {
 
 // How the weights are made: rows of a sequence (the host's mean) that a wave holds, in blocks of
 // 16, with keys streaming past in runs; 0: more, with 64 keys to a workgroup.  Up to 384 rows the
-// keys pass by for every 32 (64 sequences of 4,096 to 16,384 cached tokens, 16 heads over 4: one
-// new token 41 us against 666 with 64 keys to a workgroup, 24 new 163 against 710, 64 new 408
-// against 900; 8 such sequences, 64 new 98 against 122, 100 new 154 against 152, 200 new 286 against
-// 224).  fp32 rows are three terms, 16 of them at a time up to 128 (8 sequences, 24 new 77 against
-// 117, 64 new 193 against 174).
+// keys pass by for every 32.  64 sequences of 4,096 to 16,384 cached tokens, 16 heads over 4, with
+// rows and with 64 keys to a workgroup (us):
+//   one new token each 43 and 661, 24 new 159 and 704, 40 new 257 and 810, 64 new 400 and 885, 100
+//   new 641 and 1,118, 200 new 1,207 and 1,744; 8 such sequences 13 and 96, 41 and 101, 64 and 119,
+//   99 and 128, 151 and 162, 281 and 234; 12 sequences of up to 1,000 new ones behind 200 to 4,000
+//   246 and 42.
+// So with many sequences the rows would be the better ones at 400 and 800 too.  The mean serves
+// batches badly whose lengths differ much: 63 single tokens beside 1,000 and beside 2,048 new ones
+// of one sequence take 3,793 and 7,748 us, where the single tokens alone take 44 and the others 115
+// and 231.  fp32 rows are three terms, 16 of them at a time up to 128 (8 sequences, 5 new 29 and
+// 104, 24 new 77 and 122, 64 new 183 and 175).
 struct WeighPlan {
   int RB, blocks, per;
 };

@@ -5,16 +5,18 @@
 // move to the front in their order (include/kla.h, kla_kv4_evict).
 //
 // Three kernels.  Choice, a workgroup to a (sequence, head): a radix selection finds the smallest
-// weight that stays, eleven bits of the weights' order at a time (a histogram in LDS per pass, wide
-// enough that a wave's tokens seldom meet in a bin; integer counts, so the order of the atomics
-// changes nothing); then each wave goes over its part of the tokens and writes the positions
-// that stay, at places counted ahead.  Few (sequence, head)s: the same in parts, over four
-// launches.  Then the rows that change place go to a workspace and from there to their places: kept
-// rows move towards the front over rows that others still have to read.
+// weight that stays, eleven bits of the weights' order at a time (a histogram in LDS per pass;
+// integer counts, so the order of the atomics changes nothing; the first pass's bins are a weight's
+// sign, exponent and two more bits, so weights of like size meet in one and are added in turn);
+// then each wave goes over its part of the tokens and writes the positions that stay, at places
+// counted ahead.  Few (sequence, head)s: the same in parts, over four launches.  Then the rows that
+// change place go to a workspace and from there to their places: kept rows move towards the front
+// over rows that others still have to read.
 // Bound: the choice by its passes over the weights (from L2), the moves by HBM and the memory-side
 // cache, which holds the workspace in between: 64 sequences of 4,096 to 16,384 tokens and four heads
-// cut to 4,096 tokens, choice 30 us, rows out 34 (200 MB read) and in 25; one sequence of 131,071 and
-// two heads cut to 32,768, choice 39 in four launches, rows 5 and 5.
+// cut to 4,096 tokens, choice 30 us, rows out 34 (200 MB read) and in 25; one sequence of 131,071
+// and two heads cut to 32,768, choice 39 in four launches (the first 7, the others 10 to 12: each of
+// their workgroups adds up the histograms of all parts, 8 KB each), rows 5 and 5.
 #include <algorithm>
 
 #include "kla_common.h"
@@ -391,8 +393,8 @@ int row_bytes(int D) { return D + 32; }  // codes, 2 D / 32 scales, the weight
 
 // Parts of a choice: one workgroup for all tokens of a (sequence, head), unless those are few
 // enough that parts of 4,096 tokens do not make more than 256 (one sequence of 131,071 tokens and
-// two heads 59 us, in one piece 182; a batch of 64 sequences and four heads 193 us in one piece
-// each, in parts 259).
+// two heads 60 us, in one piece 184; a batch of 64 sequences and four heads 261 us in one piece
+// each, in parts 299; each with what is left read back).
 int evict_parts(int N, int Hkv, long long room) {
   const long long pairs = (long long)N * Hkv, parts = (room + EV_PART - 1) / EV_PART;
   return parts > 2 && pairs * parts <= 256 ? (int)parts : 1;

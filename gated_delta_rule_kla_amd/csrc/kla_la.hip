@@ -204,7 +204,8 @@ __device__ __forceinline__ void la_span(const int32_t *cu, int n, int T, int C, 
 // state, and leave a copy of it in the element type in LDS.  Beside them four waves compute the
 // outputs from those copies, 16 rows each (fp32, 32 tokens to a chunk: half of the columns);
 // the first, which has the fewest scores, also sums the decays of the chunk after next.  One
-// barrier per chunk.  B=4 H=16 T=4096 dk=dv=128: 94 us, H=16 T=65536 dv=256: 843 us (1.9 TB/s).
+// barrier per chunk.  B=4 H=16 T=4096 dk=dv=128: 90 to 107 us; H=16 T=65536 dv=256, in segments of
+// 256 chunks with the pass for their ends: 825 to 840 us (1.9 TB/s).
 // Bound: a chunk's chain, 1.5 us: LDS takes 1,370 cycles of it (the state's operands of every wave),
 // and the vector ALU, matrix products and the exchange behind the barrier hide little of each other
 // with one workgroup to a CU.
@@ -617,7 +618,7 @@ __global__ __launch_bounds__(la_threads(MODE)) void kla_la_scan_kernel(LaParams 
 // products' accumulators hold gradients transposed (channels in a lane, tokens along lanes), and
 // the scores that the second products take are accumulator tiles as they stand: (do . v)
 // transposed for dq, (do . v) and (q . k) for dk and dv.  The values' channels come in slices of
-// LA_NV.  16 packed documents (26,339 tokens, 16 heads, dk=dv=128): 328 of the backward's 610 us.
+// LA_NV.  16 packed documents (26,339 tokens, 16 heads, dk=dv=128): 316 of the backward's 620 us.
 // Bound: latency, with two workgroups to a CU (70 KB of LDS; beyond 128 registers it takes 470 us).
 struct LaGradParams {
   const void *q, *k, *v, *g, *dout, *states, *dstates;
@@ -959,7 +960,7 @@ __global__ __launch_bounds__(256) void kla_la_sum_kernel(const float *part, floa
 
 // One token.  A workgroup owns 4 CG columns of one state, CG threads to a row and 256 / CG rows
 // at a time; each thread's rows are loaded together.  256 sequences of 16 heads, dk=dv=128 (537 MB
-// in and out): 87 us on one state, 112 on several in turn (4.8 TB/s).  Bound: HBM.
+// in and out): 87 us on one state, 112 to 117 on several in turn (4.6 to 4.8 TB/s).  Bound: HBM.
 struct LaStepParams {
   const void *q, *k, *v, *g;
   const float *gfix;
@@ -1041,9 +1042,9 @@ hipError_t launch_scan_t(LaParams p, int dirs, hipStream_t st) {
   return hipGetLastError();
 }
 // Slices of 64 columns, which read x half as often, where they still make a workgroup to a CU and
-// where their rows, states and scaled values fit LDS (T=65536 dv=256 of 16 heads: 832 us, with 32
-// columns 1,025).  Not where states are stored, for which the registers do not suffice (16 packed
-// documents backward 685 us, with 32 columns 610).
+// where their rows, states and scaled values fit LDS (T=65536 dv=256 of 16 heads: 840 us, with 32
+// columns 1,026).  Not where states are stored, for which the registers do not suffice (when that was
+// tried, 16 packed documents backward took 685 us, with 32 columns 610).
 template <typename E, int MODE>
 hipError_t launch_scan(const LaParams &p, int dirs, hipStream_t st) {
   if constexpr (sizeof(E) == 2 && MODE != LA_STORE) {
@@ -1065,8 +1066,9 @@ int la_slots(const LaArgs &a) {
 }
 
 // Segments of the scans, where their workgroups leave CUs idle: as many as make two rounds of
-// workgroups, each of 8 chunks at least (T=65536 dv=256 of 16 heads, 128 workgroups unsplit: 939
-// us, in one segment 1,188, for 256 workgroups 1,089, for 1,024 1,042).
+// workgroups, each of 8 chunks at least (T=65536 dv=256 of 16 heads, 128 workgroups unsplit: 840
+// us, in one segment 1,182, for 256 workgroups 1,001, for 1,024 918).  All sequences count as work:
+// one of 65,536 tokens packed beside fifteen of 256 is not cut and takes 1,803, alone 877.
 void la_segments(const LaArgs &a, int *segs, int *chunks) {
   const int C = la_chunk(a.dtype), nch = (a.longest + C - 1) / C;
   const long long wgs = (long long)a.num_seqs * a.H * ((a.dv + LA_NV - 1) / LA_NV);
@@ -1216,8 +1218,8 @@ hipError_t launch_step_t(LaStepParams p, long long nh, hipStream_t st) {
 }
 template <typename E>
 hipError_t launch_step(const LaStepParams &p, long long nh, hipStream_t st) {
-  // few states: narrow pieces, for more workgroups (16 states 10.3 against 10.6 us, where the host
-  // bounds the call; 4,096 states 136 against 87)
+  // few states: narrow pieces, for more workgroups (16 states 9.4 us either way, since the host
+  // bounds the call; 4,096 states 140 against 117)
   if (nh * ((p.dv + 127) / 128) < 512) return launch_step_t<E, 4>(p, nh, st);
   return launch_step_t<E, 32>(p, nh, st);
 }

@@ -1268,7 +1268,8 @@ def attn_kv4_weigh(
 
 
 def kv4_evict_workspace_bytes(N: int, Hkv: int, D: int, budget: int, page_size: int, max_pages: int) -> int:
-    """Workspace bytes kv4_evict needs (kla_kv4_evict_workspace_bytes)."""
+    """Workspace bytes kv4_evict needs (kla_kv4_evict_workspace_bytes); 0 where the budget covers all
+    that the block table has room for."""
     return lib().kla_kv4_evict_workspace_bytes(N, Hkv, D, min(int(budget), _INT32), page_size, max_pages)
 
 

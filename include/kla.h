@@ -556,9 +556,9 @@ kla_status_t kla_glr_decode_step(const void *x, const void *g, float *state, voi
  * bf16 once (half a step of 2^-8, as o itself is), the state is summed in fp32 from products of
  * 24 bits (three bf16 terms); F32 is fp32 throughout.  Where g > 0 makes a product of decays
  * overflow fp32, outputs are not finite even if the recurrence would be; a value that is not finite
- * reaches all outputs of its chunk, of its own and of later chunks, and no other sequence.  Sizes whose launch would
- * have more than 2^32 threads are refused (KLA_ERR_SHAPE).  Results repeat bit for bit.  Status
- * codes as kla_chunk_fwd.
+ * can reach all outputs of its chunk, earlier tokens' among them, and of later chunks, and no other
+ * sequence.  Sizes whose launch would have more than 2^32 threads are refused (KLA_ERR_SHAPE).
+ * Results repeat bit for bit.  Status codes as kla_chunk_fwd.
  */
 kla_status_t kla_la_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const float *decay,
                               const float *initial_state, void *o, float *final_state,
